@@ -18,7 +18,11 @@
  * (MXFP4 indexer-K entries), csa2_indexer_score_topk (indexer + top-K, Full
  * or Reindex), csa2_hier_pool_select (+ _static: the HSI pool),
  * csa2_sparse_attn (the readout), csa2_sparse_decode (one layer in a mode),
- * csa2_prefill_chunk (a chunk at m = 2); helpers csa2_workspace_bytes,
+ * csa2_prefill_chunk (a chunk at m = 2), csa2_swa_quant_write (new FP8
+ * sliding-window rows), csa2_kv_read, csa2_swa_read and csa2_indexer_k_read
+ * (cache rows read back), csa2_cross_attn (query tokens over every entry of
+ * another sequence), csa2_prefix_attn (the readout of a batch that shares a
+ * long prefix); helpers csa2_workspace_bytes,
  * csa2_get_device_status, csa2_status_string, csa2_default_params,
  * csa2_entry_bytes, csa2_indexer_entry_bytes, csa2_last_launch_count,
  * csa2_set_profile_events, csa2_set_topk_kernel.
@@ -329,13 +333,101 @@ csa2_status csa2_hier_pool_select_static(const float *block_scores, const int32_
                                          int32_t batch, int64_t n_max, const csa2_params *params,
                                          int32_t *pool_blocks, csa2_stream_t stream);
 
+/*
+ * csa2_swa_quant_write -- write sliding-window rows as FP8 ([A] 2.4.4: the
+ * local cache stays FP8; [N] section 4), in the form csa2_sparse_attn reads.
+ *   For row i: x = latent[i], with RoPE on channels 448..511 at position
+ *   pos[i] as csa2_kv_quant_write rotates an entry (interleaved pairs, the
+ *   same frequencies; cos and sin to 2 ulp of fp32), or as given when pos is
+ *   NULL; scale = fl32(max |x| / 448); codes = E4M3_rne_satfinite(x / scale),
+ *   all zero when the scale is zero.  A row that holds a NaN or an infinity
+ *   has NaN codes in their places.
+ *   latent    bf16 [n][512], 16-byte aligned
+ *   pos       int64 [n], 0 <= pos < 2^22, or NULL (no RoPE)
+ *   slot      int64 [n] destination rows, distinct, 0 <= slot < rows (a slot
+ *             or position out of range is skipped and sets CSA2_DEV_ERR_INDEX;
+ *             rows named twice hold a mixture of their writers)
+ *   swa       uint8 E4M3 [rows][512], 16-byte aligned; swa_scale fp32 [rows]
+ * Rows not named are left as they were.  n == 0 is a no-op.
+ */
+csa2_status csa2_swa_quant_write(const void *latent, int64_t n, const int64_t *pos, const int64_t *slot, uint8_t *swa,
+                                 float *swa_scale, int64_t rows, float rope_theta, csa2_stream_t stream);
+
+/*
+ * csa2_kv_read, csa2_swa_read, csa2_indexer_k_read -- read cache rows back as
+ * bf16: code x scale, rounded once (main-KV entries and MXFP4 keys are exact
+ * in bf16).  out[b][j] is row idx[b][j] of sequence b's cache, a row of zeros
+ * for idx[b][j] < 0 (the padding of csa2_indexer_score_topk's lists); with idx
+ * NULL it is row j (k <= cap).  The same row may be named any number of times.
+ * An idx >= cap gives zeros and sets CSA2_DEV_ERR_INDEX.
+ *   kv        uint8 [batch][cap][288], 16-byte aligned
+ *   swa       uint8 E4M3 [batch][rows][512], 16-byte aligned; swa_scale fp32 [batch][rows]
+ *   k_fp4     the MXFP4 planes of batch * cap rows (a multiple of 4), as
+ *             csa2_indexer_k_quant writes them, 16-byte aligned
+ *   idx       int32 [batch][k] or NULL
+ *   out       bf16 [batch][k][512] (csa2_indexer_k_read: [batch][k][128]), 16-byte aligned
+ * batch == 0 or k == 0 is a no-op.
+ */
+csa2_status csa2_kv_read(const uint8_t *kv, int32_t batch, int64_t cap, const int32_t *idx, int64_t k, void *out,
+                         csa2_stream_t stream);
+csa2_status csa2_swa_read(const uint8_t *swa, const float *swa_scale, int32_t batch, int64_t rows, const int32_t *idx,
+                          int64_t k, void *out, csa2_stream_t stream);
+csa2_status csa2_indexer_k_read(const uint8_t *k_fp4, int32_t batch, int64_t cap, const int32_t *idx, int64_t k,
+                                void *out, csa2_stream_t stream);
+
+/*
+ * csa2_cross_attn -- cross attention: n_q query tokens of each sequence over
+ * every visible entry of that sequence's cache, of another length (an
+ * encoder's entries; [A] 2.3.1 and [N] section 1: the decoder reads global
+ * KV made from the encoder's final states).  For each token and head one
+ * softmax over entries n < n_vis[b], logits q . k / sqrt(512), key = value =
+ * the dequantised latent, as in csa2_sparse_attn; every token of a sequence
+ * sees the same entries (n_q = 1 is a decode step).  A sequence with no
+ * visible entry gives out = 0 and lse = -inf.  Rows past n_vis[b] are not
+ * read, whatever they hold.
+ *   q         bf16 [batch][n_q][64][512], 16-byte aligned (|q| below 65504)
+ *   kv        uint8 [batch][cap][288], 16-byte aligned (NULL when n_max is 0)
+ *   n_vis     int32 [batch], 0 <= n_vis[b] <= n_max <= cap (checked on device)
+ *   n_max     host-side bound on n_vis, sizes the launch
+ *   out       bf16 [batch][n_q][64][512] (out), 16-byte aligned;
+ *             lse fp32 [batch][n_q][64] or NULL (out)
+ *   ws        at least csa2_workspace_bytes(CSA2_OP_CROSS, ...) bytes,
+ *             256-byte aligned, any contents; calls that may overlap on the
+ *             GPU need their own
+ * batch == 0 or n_q == 0 is a no-op.
+ */
+csa2_status csa2_cross_attn(int32_t batch, int32_t n_q, const void *q, const uint8_t *kv, int64_t cap,
+                            const int32_t *n_vis, int64_t n_max, void *out, float *lse, void *ws, size_t ws_bytes,
+                            csa2_stream_t stream);
+
+/*
+ * csa2_prefix_attn -- csa2_sparse_attn for a batch whose sequences share one
+ * long prefix: for each sequence b and head h one softmax over every entry of
+ * the prefix, {kv[b][topk_idx[b][j]] : topk_idx >= 0} and the SWA rows
+ * {swa[b][t] : t < swa_len[b]}.  The prefix's entries are read for two
+ * sequences at a time and never copied per sequence.
+ *   prefix_kv uint8 [n_prefix][288], 16-byte aligned (NULL when n_prefix is 0)
+ *   n_prefix  entries of the prefix, all visible to every sequence
+ *   out       bf16 [batch][64][512] (out), 16-byte aligned; lse fp32 [batch][64] or NULL
+ *   ws        at least csa2_workspace_bytes(CSA2_OP_PREFIX, batch, n_prefix,
+ *             params) bytes, 256-byte aligned, any contents; calls that may
+ *             overlap on the GPU need their own
+ * The other arguments, and what holds for them, as csa2_sparse_attn.
+ */
+csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch, const void *q, const uint8_t *prefix_kv,
+                             int64_t n_prefix, const uint8_t *kv, int64_t cap, const int32_t *topk_idx,
+                             const uint8_t *swa, const float *swa_scale, const int32_t *swa_len, void *out, float *lse,
+                             void *ws, size_t ws_bytes, csa2_stream_t stream);
+
 /* Operation selector for csa2_workspace_bytes. */
 typedef enum {
   CSA2_OP_INDEXER = 0,   /* csa2_indexer_score_topk        */
   CSA2_OP_POOL = 1,      /* csa2_hier_pool_select          */
   CSA2_OP_ATTN = 2,      /* csa2_sparse_attn               */
   CSA2_OP_DECODE = 3,    /* csa2_sparse_decode (any mode)  */
-  CSA2_OP_PREFILL = 4    /* csa2_prefill_chunk (n_max = cap) */
+  CSA2_OP_PREFILL = 4,   /* csa2_prefill_chunk (n_max = cap) */
+  CSA2_OP_PREFIX = 5,    /* csa2_prefix_attn (n_max = n_prefix) */
+  CSA2_OP_CROSS = 6      /* csa2_cross_attn (batch = query tokens) */
 } csa2_op;
 
 /* Scratch bytes an operation needs for `batch` sequences and visible

@@ -82,8 +82,15 @@ def lib():
         L.csa2_prefill_chunk.restype = ctypes.c_int
         L.csa2_set_profile_events.argtypes, L.csa2_set_profile_events.restype = [ctypes.c_int, P, P], ctypes.c_int
         L.csa2_set_topk_kernel.argtypes, L.csa2_set_topk_kernel.restype = [ctypes.c_int32], ctypes.c_int
+        L.csa2_swa_quant_write.argtypes = [P, i64, P, P, P, P, i64, f32, P]
+        L.csa2_kv_read.argtypes = [P, i32, i64, P, i64, P, P]
+        L.csa2_swa_read.argtypes = [P, P, i32, i64, P, i64, P, P]
+        L.csa2_indexer_k_read.argtypes = [P, i32, i64, P, i64, P, P]
+        L.csa2_cross_attn.argtypes = [i32, i32, P, P, i64, P, i64, P, P, P, sz, P]
+        L.csa2_prefix_attn.argtypes = [PP, i32, P, P, i64, P, i64, P, P, P, P, P, P, P, sz, P]
         for f in ("csa2_kv_quant_write", "csa2_kv_quant_write_ik", "csa2_indexer_k_quant", "csa2_indexer_score_topk", "csa2_hier_pool_select",
-                  "csa2_sparse_attn", "csa2_sparse_decode"):
+                  "csa2_sparse_attn", "csa2_sparse_decode", "csa2_swa_quant_write", "csa2_kv_read", "csa2_swa_read",
+                  "csa2_indexer_k_read", "csa2_cross_attn", "csa2_prefix_attn"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -309,3 +316,101 @@ def prefill_chunk(params, q, q_idx, w, kv, k_idx, first_pos, m, swa, swa_scale, 
         _ptr(swa_scale, torch.float32, "swa_scale"), swa.shape[1], int(swa_first_pos),
         _ptr(topk_idx, torch.int32, "topk_idx"), _ptr(out, torch.float32, "out"), _ptr(lse, torch.float32, "lse"),
         _ptr(ws, None, "ws"), ws.numel() * ws.element_size(), _stream(stream)), "csa2_prefill_chunk")
+
+
+OP_PREFIX, OP_CROSS = 5, 6
+
+
+def _dev(t, dtype, shape, name, none_ok=False):
+    """Device pointer of a contiguous tensor of this dtype and shape on the
+    current device (a shape entry of None takes any size)."""
+    if t is None and none_ok:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise Csa2Error(f"{name} must be a CUDA tensor on the current device")
+    if t.dtype != dtype or not t.is_contiguous():
+        raise Csa2Error(f"{name} must be contiguous {dtype}, got {t.dtype} of strides {t.stride()}")
+    if shape is not None and (t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape))):
+        raise Csa2Error(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _ws(ws):
+    return _dev(ws, torch.uint8, None, "ws"), ws.numel()
+
+
+def swa_quant_write(latent, slot, swa, swa_scale, pos=None, rope_theta=10000.0, stream=None):
+    """Write sliding-window rows as FP8: latent bf16 [n, 512]; slot int64 [n]
+    (distinct); pos int64 [n] or None (no RoPE); swa uint8 [rows, 512] and
+    swa_scale fp32 [rows] (or with leading dimensions, rows flattened)."""
+    n, rows = slot.numel(), swa_scale.numel()
+    if swa.numel() != rows * D:
+        raise Csa2Error(f"swa: {rows} scales go with {rows} rows of {D}, got {swa.numel()} bytes")
+    _check(lib().csa2_swa_quant_write(
+        _dev(latent, torch.bfloat16, (n, D), "latent"), n, _dev(pos, torch.int64, (n,), "pos", True),
+        _dev(slot, torch.int64, (n,), "slot"), _dev(swa, torch.uint8, None, "swa"),
+        _dev(swa_scale, torch.float32, None, "swa_scale"), rows, float(rope_theta), _stream(stream)),
+        "csa2_swa_quant_write")
+
+
+def kv_read(kv, out, idx=None, stream=None):
+    """Read main-KV entries back: kv uint8 [B, cap, 288]; idx int32 [B, k] (a
+    negative index gives zeros) or None (rows 0 .. k - 1); out bf16 [B, k, 512]."""
+    B, k = out.shape[0], out.shape[1]
+    _check(lib().csa2_kv_read(_dev(kv, torch.uint8, (B, None, ENTRY_BYTES), "kv"), B, kv.shape[1],
+                              _dev(idx, torch.int32, (B, k), "idx", True), k,
+                              _dev(out, torch.bfloat16, (B, k, D), "out"), _stream(stream)), "csa2_kv_read")
+
+
+def swa_read(swa, swa_scale, out, idx=None, stream=None):
+    """Read sliding-window rows back: swa uint8 [B, rows, 512], swa_scale fp32
+    [B, rows]; idx and out as ``kv_read``."""
+    B, k = out.shape[0], out.shape[1]
+    _check(lib().csa2_swa_read(_dev(swa, torch.uint8, (B, None, D), "swa"),
+                               _dev(swa_scale, torch.float32, (B, swa.shape[1]), "swa_scale"), B, swa.shape[1],
+                               _dev(idx, torch.int32, (B, k), "idx", True), k,
+                               _dev(out, torch.bfloat16, (B, k, D), "out"), _stream(stream)), "csa2_swa_read")
+
+
+def indexer_k_read(k_fp4, out, idx=None, stream=None):
+    """Read MXFP4 indexer keys back: k_fp4 a cache of ``indexer_k_fp4_cache``
+    whose rows are B sequences of equal capacity; idx as ``kv_read``; out bf16
+    [B, k, 128]."""
+    B, k = out.shape[0], out.shape[1]
+    rows = k_fp4.numel() // FP4_ENTRY_BYTES
+    if k_fp4.numel() % FP4_ENTRY_BYTES or (B and rows % B):
+        raise Csa2Error(f"k_fp4: {k_fp4.numel()} bytes are no {B} sequences of MXFP4 rows")
+    _check(lib().csa2_indexer_k_read(_dev(k_fp4, torch.uint8, None, "k_fp4"), B, rows // B if B else 0,
+                                     _dev(idx, torch.int32, (B, k), "idx", True), k,
+                                     _dev(out, torch.bfloat16, (B, k, DI), "out"), _stream(stream)),
+           "csa2_indexer_k_read")
+
+
+def cross_attn(q, kv, n_vis, n_max, out, ws, lse=None, stream=None):
+    """Query tokens over every visible entry of their sequence: q bf16
+    [B, T, 64, 512]; kv uint8 [B, cap, 288]; n_vis int32 [B], at most n_max;
+    out bf16 [B, T, 64, 512]; lse fp32 [B, T, 64] or None; ws from
+    ``workspace(OP_CROSS, B * T, n_max, params)``."""
+    B, T = q.shape[0], q.shape[1]
+    wp, wn = _ws(ws)
+    _check(lib().csa2_cross_attn(
+        B, T, _dev(q, torch.bfloat16, (B, T, H, D), "q"), _dev(kv, torch.uint8, (B, None, ENTRY_BYTES), "kv"),
+        kv.shape[1], _dev(n_vis, torch.int32, (B,), "n_vis"), int(n_max), _dev(out, torch.bfloat16, (B, T, H, D), "out"),
+        _dev(lse, torch.float32, (B, T, H), "lse", True), wp, wn, _stream(stream)), "csa2_cross_attn")
+
+
+def prefix_attn(params, q, prefix_kv, kv, topk_idx, swa, swa_scale, swa_len, out, ws, lse=None, stream=None):
+    """``sparse_attn`` for a batch whose sequences share a prefix: prefix_kv
+    uint8 [n_prefix, 288], all of it visible to every sequence; out bf16
+    [B, 64, 512]; ws from ``workspace(OP_PREFIX, B, n_prefix, params)``; the
+    other arguments as ``sparse_attn``."""
+    B, K, W = q.shape[0], params.index_topk, params.sliding_window
+    wp, wn = _ws(ws)
+    _check(lib().csa2_prefix_attn(
+        ctypes.byref(params), B, _dev(q, torch.bfloat16, (B, H, D), "q"),
+        _dev(prefix_kv, torch.uint8, (None, ENTRY_BYTES), "prefix_kv"), prefix_kv.shape[0],
+        _dev(kv, torch.uint8, (B, None, ENTRY_BYTES), "kv"), kv.shape[1],
+        _dev(topk_idx, torch.int32, (B, K), "topk_idx"), _dev(swa, torch.uint8, (B, W, D), "swa", W == 0),
+        _dev(swa_scale, torch.float32, (B, W), "swa_scale", W == 0), _dev(swa_len, torch.int32, (B,), "swa_len", W == 0),
+        _dev(out, torch.bfloat16, (B, H, D), "out"), _dev(lse, torch.float32, (B, H), "lse", True), wp, wn,
+        _stream(stream)), "csa2_prefix_attn")

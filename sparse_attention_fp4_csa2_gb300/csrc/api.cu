@@ -2,6 +2,7 @@
 // maps and the launch sequence of each call (declared in include/csa2.h).
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstring>
 #include <mutex>
 
@@ -167,6 +168,22 @@ size_t decode_ws(int32_t batch, int64_t n_max, const csa2_params *p) {
   return bs + h + m;
 }
 
+// Prefix readout: the own part's fp32 rows and log-sum-exps, the dense
+// readout's partials, the sparse readout's scratch.
+struct PrefixLayout {
+  size_t out_off, lse_off, part_off, attn_off, end;
+};
+
+PrefixLayout prefix_layout(int32_t batch, const csa2_params *p) {
+  PrefixLayout L;
+  L.out_off = 0;
+  L.lse_off = (size_t)batch * H * D * 4;
+  L.part_off = L.lse_off + (size_t)round_up((int64_t)batch * H * 4, 256);
+  L.attn_off = L.part_off + (size_t)round_up((int64_t)dense_scratch_bytes(), 256);
+  L.end = L.attn_off + attn_ws(batch, p);
+  return L;
+}
+
 constexpr int64_t kPrefillBlock = 1024;   // query tokens per indexer / top-K / attention block
 
 size_t prefill_ws(int32_t batch, int64_t cap, const csa2_params *p) {
@@ -176,6 +193,9 @@ size_t prefill_ws(int32_t batch, int64_t cap, const csa2_params *p) {
   (void)batch;
   return b;
 }
+
+constexpr int64_t kMaxCacheRows = (int64_t)1 << 33;     // rows of one call's caches, writes and reads
+constexpr int64_t kMaxDenseTokens = (int64_t)1 << 24;   // query tokens of a dense readout
 
 csa2_status cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
 
@@ -370,6 +390,8 @@ size_t csa2_workspace_bytes(csa2_op op, int32_t batch, int64_t n_max, const csa2
     case CSA2_OP_ATTN: return attn_ws(batch, params);
     case CSA2_OP_DECODE: return decode_ws(batch, n_max, params);
     case CSA2_OP_PREFILL: return prefill_ws(batch, n_max, params);
+    case CSA2_OP_PREFIX: return prefix_layout(batch, params).end;
+    case CSA2_OP_CROSS: return dense_scratch_bytes();
   }
   return 0;
 }
@@ -619,6 +641,125 @@ extern "C" csa2_status csa2_prefill_chunk(const csa2_params *params, int32_t bat
     a.swa_seq_rows = swa_rows;
     if (launch_sparse_attn(a, attn_ws, st, &launches) != cudaSuccess) return CSA2_ERR_CUDA;
   }
+  g_last_launches = launches;
+  return CSA2_OK;
+}
+
+extern "C" csa2_status csa2_swa_quant_write(const void *latent, int64_t n, const int64_t *pos, const int64_t *slot,
+                                            uint8_t *swa, float *swa_scale, int64_t rows, float rope_theta,
+                                            csa2_stream_t stream) {
+  g_last_launches = 0;
+  if (n < 0 || rows < 0) return CSA2_ERR_INVALID_ARG;
+  if (n == 0) return CSA2_OK;
+  if (!latent || !slot || !swa || !swa_scale || !aligned16(latent) || !aligned16(swa)) return CSA2_ERR_INVALID_ARG;
+  if (pos && !(rope_theta > 1.0f && rope_theta < INFINITY)) return CSA2_ERR_INVALID_ARG;
+  if (n > kMaxCacheRows) return CSA2_ERR_UNSUPPORTED;
+  if (launch_swa_quant_write(latent, n, pos, slot, swa, swa_scale, rows, rope_theta,
+                             reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  g_last_launches = 1;
+  return CSA2_OK;
+}
+
+namespace {
+
+// The read-backs' common checks; `skip` is set when there is nothing to read.
+csa2_status check_read(int32_t batch, int64_t cap, const int32_t *idx, int64_t k, const void *out, bool *skip) {
+  *skip = false;
+  if (batch < 0 || cap < 0 || k < 0) return CSA2_ERR_INVALID_ARG;
+  if (!idx && k > cap) return CSA2_ERR_INVALID_ARG;
+  if (batch == 0 || k == 0) {
+    *skip = true;
+    return CSA2_OK;
+  }
+  if (!out || !aligned16(out)) return CSA2_ERR_INVALID_ARG;
+  if (cap > kMaxCacheRows / batch || k > kMaxCacheRows / batch) return CSA2_ERR_UNSUPPORTED;
+  return CSA2_OK;
+}
+
+csa2_status read_status(cudaError_t e) {
+  if (e != cudaSuccess) return CSA2_ERR_CUDA;
+  g_last_launches = 1;
+  return CSA2_OK;
+}
+
+}  // namespace
+
+extern "C" csa2_status csa2_kv_read(const uint8_t *kv, int32_t batch, int64_t cap, const int32_t *idx, int64_t k,
+                                    void *out, csa2_stream_t stream) {
+  g_last_launches = 0;
+  bool skip;
+  const csa2_status s = check_read(batch, cap, idx, k, out, &skip);
+  if (s != CSA2_OK || skip) return s;
+  if (!kv || !aligned16(kv)) return CSA2_ERR_INVALID_ARG;
+  return read_status(launch_kv_read(kv, batch, cap, idx, k, out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" csa2_status csa2_swa_read(const uint8_t *swa, const float *swa_scale, int32_t batch, int64_t rows,
+                                     const int32_t *idx, int64_t k, void *out, csa2_stream_t stream) {
+  g_last_launches = 0;
+  bool skip;
+  const csa2_status s = check_read(batch, rows, idx, k, out, &skip);
+  if (s != CSA2_OK || skip) return s;
+  if (!swa || !swa_scale || !aligned16(swa)) return CSA2_ERR_INVALID_ARG;
+  return read_status(
+      launch_swa_read(swa, swa_scale, batch, rows, idx, k, out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" csa2_status csa2_indexer_k_read(const uint8_t *k_fp4, int32_t batch, int64_t cap, const int32_t *idx,
+                                           int64_t k, void *out, csa2_stream_t stream) {
+  g_last_launches = 0;
+  bool skip;
+  const csa2_status s = check_read(batch, cap, idx, k, out, &skip);
+  if (s != CSA2_OK || skip) return s;
+  if (!k_fp4 || !aligned16(k_fp4) || ((int64_t)batch * cap) % 4 != 0) return CSA2_ERR_INVALID_ARG;
+  return read_status(launch_indexer_k_read(k_fp4, batch, cap, idx, k, out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" csa2_status csa2_cross_attn(int32_t batch, int32_t n_q, const void *q, const uint8_t *kv, int64_t cap,
+                                       const int32_t *n_vis, int64_t n_max, void *out, float *lse, void *ws,
+                                       size_t ws_bytes, csa2_stream_t stream) {
+  g_last_launches = 0;
+  if (batch < 0 || n_q < 0 || cap < 0 || n_max < 0 || n_max > cap) return CSA2_ERR_INVALID_ARG;
+  if (batch == 0 || n_q == 0) return CSA2_OK;
+  if (!q || !n_vis || !out || !ws || (n_max > 0 && !kv)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return CSA2_ERR_INVALID_ARG;
+  if ((int64_t)batch * n_q > kMaxDenseTokens || cap > kMaxCacheRows / batch) return CSA2_ERR_UNSUPPORTED;
+  if (ws_bytes < dense_scratch_bytes()) return CSA2_ERR_WORKSPACE;
+  int launches = 0;
+  if (launch_dense_attn(q, kv, n_vis, n_max, cap, batch, n_q, out, lse, nullptr, nullptr, ws, num_sms(),
+                        reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  g_last_launches = launches;
+  return CSA2_OK;
+}
+
+extern "C" csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch, const void *q,
+                                        const uint8_t *prefix_kv, int64_t n_prefix, const uint8_t *kv, int64_t cap,
+                                        const int32_t *topk_idx, const uint8_t *swa, const float *swa_scale,
+                                        const int32_t *swa_len, void *out, float *lse, void *ws, size_t ws_bytes,
+                                        csa2_stream_t stream) {
+  g_last_launches = 0;
+  if (!params_ok(params)) return CSA2_ERR_UNSUPPORTED;
+  if (batch < 1 || n_prefix < 0) return CSA2_ERR_INVALID_ARG;
+  if (!q || !out || !ws || (n_prefix > 0 && !prefix_kv)) return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(prefix_kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(ws) & 255u))
+    return CSA2_ERR_INVALID_ARG;
+  if (n_prefix > kMaxCacheRows) return CSA2_ERR_UNSUPPORTED;
+  const PrefixLayout L = prefix_layout(batch, params);
+  if (ws_bytes < L.end) return CSA2_ERR_WORKSPACE;
+  uint8_t *wsb = static_cast<uint8_t *>(ws);
+  float *own_out = reinterpret_cast<float *>(wsb + L.out_off);
+  float *own_lse = reinterpret_cast<float *>(wsb + L.lse_off);
+  const cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  int launches = 0;
+  const csa2_status s = run_attn(params, batch, q, kv, cap, topk_idx, swa, swa_scale, swa_len, own_out, own_lse,
+                                 wsb + L.attn_off, ws_bytes - L.attn_off, st, &launches);
+  if (s != CSA2_OK) return s;
+  if (launch_dense_attn(q, prefix_kv, nullptr, n_prefix, n_prefix, 1, batch, out, lse, own_out, own_lse,
+                        wsb + L.part_off, num_sms(), st, &launches) != cudaSuccess)
+    return CSA2_ERR_CUDA;
   g_last_launches = launches;
   return CSA2_OK;
 }

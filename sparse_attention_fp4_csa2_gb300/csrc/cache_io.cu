@@ -1,0 +1,275 @@
+// csa2_swa_quant_write and the cache read-backs (csa2_kv_read, csa2_swa_read,
+// csa2_indexer_k_read).
+//
+// Both directions are streams with a few operations per byte, so they are
+// bound by HBM for many rows and by launch latency for a decode step's few.
+// One warp handles a row (half a warp an indexer key) and every load and
+// store of a warp covers contiguous 16-, 8- or 4-byte pieces.
+#include <cmath>
+
+#include "kernels.cuh"
+
+namespace csa2 {
+
+namespace {
+
+// RoPE frequencies as fractions of a turn per position, in units of 2^-64
+// turns: floor(2^64 * inv_j / (2 pi)), inv_j = fl32(theta^(-2j/64)).
+struct RopeTurns {
+  uint64_t step[ROPE_DIM / 2];
+};
+
+// Positions of kv_quant_write: [0, 2^22).
+constexpr int64_t kMaxRopePos = int64_t(1) << 22;
+
+// cos and sin of position p's rotation for one frequency.  p * step wraps
+// modulo whole turns by itself, and its error is below 2^22 * 2^-64 turns, so
+// no double-precision reduction is needed (GB300 has few FP64 units: 32,768
+// rows of double sincos alone would take over 100 us against 7.5 us of
+// memory traffic).  The nearest quarter turn is taken out exactly; what is
+// left, at most an eighth of a turn, is rounded once to fp32 and goes
+// through sincospif, within 2 ulp of fp32 in all.
+__device__ __forceinline__ void rope_cos_sin(uint64_t step, int64_t p, float &c, float &s) {
+  const uint64_t phase = step * (uint64_t)p;
+  const uint64_t quarter = (phase + (1ull << 61)) >> 62;
+  const float half_turns = __ll2float_rn((int64_t)(phase - (quarter << 62))) * 0x1p-63f;
+  float sr, cr;
+  sincospif(half_turns, &sr, &cr);
+  const bool odd = quarter & 1;
+  const float a = odd ? sr : cr, b = odd ? cr : sr;
+  c = ((quarter + 1) & 2) ? -a : a;
+  s = (quarter & 2) ? -b : b;
+}
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Lane l owns channels 16 l .. + 15: it loads 32 bytes, rotates them if they
+// are RoPE channels (lane j evaluates frequency j; products and sums rounded
+// separately), and stores 16 bytes of codes.  One warp per block for a decode
+// step's few rows, so that they spread over the SMs.
+__global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat16 *__restrict__ latent, int64_t n,
+                                                              const int64_t *__restrict__ pos,
+                                                              const int64_t *__restrict__ slot,
+                                                              uint8_t *__restrict__ swa, float *__restrict__ swa_scale,
+                                                              int64_t rows, const RopeTurns turns) {
+  pdl_wait();   // the inputs' producer is complete past here (programmatic launch)
+  const int lane = threadIdx.x & 31;
+  const int64_t e = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (e >= n) return;
+  const int64_t row = slot[e];
+  const int64_t p = pos ? pos[e] : 0;
+  if (row < 0 || row >= rows || p < 0 || p >= kMaxRopePos) {
+    if (lane == 0) set_error(CSA2_DEV_ERR_INDEX);
+    return;
+  }
+  const uint4 *src = reinterpret_cast<const uint4 *>(latent + e * D + lane * 16);
+  const uint4 u0 = __ldg(src), u1 = __ldg(src + 1);
+  const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  if (pos) {
+    float cj, sj;
+    rope_cos_sin(turns.step[lane], p, cj, sj);
+    const int jbase = (lane - (D - ROPE_DIM) / 16) * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int from = (jbase + i) & 31;
+      const float c = __shfl_sync(0xffffffffu, cj, from);
+      const float s = __shfl_sync(0xffffffffu, sj, from);
+      if (lane >= (D - ROPE_DIM) / 16) {
+        const float a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+        x[2 * i + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+      }
+    }
+  }
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float scale = __fdiv_rn(amax, 448.0f);
+  uint32_t q[4] = {0, 0, 0, 0};
+  if (scale > 0.0f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i >> 1] |= cvt_e4m3x2(__fdiv_rn(x[2 * i + 1], scale), __fdiv_rn(x[2 * i], scale)) << (16 * (i & 1));
+  }
+  *reinterpret_cast<uint4 *>(swa + row * D + lane * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+  if (lane == 0) swa_scale[row] = scale;
+}
+
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// half2 (a pair of decoded codes) times an fp32 scale, rounded once to bf16.
+__device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float scale) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
+  return bf16x2(f.x * scale, f.y * scale);
+}
+
+// UE8M0 byte -> 2^(b - 127) (255 is NaN).
+__device__ __forceinline__ float ue8m0_to_f32(uint32_t b) {
+  return b == 0 ? __uint_as_float(0x00400000u) : b == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(b << 23);
+}
+
+enum { kFmtKv = 0, kFmtSwa = 1, kFmtIk = 2 };
+
+struct ReadArgs {
+  const uint8_t *codes;    // kv entries, SWA rows or MXFP4 code plane
+  const void *scales;      // SWA: fp32 [rows]; MXFP4: bytes [rows][4]
+  const int32_t *idx;      // [batch][k] or NULL
+  __nv_bfloat16 *out;      // [batch][k][512 or 128]
+  int64_t cap, total;      // rows per sequence, batch * k
+  int64_t k;
+};
+
+// One output piece of 8 channels: its codes and its scale.
+struct Piece {
+  uint2 c;
+  float scale;
+};
+
+template <int FMT>
+__device__ __forceinline__ Piece load_piece(const ReadArgs &a, int64_t row, int piece) {
+  Piece r;
+  if (FMT == kFmtKv) {
+    const uint8_t *src = a.codes + row * ENTRY_BYTES;
+    r.c = make_uint2(ld_nc_u32(src + 4 * piece), 0u);
+    r.scale = e4m3_to_f32(__ldg(src + 256 + (piece >> 1)));
+  } else if (FMT == kFmtSwa) {
+    r.c = __ldg(reinterpret_cast<const uint2 *>(a.codes + row * D + 8 * piece));
+    r.scale = __ldg(static_cast<const float *>(a.scales) + row);
+  } else {
+    r.c = make_uint2(ld_nc_u32(a.codes + row * (DI / 2) + 4 * piece), 0u);
+    r.scale = ue8m0_to_f32(__ldg(static_cast<const uint8_t *>(a.scales) + row * 4 + (piece >> 2)));
+  }
+  return r;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint4 decode_piece(const Piece &p) {
+  uint32_t h[4];
+  if (FMT == kFmtSwa) {
+    h[0] = e4m3x2_to_half2((uint16_t)(p.c.x & 0xFFFF));
+    h[1] = e4m3x2_to_half2((uint16_t)(p.c.x >> 16));
+    h[2] = e4m3x2_to_half2((uint16_t)(p.c.y & 0xFFFF));
+    h[3] = e4m3x2_to_half2((uint16_t)(p.c.y >> 16));
+  } else {
+    e2m1x8_to_half2x4(p.c.x, h);
+  }
+  return make_uint4(scaled_bf16x2(h[0], p.scale), scaled_bf16x2(h[1], p.scale), scaled_bf16x2(h[2], p.scale),
+                    scaled_bf16x2(h[3], p.scale));
+}
+
+// Output rows in pieces of 8 channels (16 bytes), 64 per entry and window
+// row (lane l stores pieces l and 32 + l) and 16 per indexer key (half a warp
+// each, so a warp step covers two keys).  A warp takes R consecutive steps
+// and issues all their loads before the first store.
+template <int FMT, int R>
+__global__ void __launch_bounds__(256) cache_read_kernel(const ReadArgs a) {
+  pdl_wait();
+  constexpr int kHalves = FMT == kFmtIk ? 1 : 2;   // pieces per lane and row
+  constexpr int kRows = FMT == kFmtIk ? 2 : 1;     // rows per warp step
+  constexpr int kWidth = FMT == kFmtIk ? DI : D;
+  const int lane = threadIdx.x & 31;
+  const int sub = FMT == kFmtIk ? lane >> 4 : 0;
+  const int piece = FMT == kFmtIk ? lane & 15 : lane;
+  const int64_t first = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * (R * kRows) + sub;
+  if (first - sub >= a.total) return;
+  int64_t row[R];
+  Piece p[R][kHalves];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = first + r * kRows;
+    row[r] = -1;
+    if (i < a.total) {
+      const int64_t b = i / a.k;
+      const int64_t id = a.idx ? (int64_t)__ldg(a.idx + i) : i - b * a.k;
+      if (id >= a.cap) {
+        if (piece == 0) set_error(CSA2_DEV_ERR_INDEX);
+      } else if (id >= 0) {
+        row[r] = b * a.cap + id;
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+      if (row[r] >= 0) p[r][h] = load_piece<FMT>(a, row[r], piece + 32 * h);
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int64_t i = first + r * kRows;
+    if (i >= a.total) continue;
+    uint4 *dst = reinterpret_cast<uint4 *>(a.out + i * kWidth);
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+      dst[piece + 32 * h] = row[r] >= 0 ? decode_piece<FMT>(p[r][h]) : make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <int FMT>
+cudaError_t launch_read(const ReadArgs &a, cudaStream_t stream) {
+  constexpr int kRows = FMT == kFmtIk ? 2 : 1;
+  const int64_t steps = (a.total + kRows - 1) / kRows;
+  // few rows: one step per warp and one warp per block, over all SMs
+  if (steps <= 2048)
+    return launch_pdl(cache_read_kernel<FMT, 1>, dim3((unsigned)steps), dim3(32), 0, stream, 0u, a);
+  const int64_t blocks = (steps + 31) / 32;   // 8 warps x 4 steps
+  return launch_pdl(cache_read_kernel<FMT, 4>, dim3((unsigned)blocks), dim3(256), 0, stream, 0u, a);
+}
+
+}  // namespace
+
+cudaError_t launch_swa_quant_write(const void *latent, int64_t n, const int64_t *pos, const int64_t *slot, uint8_t *swa,
+                                   float *swa_scale, int64_t rows, float rope_theta, cudaStream_t stream) {
+  // 1 / (2 pi) = 0x0.28BE60DB9391054A7F09D5F47D4D3770... (binary expansion)
+  constexpr uint64_t kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;
+  RopeTurns turns = {};
+  if (pos) {
+    for (int j = 0; j < ROPE_DIM / 2; ++j) {
+      const float inv = (float)std::pow((double)rope_theta, -(2.0 * j) / (double)ROPE_DIM);
+      int ex;
+      const uint64_t m = (uint64_t)std::ldexp(std::frexp(inv, &ex), 24);   // inv = m * 2^(ex - 24), ex <= 1
+      const unsigned __int128 lo = (unsigned __int128)m * kLo;
+      const unsigned __int128 prod = (unsigned __int128)m * kHi + (uint64_t)(lo >> 64);   // 2^64 m / (2 pi)
+      const int sh = 24 - ex;
+      turns.step[j] = sh >= 128 ? 0 : (uint64_t)(prod >> sh);
+    }
+  }
+  const int warps = n <= 1024 ? 1 : 8;
+  const int64_t blocks = (n + warps - 1) / warps;
+  return launch_pdl(swa_quant_write_kernel, dim3((unsigned)blocks), dim3(warps * 32), 0, stream, 0u,
+                    static_cast<const __nv_bfloat16 *>(latent), n, pos, slot, swa, swa_scale, rows, turns);
+}
+
+cudaError_t launch_kv_read(const uint8_t *kv, int64_t batch, int64_t cap, const int32_t *idx, int64_t k, void *out,
+                           cudaStream_t stream) {
+  const ReadArgs a{kv, nullptr, idx, static_cast<__nv_bfloat16 *>(out), cap, batch * k, k};
+  return launch_read<kFmtKv>(a, stream);
+}
+
+cudaError_t launch_swa_read(const uint8_t *swa, const float *swa_scale, int64_t batch, int64_t rows, const int32_t *idx,
+                            int64_t k, void *out, cudaStream_t stream) {
+  const ReadArgs a{swa, swa_scale, idx, static_cast<__nv_bfloat16 *>(out), rows, batch * k, k};
+  return launch_read<kFmtSwa>(a, stream);
+}
+
+cudaError_t launch_indexer_k_read(const uint8_t *k_fp4, int64_t batch, int64_t cap, const int32_t *idx, int64_t k,
+                                  void *out, cudaStream_t stream) {
+  const ReadArgs a{k_fp4, k_fp4 + batch * cap * (DI / 2), idx, static_cast<__nv_bfloat16 *>(out), cap, batch * k, k};
+  return launch_read<kFmtIk>(a, stream);
+}
+
+}  // namespace csa2

@@ -1,0 +1,135 @@
+// Work split of the dense readout (csa2_cross_attn, csa2_prefix_attn).
+//
+// A unit is a pair of query tokens of one sequence (128 query rows) against
+// one step of kDenseStep entries.  The units of all pairs, sequence by
+// sequence and pair by pair, form one line that the workers (clusters of two
+// CTAs) cut into equal contiguous ranges, whatever the sequences' lengths: a
+// worker's range is the end of one pair, whole pairs, and the start of
+// another.  A pair inside one range is finished there; the others leave one
+// partial per range, merged by dense_combine_kernel.  So a worker has at most
+// two partials: slot 2w for the pair that holds the range's first unit, slot
+// 2w + 1 for a pair that starts inside the range.
+#pragma once
+#include "kernels.cuh"
+
+namespace csa2 {
+
+constexpr int kDenseStep = 256;      // entries per unit
+constexpr int kDenseWorkers = 76;    // most workers (one CTA pair per two SMs)
+
+struct DenseArgs {
+  const __nv_bfloat16 *q;      // [seqs][n_q][64][512]
+  const uint8_t *kv;           // [seqs][cap][288]
+  const int32_t *n_vis;        // [seqs], or NULL: n_max entries each
+  int64_t n_max, cap;
+  int32_t seqs, n_q;
+  int32_t workers;
+  __nv_bfloat16 *out;          // [seqs][n_q][64][512]
+  float *lse;                  // [seqs][n_q][64] or NULL
+  const float *own_out;        // another part of each token's softmax to merge in
+  const float *own_lse;        // (fp32 rows and natural log-sum-exps), or NULL
+  __half *part;                // [2 workers][2 tokens][64][512] normalised partials
+  float *part_lse;             // [2 workers][2 tokens][64] their natural log-sum-exps
+};
+
+__device__ __forceinline__ int64_t dense_len(const DenseArgs &a, int b) {
+  if (!a.n_vis) return a.n_max;
+  const int64_t n = __ldg(a.n_vis + b);
+  if (n < 0 || n > a.n_max) set_error(CSA2_DEV_ERR_NVIS);
+  return n < 0 ? 0 : n > a.n_max ? a.n_max : n;
+}
+
+__device__ __forceinline__ int64_t dense_steps(int64_t n) { return (n + kDenseStep - 1) / kDenseStep; }
+
+// Units of sequences [0, b) and of all sequences, and how many workers have
+// a range (a.workers, but no more than there are units: no range is empty);
+// a whole warp calls it.
+__device__ __forceinline__ void dense_units(const DenseArgs &a, int b, int lane, int64_t &before, int64_t &total,
+                                            int &workers) {
+  const int64_t pairs = (a.n_q + 1) / 2;
+  if (!a.n_vis) {
+    before = b * pairs * dense_steps(a.n_max);
+    total = a.seqs * pairs * dense_steps(a.n_max);
+    workers = (int)(total < a.workers ? total : a.workers);
+    return;
+  }
+  int64_t x = 0, y = 0;
+  for (int i = lane; i < a.seqs; i += 32) {
+    const int64_t s = dense_steps(dense_len(a, i));
+    y += s;
+    if (i < b) x += s;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    x += __shfl_xor_sync(0xffffffffu, x, o);
+    y += __shfl_xor_sync(0xffffffffu, y, o);
+  }
+  before = x * pairs;
+  total = y * pairs;
+  workers = (int)(total < a.workers ? total : a.workers);
+}
+
+// Worker w's range starts at unit floor(w total / workers).
+__device__ __forceinline__ int64_t dense_range(int64_t total, int workers, int w) { return total * w / workers; }
+
+// The worker whose range holds unit u.
+__device__ __forceinline__ int dense_worker(int64_t total, int workers, int64_t u) {
+  return (int)(((u + 1) * workers - 1) / total);
+}
+
+// A worker's walk over its range, one segment (a pair and its steps inside
+// the range) at a time.
+struct DenseWalk {
+  int64_t at, end;        // the unit that comes next, the range's end
+  int64_t start;          // the range's first unit
+  int64_t seq0;           // first unit of sequence b
+  int b;
+  int64_t len, steps;     // of sequence b
+};
+
+struct DenseSegment {
+  int b, pair;
+  int64_t len;            // entries of the sequence
+  int64_t s0, s1;         // steps [s0, s1) of the pair
+  bool whole;             // every step of the pair
+  int slot;               // partial slot otherwise
+};
+
+__device__ __forceinline__ DenseWalk dense_walk(const DenseArgs &a, int w, int lane) {
+  DenseWalk k;
+  int64_t before, total;
+  int workers;
+  dense_units(a, 0, lane, before, total, workers);
+  k.start = k.at = w < workers ? dense_range(total, workers, w) : 0;
+  k.end = w < workers ? dense_range(total, workers, w + 1) : 0;
+  k.seq0 = 0;
+  k.b = 0;
+  k.len = k.at < k.end ? dense_len(a, 0) : 0;
+  k.steps = dense_steps(k.len);
+  return k;
+}
+
+// The next segment; false at the range's end.  Any thread, no warp operation.
+__device__ __forceinline__ bool dense_next(const DenseArgs &a, int w, DenseWalk &k, DenseSegment &g) {
+  if (k.at >= k.end) return false;
+  const int64_t pairs = (a.n_q + 1) / 2;
+  while (k.at >= k.seq0 + pairs * k.steps) {   // at < end <= total: some sequence holds it
+    k.seq0 += pairs * k.steps;
+    ++k.b;
+    k.len = dense_len(a, k.b);
+    k.steps = dense_steps(k.len);
+  }
+  const int64_t rel = k.at - k.seq0;
+  g.b = k.b;
+  g.pair = (int)(rel / k.steps);
+  g.len = k.len;
+  g.s0 = rel - (int64_t)g.pair * k.steps;
+  const int64_t left = k.steps - g.s0;
+  g.s1 = g.s0 + (left < k.end - k.at ? left : k.end - k.at);
+  g.whole = g.s0 == 0 && g.s1 == k.steps;
+  g.slot = 2 * w + (k.at == k.start ? 0 : 1);
+  k.at += g.s1 - g.s0;
+  return true;
+}
+
+}  // namespace csa2

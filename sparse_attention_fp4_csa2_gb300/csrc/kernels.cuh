@@ -229,4 +229,23 @@ size_t attn_scratch_bytes(int32_t problems, int32_t K, int32_t W, int32_t kernel
 cudaError_t attn_take_error(unsigned int *bits);
 cudaError_t launch_sparse_attn(AttnArgs a, void *scratch, cudaStream_t stream, int *launches);
 
+// Sliding-window rows as FP8 (pos NULL: no RoPE) and the caches' read-backs
+// (idx NULL: rows 0 .. k - 1 of each sequence).
+cudaError_t launch_swa_quant_write(const void *latent, int64_t n, const int64_t *pos, const int64_t *slot, uint8_t *swa,
+                                   float *swa_scale, int64_t rows, float rope_theta, cudaStream_t stream);
+cudaError_t launch_kv_read(const uint8_t *kv, int64_t batch, int64_t cap, const int32_t *idx, int64_t k, void *out,
+                           cudaStream_t stream);
+cudaError_t launch_swa_read(const uint8_t *swa, const float *swa_scale, int64_t batch, int64_t rows, const int32_t *idx,
+                            int64_t k, void *out, cudaStream_t stream);
+cudaError_t launch_indexer_k_read(const uint8_t *k_fp4, int64_t batch, int64_t cap, const int32_t *idx, int64_t k,
+                                  void *out, cudaStream_t stream);
+
+// Dense readout of seqs x n_q tokens over the first n_vis[b] (NULL: n_max)
+// entries of their sequence, merged with own_out / own_lse (fp32 rows and
+// log-sum-exps of another part of each token's softmax) unless NULL.
+size_t dense_scratch_bytes();
+cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n_vis, int64_t n_max, int64_t cap,
+                              int32_t seqs, int32_t n_q, void *out, float *lse, const float *own_out,
+                              const float *own_lse, void *scratch, int num_sms, cudaStream_t stream, int *launches);
+
 }  // namespace csa2
