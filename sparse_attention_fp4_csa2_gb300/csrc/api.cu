@@ -174,12 +174,12 @@ struct PrefixLayout {
   size_t out_off, lse_off, part_off, attn_off, end;
 };
 
-PrefixLayout prefix_layout(int32_t batch, const csa2_params *p) {
+PrefixLayout prefix_layout(int32_t batch, int64_t n_prefix, const csa2_params *p) {
   PrefixLayout L;
   L.out_off = 0;
   L.lse_off = (size_t)batch * H * D * 4;
   L.part_off = L.lse_off + (size_t)round_up((int64_t)batch * H * 4, 256);
-  L.attn_off = L.part_off + (size_t)round_up((int64_t)dense_scratch_bytes(), 256);
+  L.attn_off = L.part_off + (size_t)round_up((int64_t)dense_scratch_bytes(batch, n_prefix), 256);
   L.end = L.attn_off + attn_ws(batch, p);
   return L;
 }
@@ -390,8 +390,8 @@ size_t csa2_workspace_bytes(csa2_op op, int32_t batch, int64_t n_max, const csa2
     case CSA2_OP_ATTN: return attn_ws(batch, params);
     case CSA2_OP_DECODE: return decode_ws(batch, n_max, params);
     case CSA2_OP_PREFILL: return prefill_ws(batch, n_max, params);
-    case CSA2_OP_PREFIX: return prefix_layout(batch, params).end;
-    case CSA2_OP_CROSS: return dense_scratch_bytes();
+    case CSA2_OP_PREFIX: return prefix_layout(batch, n_max, params).end;
+    case CSA2_OP_CROSS: return dense_scratch_bytes(batch, n_max);
   }
   return 0;
 }
@@ -402,6 +402,8 @@ csa2_status csa2_get_device_status(csa2_stream_t stream, uint32_t *bits) {
   if (cudaMemcpyFromSymbol(&v, g_dev_error, sizeof(v)) != cudaSuccess) return CSA2_ERR_CUDA;
   if (v && cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero)) != cudaSuccess) return CSA2_ERR_CUDA;
   if (attn_take_error(&va) != cudaSuccess) return CSA2_ERR_CUDA;   // the readout's own word
+  v |= va;
+  if (dense_take_error(&va) != cudaSuccess) return CSA2_ERR_CUDA;   // the dense readout's
   v |= va;
   if (bits) *bits = v;
   return v ? CSA2_ERR_DEVICE : CSA2_OK;
@@ -726,7 +728,7 @@ extern "C" csa2_status csa2_cross_attn(int32_t batch, int32_t n_q, const void *q
   if (!aligned16(q) || !aligned16(kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return CSA2_ERR_INVALID_ARG;
   if ((int64_t)batch * n_q > kMaxDenseTokens || cap > kMaxCacheRows / batch) return CSA2_ERR_UNSUPPORTED;
-  if (ws_bytes < dense_scratch_bytes()) return CSA2_ERR_WORKSPACE;
+  if (ws_bytes < dense_scratch_bytes((int64_t)batch * n_q, n_max)) return CSA2_ERR_WORKSPACE;
   int launches = 0;
   if (launch_dense_attn(q, kv, n_vis, n_max, cap, batch, n_q, out, lse, nullptr, nullptr, ws, num_sms(),
                         reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
@@ -747,7 +749,7 @@ extern "C" csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch
   if (!aligned16(prefix_kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return CSA2_ERR_INVALID_ARG;
   if (n_prefix > kMaxCacheRows) return CSA2_ERR_UNSUPPORTED;
-  const PrefixLayout L = prefix_layout(batch, params);
+  const PrefixLayout L = prefix_layout(batch, n_prefix, params);
   if (ws_bytes < L.end) return CSA2_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);
   float *own_out = reinterpret_cast<float *>(wsb + L.out_off);

@@ -27,6 +27,10 @@
 // Every wait is bounded; after one runs out every role falls through its
 // waits, the CTAs meet at the end and the output is undefined
 // (CSA2_DEV_ERR_TIMEOUT).
+//
+// This unit is compiled without relocatable device code, so that ptxas allots
+// each role the registers its setmaxnreg asks for; it keeps its own error word.
+#define CSA2_WHOLE_PROGRAM_TU 1
 #include "dense_plan.cuh"
 
 namespace csa2 {
@@ -35,7 +39,10 @@ namespace {
 
 constexpr int kSoftWarps = 4, kDeqWarps = 8;
 constexpr int kMmaWarpD = kSoftWarps + kDeqWarps;
-constexpr int kThreadsD = (kMmaWarpD + 1) * 32;
+constexpr int kThreadsD = (kMmaWarpD + 4) * 32;   // whole warpgroups: setmaxnreg
+// registers: 4 warpgroups launched with 128 a thread
+constexpr uint32_t kRegsSoft = 144, kRegsDeq = 152, kRegsMmaD = 64;
+static_assert(kRegsSoft + 2 * kRegsDeq + kRegsMmaD <= 4 * 128, "register split exceeds the launch budget");
 constexpr int kSlots = 8;
 constexpr int kSlotBytes = 16384;             // 128 keys x 64 channels, or 32 keys x 256 channels
 constexpr int kQBytesD = H * D * 2;
@@ -52,7 +59,7 @@ constexpr uint32_t kIdescS = idesc_f16(0, 0, 0, 256, 128);
 constexpr uint32_t kIdescO = idesc_f16(0, 0, /*B MN-major*/ 1, 256, 128);
 
 struct __align__(16) CtlD {
-  uint64_t full[kSlots], free[kSlots];        // full: both CTAs' warps arrive at the even CTA
+  uint64_t full[kSlots], free[kSlots];        // full, q_full, p_full: both CTAs arrive at the even CTA
   uint64_t q_full, q_free, s_full[2], p_full, p_free, done;
   uint32_t tmem_base;
   volatile uint32_t abort;
@@ -62,31 +69,24 @@ struct __align__(16) CtlD {
 constexpr size_t kSmemD = 1024 + (size_t)kQBytesD + kPBytes + kSlots * kSlotBytes + sizeof(CtlD);
 static_assert(kSmemD <= 232448, "dense readout exceeds the shared-memory limit");
 
+// A wait for arrivals of this CTA or of the tensor cores, and one that is also
+// ordered after the other CTA's arrivals.
 __device__ __forceinline__ void wait_d(CtlD &S, uint64_t *bar, uint32_t parity) {
-  if (S.abort) return;
+  if (mbar_try_wait(bar, parity) || S.abort) return;
+  if (!mbar_wait(bar, parity)) S.abort = 1;
+}
+__device__ __forceinline__ void wait_pair(CtlD &S, uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait_cluster(bar, parity) || S.abort) return;
   if (!mbar_wait_cluster(bar, parity)) S.abort = 1;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
-}
-
-// 32 channels of one entry (16 bytes of codes, their two scales in the low
-// half of sc) as fp16 into chunks c0 .. c0 + 3 of a 128-byte row whose 16-byte
-// chunks are XOR-swizzled by sw.
-__device__ __forceinline__ void put32(uint8_t *row, int c0, int sw, const uint4 &v, uint32_t sc) {
-  const uint32_t s = e4m3x2_to_half2((uint16_t)sc);
-  const uint32_t s0 = __byte_perm(s, 0, 0x1010), s1 = __byte_perm(s, 0, 0x3232);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t h[4];
-    e2m1x8_to_half2x4(w[i], h);
-    const uint32_t si = i < 2 ? s0 : s1;
-    *reinterpret_cast<uint4 *>(row + (((c0 + i) ^ sw) << 4)) =
-        make_uint4(hmul2_u32(h[0], si), hmul2_u32(h[1], si), hmul2_u32(h[2], si), hmul2_u32(h[3], si));
-  }
 }
 
 // ---------------------------------------------------------- dequantisation
@@ -95,23 +95,71 @@ __device__ __forceinline__ void put32(uint8_t *row, int c0, int sw, const uint4 
 //     [128 keys][128 B];
 //   V(i), 8 slots: 32 keys of the step per slot, this CTA's 256 channels,
 //     [4 x 64 channels][32 keys][128 B].
-// Thread (key, half) of a K slot and (64 channels, key, half) of a V slot
-// handles 32 channels, 16 bytes of codes: two neighbours read a full sector
-// and eight write eight different bank groups.  Keys past the sequence's
-// length become zeros.
+// A lane takes 32 channels (16 bytes of codes, two scales) of a key and eight
+// lanes read 128 contiguous bytes of an entry, so that a load touches few
+// lines: the L1 / shared-memory data pipe is what the kernel runs against
+// (two lanes per key and 16 lines a load took it 16 passes).  Of K a warp holds
+// 16 keys over all channels, four slots at a time; of V it fills slot `warp`
+// alone.  The eight lanes of a key write four slots (or channel blocks) at
+// the same offset, so each starts at another 16-byte chunk: chunk i ^ (lane %
+// 8 / 2) of its four at step i, eight bank groups for eight lanes.  Keys past
+// the sequence's length become zeros.
 struct DeqRegs {
   uint4 v[8];
   uint32_t sc[8];
 };
 
+// 32 channels into a 128-byte swizzled row: `at` is the place of the lane's
+// first chunk, chunk i of its order at ^ 16 i; o = lane % 8 / 2.
+__device__ __forceinline__ void put32(uint32_t at, const uint4 &v, uint32_t sc, bool o1, bool o2) {
+  const uint32_t e = e4m3x2_to_half2((uint16_t)sc);
+  const uint32_t s0 = __byte_perm(e, 0, o2 ? 0x3232 : 0x1010), s1 = __byte_perm(e, 0, o2 ? 0x1010 : 0x3232);
+  const uint32_t x = o1 ? v.y : v.x, y = o1 ? v.x : v.y, z = o1 ? v.w : v.z, u = o1 ? v.z : v.w;
+  const uint32_t w[4] = {o2 ? z : x, o2 ? u : y, o2 ? x : z, o2 ? y : u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[4];
+    e2m1x8_to_half2x4(w[i], h);
+    const uint32_t si = i < 2 ? s0 : s1;
+    st_shared_v4(at ^ (uint32_t)(i << 4), hmul2_u32(h[0], si), hmul2_u32(h[1], si), hmul2_u32(h[2], si),
+                 hmul2_u32(h[3], si));
+  }
+}
+
+// Q of a token, bf16 -> fp16 (zeros for the missing token of an odd count).
+template <int T>
+__device__ __forceinline__ void convert_q(const DenseArgs &a, const DenseSegment &g, uint32_t rank, uint8_t *qs, int i0) {
+  const int t = 2 * g.pair + (int)rank;
+  const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((int64_t)g.b * a.n_q + t) * (H * D));
+#pragma unroll 1
+  for (; i0 < H * D / 8; i0 += T * 8) {
+    uint4 u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = t < a.n_q ? ld_nc_v4(src + i0 + i * T) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = i0 + i * T, r = at >> 6, c = at & 63;
+      const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = half2_bits(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
+      *reinterpret_cast<uint4 *>(qs + (c >> 3) * kAtomD + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+          make_uint4(h[0], h[1], h[2], h[3]);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
 __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ring, int w, uint32_t rank, int pt,
                               int lane) {
-  const int hf = pt & 1, key = pt >> 1;
-  const int vkey = key & 31, vatom = key >> 5;
-  uint32_t full_at[kSlots];
-#pragma unroll
-  for (int s = 0; s < kSlots; ++s) full_at[s] = dsmem_addr(&S.full[s], 0);
-  const uint32_t q_full_at = dsmem_addr(&S.q_full, 0);
+  const int warp = pt >> 5, key4 = lane >> 3, c8 = lane & 7;
+  const int o = c8 >> 1;
+  const bool o1 = o & 1, o2 = o & 2;
+  const uint32_t z = (uint32_t)((4 * (c8 & 1)) ^ key4 ^ o) << 4;
+  const uint32_t k_at = smem_u32(ring) + (uint32_t)(o * kSlotBytes + (16 * warp + key4) * 128) + z;
+  const uint32_t v_at = smem_u32(ring) + (uint32_t)(warp * kSlotBytes + o * 4096 + key4 * 128) + z;
+  const uint32_t full_at = dsmem_addr(&S.full[0], 0), q_full_at = dsmem_addr(&S.q_full, 0);
   DenseWalk walk = dense_walk(a, w, lane);
   DenseSegment g;
   uint32_t round = 0;   // 8-slot rounds so far
@@ -119,77 +167,58 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
   DeqRegs kr, vr;
   while (dense_next(a, w, walk, g)) {
     const uint8_t *base = a.kv + (int64_t)g.b * a.cap * ENTRY_BYTES;
-    auto load_k = [&](int64_t step) {
-      const int64_t n = step * kDenseStep + (int)rank * 128 + key;
+    auto load_piece = [&](DeqRegs &r, int i, int64_t n, int half) {   // channels 256 half + 32 c8 .. of entry n
+      r.v[i] = make_uint4(0, 0, 0, 0);
+      r.sc[i] = 0;
       if (n < g.len) {
         const uint8_t *e = base + n * ENTRY_BYTES;
-#pragma unroll
-        for (int p = 0; p < 8; ++p) kr.v[p] = ld_nc_v4(e + 32 * p + 16 * hf);
-        const uint4 s0 = ld_nc_v4(e + 256), s1 = ld_nc_v4(e + 272);
-        const uint32_t sw[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
-#pragma unroll
-        for (int p = 0; p < 8; ++p) kr.sc[p] = sw[p];
-      } else {
-#pragma unroll
-        for (int p = 0; p < 8; ++p) {
-          kr.v[p] = make_uint4(0, 0, 0, 0);
-          kr.sc[p] = 0;
-        }
+        r.v[i] = ld_nc_v4(e + 128 * half + 16 * c8);
+        r.sc[i] = ld_nc_u16(e + 256 + 16 * half + 2 * c8);
       }
     };
-    auto load_v = [&](int64_t step) {
+    auto load_k = [&](int64_t step) {   // [channel half][4 keys]
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int64_t n = step * kDenseStep + 32 * j + vkey;
-        if (n < g.len) {
-          const uint8_t *e = base + n * ENTRY_BYTES + (int)rank * 128 + vatom * 32;
-          vr.v[j] = ld_nc_v4(e + 16 * hf);
-          vr.sc[j] = ld_nc_u32(base + n * ENTRY_BYTES + 256 + (int)rank * 16 + vatom * 4);
-        } else {
-          vr.v[j] = make_uint4(0, 0, 0, 0);
-          vr.sc[j] = 0;
-        }
-      }
+      for (int i = 0; i < 8; ++i)
+        load_piece(kr, i, step * kDenseStep + (int)rank * 128 + 16 * warp + 4 * (i & 3) + key4, i >> 2);
     };
-    auto emit = [&](const DeqRegs &r, uint8_t *row0, int sw) {
+    auto load_v = [&](int64_t step) {   // [4 keys]
 #pragma unroll
-      for (int s = 0; s < 8; ++s) {
-        if (round) wait_d(S, &S.free[s], (round - 1) & 1u);
-        put32(row0 + s * kSlotBytes, 4 * hf, sw, r.v[s], hf ? r.sc[s] >> 16 : r.sc[s]);
+      for (int i = 0; i < 8; ++i) load_piece(vr, i, step * kDenseStep + 32 * warp + 4 * i + key4, (int)rank);
+    };
+    auto emit_k = [&]() {
+#pragma unroll
+      for (int hc = 0; hc < 2; ++hc) {
+        if (round)
+#pragma unroll
+          for (int s = 0; s < 4; ++s) wait_d(S, &S.free[4 * hc + s], (round - 1) & 1u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          put32((k_at + (uint32_t)(4 * hc * kSlotBytes + i * 512)) ^ (uint32_t)((i & 1) << 6), kr.v[4 * hc + i],
+                kr.sc[4 * hc + i], o1, o2);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(full_at[s]);
+        if (lane < 4) mbar_arrive_pair(full_at + 8 * (4 * hc + lane), 1);
       }
       ++round;
     };
-    auto emit_k = [&]() { emit(kr, ring + key * 128, key & 7); };
-    auto emit_v = [&]() { emit(vr, ring + vatom * 4096 + vkey * 128, vkey & 7); };
+    auto emit_v = [&]() {
+      if (round) wait_d(S, &S.free[warp], (round - 1) & 1u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        put32((v_at + (uint32_t)(i * 512)) ^ (uint32_t)((i & 1) << 6), vr.v[i], vr.sc[i], o1, o2);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(full_at + 8 * warp, kDeqWarps);
+      ++round;
+    };
 
     load_k(g.s0);
     load_v(g.s0);
-    // Q of this CTA's token, bf16 -> fp16 (zeros for the missing token of an odd count)
-    const int t = 2 * g.pair + (int)rank;
-    const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((int64_t)g.b * a.n_q + t) * (H * D));
-    if (item) wait_d(S, &S.q_free, (item - 1) & 1u);
-#pragma unroll 1
-    for (int i0 = 0; i0 < H * D / 8; i0 += 256 * 8) {
-      uint4 u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = t < a.n_q ? ld_nc_v4(src + i0 + i * 256 + pt) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = i0 + i * 256 + pt, r = at >> 6, c = at & 63;
-        const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = half2_bits(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
-        *reinterpret_cast<uint4 *>(qs + (c >> 3) * kAtomD + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-            make_uint4(h[0], h[1], h[2], h[3]);
-      }
+    if (item) {   // the first segment's Q is the softmax warps' (they have nothing else to do then)
+      wait_d(S, &S.q_free, (item - 1) & 1u);
+      convert_q<kDeqWarps * 32>(a, g, rank, qs, pt);
+      if (lane == 0) mbar_arrive_pair(q_full_at, 1);
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(q_full_at);
     ++item;
 
     emit_k();
@@ -226,7 +255,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
     auto scores = [&](uint32_t tile) {
 #pragma unroll 1
       for (int s = 0; s < kSlots; ++s) {
-        wait_d(S, &S.full[s], round & 1u);
+        wait_pair(S, &S.full[s], round & 1u);
         tc_fence_after();
         const uint64_t qa = qd + (uint64_t)(s * kAtomD >> 4), kb = kd + (uint64_t)(s * kSlotBytes >> 4);
 #pragma unroll
@@ -236,7 +265,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
       ++round;
       mma_commit_pair(&S.s_full[tile]);
     };
-    wait_d(S, &S.q_full, item & 1u);
+    wait_pair(S, &S.q_full, item & 1u);
     ++item;
     scores(n & 1u);
     if (steps == 1) mma_commit_pair(&S.q_free);
@@ -246,19 +275,19 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
         scores((n + 1) & 1u);
         if (i + 2 == steps) mma_commit_pair(&S.q_free);
       }
-      wait_d(S, &S.p_full, n & 1u);
+      wait_pair(S, &S.p_full, n & 1u);
       tc_fence_after();
 #pragma unroll 1
       for (int s = 0; s < kSlots; ++s) {
-        wait_d(S, &S.full[s], round & 1u);
+        wait_pair(S, &S.full[s], round & 1u);
         tc_fence_after();
         const uint64_t pa = pd + (uint64_t)((s >> 1) * kAtomD >> 4) + 4 * (s & 1);
         const uint64_t vb = vd + (uint64_t)(s * kSlotBytes >> 4);
         const uint32_t acc = (i || s) ? 1u : 0u;
-        mma_f16_pair(tmem + kColOut, pa, vb, kIdescO, acc);
-        mma_f16_pair(tmem + kColOut + 128, pa, vb + 512, kIdescO, acc);
-        mma_f16_pair(tmem + kColOut, pa + 2, vb + 128, kIdescO, 1u);
-        mma_f16_pair(tmem + kColOut + 128, pa + 2, vb + 512 + 128, kIdescO, 1u);
+        mma_f16_pair_a_fill(tmem + kColOut, pa, vb, kIdescO, acc);
+        mma_f16_pair_a_last(tmem + kColOut + 128, pa, vb + 512, kIdescO, acc);
+        mma_f16_pair_a_fill(tmem + kColOut, pa + 2, vb + 128, kIdescO, 1u);
+        mma_f16_pair_a_last(tmem + kColOut + 128, pa + 2, vb + 512 + 128, kIdescO, 1u);
         mma_commit_pair(&S.free[s]);
       }
       ++round;
@@ -273,7 +302,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
 // ----------------------------------------------------------------- softmax
 // Thread tid holds head tid % 64: of S the keys 128 (tid / 64) .. + 127 of a
 // step, of O the channels 256 (tid / 64) .. + 255.
-__device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *ps, uint32_t tmem, int w, uint32_t rank, int tid,
+__device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ps, uint32_t tmem, int w, uint32_t rank, int tid,
                               int lane, int warp) {
   const uint32_t p_full_at = dsmem_addr(&S.p_full, 0);
   const uint32_t row = tmem + ((uint32_t)(32 * warp) << 16);
@@ -281,6 +310,13 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *ps, uint32_t
   uint8_t *prow = ps + 2 * kh * kAtomD + h * 128;
   DenseWalk walk = dense_walk(a, w, lane);
   DenseSegment g;
+  {
+    DenseWalk peek = walk;
+    if (dense_next(a, w, peek, g)) {
+      convert_q<kSoftWarps * 32>(a, g, rank, qs, tid);
+      if (lane == 0) mbar_arrive_pair(dsmem_addr(&S.q_full, 0), kDeqWarps / kSoftWarps);
+    }
+  }
   uint32_t n = 0;
   while (dense_next(a, w, walk, g)) {
     float m = 0.0f, l = 0.0f;
@@ -468,12 +504,15 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
   const uint32_t tmem = S.tmem_base;
 
   if (warp < kSoftWarps) {
-    dense_softmax(a, S, ps, tmem, w, rank, tid, lane, warp);
+    setmaxnreg_inc<kRegsSoft>();
+    dense_softmax(a, S, qs, ps, tmem, w, rank, tid, lane, warp);
   } else if (warp < kMmaWarpD) {
+    setmaxnreg_inc<kRegsDeq>();
     dense_dequant(a, S, qs, ring, w, rank, tid - kSoftWarps * 32, lane);
-  } else if (rank == 0) {
+  } else {
+    setmaxnreg_dec<kRegsMmaD>();
     const DenseWalk walk = dense_walk(a, w, lane);
-    if (lane == 0) dense_products(a, S, qs, ps, ring, tmem, w, walk);
+    if (rank == 0 && warp == kMmaWarpD && elect_one()) dense_products(a, S, qs, ps, ring, tmem, w, walk);
     __syncwarp();
   }
   tc_fence_before();
@@ -486,66 +525,170 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
   }
 }
 
-// One CTA per token: the token's partials (and the other part of its
-// softmax) with the weights exp(lse_i - lse), lse the log-sum-exp over all of
-// them.  Warp w merges heads 8w .. 8w + 7; lane l owns channels 16 l .. + 15.
-// Partials are fp16 rows, normalised, so within the entries' range of +-2688:
-// their rounding (2^-12 of a row) is below the bf16 output's (2^-9).
-__global__ void __launch_bounds__(256) dense_combine_kernel(const DenseArgs a) {
+// Merges the pairs that several workers share, with the weights exp(lse_i -
+// lse), lse the log-sum-exp over all their partials (and the other part of the
+// softmax).  Only a pair across a range's start is shared, so there are at
+// most workers - 1: the CTAs of worker w's start take the pair if that is its
+// first such start, for one token and two heads each; four warps per head
+// take every fourth partial.  Partials are normalised fp16 rows, within the
+// entries' +-2688; their rounding (2^-11 of a value) is below the output's
+// (2^-8).  The CTAs past those write the sequences without entries.
+constexpr int kCombineHeads = 2, kCombineWarps = 4;
+constexpr int kCombineCtas = 2 * (H / kCombineHeads);   // per worker
+constexpr int kEmptyCtas = 64;
+
+__device__ __forceinline__ void put_row16(const DenseArgs &a, int64_t row, int lane, const float (&o)[16]) {
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+    u[i] = *reinterpret_cast<const uint32_t *>(&v);
+  }
+  uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * D + lane * 16);
+  dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
+  dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
+}
+
+// Tokens with no entry at all: the other part of the softmax alone, or zeros.
+__device__ __forceinline__ void rest_rows(const DenseArgs &a, int64_t row0, int64_t rows, int warp, int warps, int lane) {
+  for (int64_t row = row0 + warp; row < row0 + rows; row += warps) {
+    float o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = a.own_out ? a.own_out[row * D + lane * 16 + i] : 0.0f;
+    put_row16(a, row, lane, o);
+    if (lane == 0 && a.lse) a.lse[row] = a.own_lse ? a.own_lse[row] : -INFINITY;
+  }
+}
+
+__global__ void __launch_bounds__(kCombineHeads * kCombineWarps * 32) dense_combine_kernel(const DenseArgs a) {
+  __shared__ float red[kCombineHeads][kCombineWarps][D];
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t token = blockIdx.x;
-  const int b = (int)(token / a.n_q), t = (int)(token % a.n_q), r = t & 1;
   int64_t before, total;
   int workers;
-  dense_units(a, b, lane, before, total, workers);
-  const int64_t steps = dense_steps(dense_len(a, b));
-  const int64_t u0 = before + (int64_t)(t >> 1) * steps;
-  int w0 = 0, w1 = -1;   // no segment
-  if (steps > 0) {
-    w0 = dense_worker(total, workers, u0);
-    w1 = dense_worker(total, workers, u0 + steps - 1);
-    if (w0 == w1) return;   // finished by its worker
+  dense_units(a, 0, lane, before, total, workers);
+  const int w = blockIdx.x / kCombineCtas;
+  if (w >= a.workers) {
+    const int warps = blockDim.x >> 5, ctas = gridDim.x - a.workers * kCombineCtas;
+    const int me = (blockIdx.x - a.workers * kCombineCtas) * warps + warp;
+    for (int b = 0; b < a.seqs; ++b)
+      if (dense_len(a, b) == 0) rest_rows(a, (int64_t)b * a.n_q * H, (int64_t)a.n_q * H, me, ctas * warps, lane);
+    return;
   }
-#pragma unroll 1
-  for (int h = 0; h < 8; ++h) {
-    const int head = warp * 8 + h;
-    const int64_t row = token * H + head;
-    auto part_row = [&](int w) {
-      const int slot = 2 * w + (dense_range(total, workers, w) >= u0 ? 0 : 1);
-      return ((int64_t)slot * 2 + r) * H + head;
-    };
-    float mx = a.own_lse ? a.own_lse[row] : -INFINITY;
-    for (int w = w0; w <= w1; ++w) mx = fmaxf(mx, a.part_lse[part_row(w)]);
-    float acc[16], sum = 0.0f;
+  if (w == 0 || w >= workers) return;
+  // the pair that holds the range's first unit
+  const int64_t at = dense_range(total, workers, w), pairs = (a.n_q + 1) / 2;
+  int b = 0;
+  int64_t seq0 = 0, steps = dense_steps(dense_len(a, 0));
+  while (at >= seq0 + pairs * steps) {
+    seq0 += pairs * steps;
+    steps = dense_steps(dense_len(a, ++b));
+  }
+  const int64_t pair = (at - seq0) / steps, u0 = seq0 + pair * steps;
+  const int w0 = dense_worker(total, workers, u0);
+  if (at == u0 || w0 != w - 1) return;   // no shared pair, or the CTAs of an earlier start have it
+  const int w1 = dense_worker(total, workers, u0 + steps - 1);
+  const int cta = blockIdx.x - w * kCombineCtas;
+  const int r = cta & 1, hw = warp / kCombineWarps, part = warp % kCombineWarps;
+  const int head = (cta >> 1) * kCombineHeads + hw;
+  const int64_t t = 2 * pair + r;
+  if (t >= a.n_q) return;
+  const int64_t row = ((int64_t)b * a.n_q + t) * H + head;
+  const int n = w1 - w0 + 1;
+  auto part_row = [&](int i) {   // partial i of the pair
+    const int slot = 2 * (w0 + i) + (i == 0 && dense_range(total, workers, w0) < u0 ? 1 : 0);
+    return ((int64_t)slot * 2 + r) * H + head;
+  };
+  constexpr int kPer = (kDenseWorkers + 31) / 32;
+  float e[kPer], own = a.own_lse ? a.own_lse[row] : -INFINITY, mx = own;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-    if (mx > -INFINITY) {
-      if (a.own_lse) {
-        const float e = expf(a.own_lse[row] - mx);
-        sum = e;
+  for (int i = 0; i < kPer; ++i) {
+    e[i] = 32 * i + lane < n ? a.part_lse[part_row(32 * i + lane)] : -INFINITY;
+    mx = fmaxf(mx, e[i]);
+  }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = e * a.own_out[row * D + lane * 16 + i];
-      }
-      for (int w = w0; w <= w1; ++w) {
-        const int64_t pr = part_row(w);
-        const float e = expf(a.part_lse[pr] - mx);
-        sum += e;
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = fmaf(e, __half2float(a.part[pr * D + lane * 16 + i]), acc[i]);
+  for (int i = 0; i < kPer; ++i) {
+    e[i] = expf(e[i] - mx);
+    sum += e[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  own = expf(own - mx);
+  sum += own;
+  float acc[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
+  if (part == 0 && a.own_out) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = own * a.own_out[row * D + lane * 16 + i];
+  }
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+#pragma unroll 4
+    for (int i = part; i < 32; i += kCombineWarps) {
+      const float f = __shfl_sync(0xffffffffu, e[j], i);
+      if (32 * j + i < n) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.part + part_row(32 * j + i) * D + lane * 16);
+        const uint4 x = src[0], y = src[1];
+        const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u[k]));
+          acc[2 * k] = fmaf(f, v.x, acc[2 * k]);
+          acc[2 * k + 1] = fmaf(f, v.y, acc[2 * k + 1]);
+        }
       }
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) a.out[row * D + lane * 16 + i] = __float2bfloat16_rn(acc[i] * inv);
-    if (lane == 0 && a.lse) a.lse[row] = sum > 0.0f ? mx + logf(sum) : -INFINITY;
   }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) red[hw][part][i * 32 + lane] = acc[i];
+  __syncthreads();
+  if (part == 0) {
+    const float inv = 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+#pragma unroll
+      for (int p = 1; p < kCombineWarps; ++p) acc[i] += red[hw][p][i * 32 + lane];
+      acc[i] *= inv;
+    }
+    put_row16(a, row, lane, acc);
+    if (lane == 0 && a.lse) a.lse[row] = mx + logf(sum);
+  }
+}
+
+// Every token when the prefix has no entry.
+__global__ void __launch_bounds__(256) dense_rest_kernel(const DenseArgs a) {
+  pdl_wait();
+  const int warps = blockDim.x >> 5;
+  rest_rows(a, 0, (int64_t)a.seqs * a.n_q * H, blockIdx.x * warps + (threadIdx.x >> 5), gridDim.x * warps,
+            threadIdx.x & 31);
 }
 
 }  // namespace
 
-size_t dense_scratch_bytes() {
-  return (size_t)2 * kDenseWorkers * 2 * H * (D * sizeof(__half) + sizeof(float));
+cudaError_t dense_take_error(unsigned int *bits) {
+  unsigned int v = 0, zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error, sizeof(v));
+  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero));
+  *bits = v;
+  return e;
+}
+
+namespace {
+
+// The most workers that can have a range, for up to `tokens` query tokens.
+int64_t dense_workers(int64_t tokens, int64_t n_max) {
+  const int64_t steps = (n_max + kDenseStep - 1) / kDenseStep;
+  return steps == 0 ? 1 : tokens >= kDenseWorkers || steps >= kDenseWorkers || tokens * steps >= kDenseWorkers ? kDenseWorkers : tokens * steps;
+}
+
+}  // namespace
+
+size_t dense_scratch_bytes(int64_t tokens, int64_t n_max) {
+  return (size_t)dense_workers(tokens, n_max) * 2 * 2 * H * (D * sizeof(__half) + sizeof(float));
 }
 
 cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n_vis, int64_t n_max, int64_t cap,
@@ -560,23 +703,30 @@ cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n
   a.seqs = seqs;
   a.n_q = n_q;
   const int64_t most = (int64_t)seqs * ((n_q + 1) / 2) * ((n_max + kDenseStep - 1) / kDenseStep);
-  const int64_t workers = most < num_sms / 2 ? most : num_sms / 2;
-  a.workers = (int32_t)(workers < 1 ? 1 : workers > kDenseWorkers ? kDenseWorkers : workers);
+  int64_t workers = dense_workers((int64_t)seqs * n_q, n_max);
+  workers = workers < most ? workers : most;
+  workers = workers < num_sms / 2 ? workers : num_sms / 2;
+  a.workers = (int32_t)(workers < 1 ? 1 : workers);
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lse = lse;
   a.own_out = own_out;
   a.own_lse = own_lse;
   a.part = static_cast<__half *>(scratch);
-  a.part_lse = reinterpret_cast<float *>(a.part + (size_t)2 * kDenseWorkers * 2 * H * D);
-  cudaError_t e = cudaSuccess;
-  if (most > 0) {
-    e = cudaFuncSetAttribute(dense_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemD);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(dense_attn_kernel, dim3((unsigned)(2 * a.workers)), dim3(kThreadsD), kSmemD, stream, 2u, a);
-    if (e != cudaSuccess) return e;
-    ++*launches;
+  a.part_lse = reinterpret_cast<float *>(a.part + (size_t)2 * a.workers * 2 * H * D);
+  if (most == 0) {
+    const int64_t rows = (int64_t)seqs * n_q * H;
+    const cudaError_t e = launch_pdl(dense_rest_kernel, dim3((unsigned)(rows < 4096 ? (rows + 7) / 8 : 512)), dim3(256), 0,
+                                     stream, 0u, a);
+    if (e == cudaSuccess) ++*launches;
+    return e;
   }
-  e = launch_pdl(dense_combine_kernel, dim3((unsigned)((int64_t)seqs * n_q)), dim3(256), 0, stream, 0u, a);
+  cudaError_t e = cudaFuncSetAttribute(dense_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemD);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(dense_attn_kernel, dim3((unsigned)(2 * a.workers)), dim3(kThreadsD), kSmemD, stream, 2u, a);
+  if (e != cudaSuccess) return e;
+  ++*launches;
+  e = launch_pdl(dense_combine_kernel, dim3((unsigned)(a.workers * kCombineCtas + (n_vis ? kEmptyCtas : 0))),
+                 dim3(kCombineHeads * kCombineWarps * 32), 0, stream, 0u, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

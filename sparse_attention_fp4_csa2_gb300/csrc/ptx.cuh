@@ -151,6 +151,16 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
 
+// The same n times, for a barrier whose phase tells the even CTA of a pair
+// that shared memory of THIS CTA is full: what it guards is read by this
+// CTA's own tensor core (tcgen05.mma of the pair), and the writers' proxy
+// fence has made it visible there, so the release stays at CTA scope.  (At
+// cluster scope it waits for the loads that the SM has in flight: 5.2 ms
+// against 2.7 in the dense readout of 2 x 512 tokens over 16K entries.)
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t addr, uint32_t n) {
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(n) : "memory");
+}
+
 // ------------------------------------------------------------- TMA copies
 // Bulk prefetch of `bytes` (a multiple of 16) at `p` (16-byte aligned) into L2.
 __device__ __forceinline__ void prefetch_l2_bulk(const void *p, uint32_t bytes) {
@@ -192,6 +202,12 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void *p) {
 __device__ __forceinline__ uint32_t ld_nc_u32(const void *p) {
   uint32_t v;
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+
+__device__ __forceinline__ uint32_t ld_nc_u16(const void *p) {
+  uint16_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
 
@@ -380,6 +396,29 @@ __device__ __forceinline__ void mma_f16_pair(uint32_t d_tmem, uint64_t a_desc, u
       : "memory");
 }
 
+// Two products of the same A with different B and D, one after the other: the
+// first keeps A in the tensor core's collector, the second takes it from
+// there (A is read from shared memory once).
+__device__ __forceinline__ void mma_f16_pair_a_fill(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16.collector::a::fill [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void mma_f16_pair_a_last(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                                    uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16.collector::a::lastuse [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
 // Arrive once on `bar` in both CTAs when every tcgen05 operation this thread
 // issued so far has completed.
 __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
@@ -388,6 +427,21 @@ __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
           smem_u32(bar)),
       "h"((uint16_t)3)
       : "memory");
+}
+
+// True in one thread of a converged warp.  A branch on it keeps the operands
+// of the tcgen05 instructions inside in uniform registers; behind a branch on
+// the lane number each of them is moved there one by one (measured, M = 128
+// N = 256 in a CTA pair with a wait and a commit per four: 115 clocks per
+// instruction against 64).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // Shared-memory matrix descriptor (tcgen05): start address, leading / stride

@@ -69,7 +69,7 @@ def test_cross_refusals(c2, change, want):
     (dict(q=ODD), INVALID), (dict(pre=None), INVALID), (dict(pre=ODD), INVALID), (dict(kv=None), INVALID),
     (dict(kv=ODD), INVALID), (dict(cap=0), INVALID), (dict(idx=None), INVALID), (dict(swa=None), INVALID),
     (dict(out=None), INVALID), (dict(out=ODD), INVALID), (dict(ws=None), INVALID), (dict(ws=0x1010), INVALID),
-    (dict(ws_bytes=1 << 20), WORKSPACE), (dict(n_prefix=1 << 40), UNSUPPORTED),
+    (dict(ws_bytes=1 << 19), WORKSPACE), (dict(n_prefix=1 << 40), UNSUPPORTED),
     (dict(params=dict(index_topk=0)), UNSUPPORTED), (dict(params=dict(sliding_window=2000)), UNSUPPORTED)])
 def test_prefix_refusals(c2, change, want):
     a = dict(params={}, batch=2, q=FAKE, pre=FAKE, n_prefix=100, kv=FAKE, cap=600, idx=FAKE, swa=FAKE, scale=FAKE,
@@ -83,7 +83,11 @@ def test_prefix_refusals(c2, change, want):
 
 def test_workspaces(c2):
     p = c2.Params.make()
-    assert c2.workspace_bytes(c2.OP_CROSS, 1, 0, p) == c2.workspace_bytes(c2.OP_CROSS, 5000, 1 << 20, p) > 0
+    # two partials of two tokens (64 rows of 512 fp16 and a log-sum-exp) per
+    # worker: one worker at least, one per 256 entries of a token, 76 at most
+    unit = 2 * 2 * 64 * (512 * 2 + 4)
+    for tokens, n, workers in ((1, 0, 1), (1, 256, 1), (1, 257, 2), (3, 1000, 12), (5000, 1, 76), (1 << 24, 1 << 31, 76)):
+        assert c2.workspace_bytes(c2.OP_CROSS, tokens, n, p) == workers * unit
     one, many = (c2.workspace_bytes(c2.OP_PREFIX, b, 1 << 20, p) for b in (1, 65))
     # 64 sequences more: their own part's fp32 rows and log-sum-exps
     assert many - one == 64 * 64 * (512 + 1) * 4
