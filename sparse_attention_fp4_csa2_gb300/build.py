@@ -22,7 +22,7 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-rdc=true", "-Xcompiler", "-fPIC", "
 
 # units compiled as whole-program device code: ptxas ignores setmaxnreg under
 # separate compilation, and these kernels split their registers between roles
-WHOLE_PROGRAM = {"attention.cu", "dense_attn.cu"}
+WHOLE_PROGRAM = {"attention.cu"}
 
 
 def _nvcc():

@@ -196,6 +196,7 @@ size_t prefill_ws(int32_t batch, int64_t cap, const csa2_params *p) {
 
 constexpr int64_t kMaxCacheRows = (int64_t)1 << 33;     // rows of one call's caches, writes and reads
 constexpr int64_t kMaxDenseTokens = (int64_t)1 << 24;   // query tokens of a dense readout
+constexpr int64_t kMaxDenseLen = ((int64_t)1 << 31) - 512;   // entries that a token sees (32-bit positions)
 
 csa2_status cuda_status(cudaError_t e) { return e == cudaSuccess ? CSA2_OK : CSA2_ERR_CUDA; }
 
@@ -402,8 +403,6 @@ csa2_status csa2_get_device_status(csa2_stream_t stream, uint32_t *bits) {
   if (cudaMemcpyFromSymbol(&v, g_dev_error, sizeof(v)) != cudaSuccess) return CSA2_ERR_CUDA;
   if (v && cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero)) != cudaSuccess) return CSA2_ERR_CUDA;
   if (attn_take_error(&va) != cudaSuccess) return CSA2_ERR_CUDA;   // the readout's own word
-  v |= va;
-  if (dense_take_error(&va) != cudaSuccess) return CSA2_ERR_CUDA;   // the dense readout's
   v |= va;
   if (bits) *bits = v;
   return v ? CSA2_ERR_DEVICE : CSA2_OK;
@@ -727,7 +726,8 @@ extern "C" csa2_status csa2_cross_attn(int32_t batch, int32_t n_q, const void *q
   if (!q || !n_vis || !out || !ws || (n_max > 0 && !kv)) return CSA2_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return CSA2_ERR_INVALID_ARG;
-  if ((int64_t)batch * n_q > kMaxDenseTokens || cap > kMaxCacheRows / batch) return CSA2_ERR_UNSUPPORTED;
+  if ((int64_t)batch * n_q > kMaxDenseTokens || cap > kMaxCacheRows / batch || n_max > kMaxDenseLen)
+    return CSA2_ERR_UNSUPPORTED;
   if (ws_bytes < dense_scratch_bytes((int64_t)batch * n_q, n_max)) return CSA2_ERR_WORKSPACE;
   int launches = 0;
   if (launch_dense_attn(q, kv, n_vis, n_max, cap, batch, n_q, out, lse, nullptr, nullptr, ws, num_sms(),
@@ -748,7 +748,7 @@ extern "C" csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch
   if (!q || !out || !ws || (n_prefix > 0 && !prefix_kv)) return CSA2_ERR_INVALID_ARG;
   if (!aligned16(prefix_kv) || !aligned16(out) || (reinterpret_cast<uintptr_t>(ws) & 255u))
     return CSA2_ERR_INVALID_ARG;
-  if (n_prefix > kMaxCacheRows) return CSA2_ERR_UNSUPPORTED;
+  if (n_prefix > kMaxDenseLen) return CSA2_ERR_UNSUPPORTED;
   const PrefixLayout L = prefix_layout(batch, n_prefix, params);
   if (ws_bytes < L.end) return CSA2_ERR_WORKSPACE;
   uint8_t *wsb = static_cast<uint8_t *>(ws);

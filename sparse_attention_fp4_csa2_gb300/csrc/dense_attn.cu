@@ -27,10 +27,6 @@
 // Every wait is bounded; after one runs out every role falls through its
 // waits, the CTAs meet at the end and the output is undefined
 // (CSA2_DEV_ERR_TIMEOUT).
-//
-// This unit is compiled without relocatable device code, so that ptxas allots
-// each role the registers its setmaxnreg asks for; it keeps its own error word.
-#define CSA2_WHOLE_PROGRAM_TU 1
 #include "dense_plan.cuh"
 
 namespace csa2 {
@@ -39,10 +35,7 @@ namespace {
 
 constexpr int kSoftWarps = 4, kDeqWarps = 8;
 constexpr int kMmaWarpD = kSoftWarps + kDeqWarps;
-constexpr int kThreadsD = (kMmaWarpD + 4) * 32;   // whole warpgroups: setmaxnreg
-// registers: 4 warpgroups launched with 128 a thread
-constexpr uint32_t kRegsSoft = 144, kRegsDeq = 152, kRegsMmaD = 64;
-static_assert(kRegsSoft + 2 * kRegsDeq + kRegsMmaD <= 4 * 128, "register split exceeds the launch budget");
+constexpr int kThreadsD = (kMmaWarpD + 1) * 32;   // 128 registers a thread, no role spills
 constexpr int kSlots = 8;
 constexpr int kSlotBytes = 16384;             // 128 keys x 64 channels, or 32 keys x 256 channels
 constexpr int kQBytesD = H * D * 2;
@@ -87,6 +80,15 @@ __device__ __forceinline__ void st_shared_v4(uint32_t at, uint32_t x, uint32_t y
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+__device__ __forceinline__ float2 half2_floats(uint32_t u) {
+  return __half22float2(*reinterpret_cast<const __half2 *>(&u));
 }
 
 // ---------------------------------------------------------- dequantisation
@@ -151,8 +153,8 @@ __device__ __forceinline__ void convert_q(const DenseArgs &a, const DenseSegment
   __syncwarp();
 }
 
-__device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ring, int w, uint32_t rank, int pt,
-                              int lane) {
+__device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ring, int w, DenseWalk walk,
+                              uint32_t rank, int pt, int lane) {
   const int warp = pt >> 5, key4 = lane >> 3, c8 = lane & 7;
   const int o = c8 >> 1;
   const bool o1 = o & 1, o2 = o & 2;
@@ -160,28 +162,27 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
   const uint32_t k_at = smem_u32(ring) + (uint32_t)(o * kSlotBytes + (16 * warp + key4) * 128) + z;
   const uint32_t v_at = smem_u32(ring) + (uint32_t)(warp * kSlotBytes + o * 4096 + key4 * 128) + z;
   const uint32_t full_at = dsmem_addr(&S.full[0], 0), q_full_at = dsmem_addr(&S.q_full, 0);
-  DenseWalk walk = dense_walk(a, w, lane);
   DenseSegment g;
   uint32_t round = 0;   // 8-slot rounds so far
   uint32_t item = 0;
   DeqRegs kr, vr;
   while (dense_next(a, w, walk, g)) {
     const uint8_t *base = a.kv + (int64_t)g.b * a.cap * ENTRY_BYTES;
-    auto load_piece = [&](DeqRegs &r, int i, int64_t n, int half) {   // channels 256 half + 32 c8 .. of entry n
+    auto load_piece = [&](DeqRegs &r, int i, int n, int half) {   // channels 256 half + 32 c8 .. of entry n
       r.v[i] = make_uint4(0, 0, 0, 0);
       r.sc[i] = 0;
       if (n < g.len) {
-        const uint8_t *e = base + n * ENTRY_BYTES;
+        const uint8_t *e = base + (int64_t)n * ENTRY_BYTES;
         r.v[i] = ld_nc_v4(e + 128 * half + 16 * c8);
         r.sc[i] = ld_nc_u16(e + 256 + 16 * half + 2 * c8);
       }
     };
-    auto load_k = [&](int64_t step) {   // [channel half][4 keys]
+    auto load_k = [&](int step) {   // [channel half][4 keys]
 #pragma unroll
       for (int i = 0; i < 8; ++i)
         load_piece(kr, i, step * kDenseStep + (int)rank * 128 + 16 * warp + 4 * (i & 3) + key4, i >> 2);
     };
-    auto load_v = [&](int64_t step) {   // [4 keys]
+    auto load_v = [&](int step) {   // [4 keys]
 #pragma unroll
       for (int i = 0; i < 8; ++i) load_piece(vr, i, step * kDenseStep + 32 * warp + 4 * i + key4, (int)rank);
     };
@@ -224,7 +225,7 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
     emit_k();
     if (g.s0 + 1 < g.s1) load_k(g.s0 + 1);
 #pragma unroll 1
-    for (int64_t i = g.s0; i < g.s1; ++i) {
+    for (int i = g.s0; i < g.s1; ++i) {
       if (i + 1 < g.s1) {
         emit_k();
         if (i + 2 < g.s1) load_k(i + 2);
@@ -251,7 +252,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
   DenseSegment g;
   uint32_t round = 0, item = 0, n = 0;
   while (dense_next(a, w, walk, g)) {
-    const int64_t steps = g.s1 - g.s0;
+    const int steps = g.s1 - g.s0;
     auto scores = [&](uint32_t tile) {
 #pragma unroll 1
       for (int s = 0; s < kSlots; ++s) {
@@ -270,7 +271,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
     scores(n & 1u);
     if (steps == 1) mma_commit_pair(&S.q_free);
 #pragma unroll 1
-    for (int64_t i = 0; i < steps; ++i, ++n) {
+    for (int i = 0; i < steps; ++i, ++n) {
       if (i + 1 < steps) {
         scores((n + 1) & 1u);
         if (i + 2 == steps) mma_commit_pair(&S.q_free);
@@ -302,13 +303,12 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
 // ----------------------------------------------------------------- softmax
 // Thread tid holds head tid % 64: of S the keys 128 (tid / 64) .. + 127 of a
 // step, of O the channels 256 (tid / 64) .. + 255.
-__device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ps, uint32_t tmem, int w, uint32_t rank, int tid,
-                              int lane, int warp) {
+__device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ps, uint32_t tmem, int w, DenseWalk walk,
+                              uint32_t rank, int tid, int lane, int warp) {
   const uint32_t p_full_at = dsmem_addr(&S.p_full, 0);
   const uint32_t row = tmem + ((uint32_t)(32 * warp) << 16);
   const int h = tid & 63, kh = tid >> 6;
   uint8_t *prow = ps + 2 * kh * kAtomD + h * 128;
-  DenseWalk walk = dense_walk(a, w, lane);
   DenseSegment g;
   {
     DenseWalk peek = walk;
@@ -321,10 +321,10 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
   while (dense_next(a, w, walk, g)) {
     float m = 0.0f, l = 0.0f;
 #pragma unroll 1
-    for (int64_t i = g.s0; i < g.s1; ++i, ++n) {
+    for (int i = g.s0; i < g.s1; ++i, ++n) {
       const uint32_t st = row + (n & 1u) * 128;
-      const int64_t left = g.len - i * kDenseStep;
-      const int valid = (left < kDenseStep ? (int)left : kDenseStep) - 128 * kh;   // of this thread's 128 keys
+      const int left = g.len - i * kDenseStep;
+      const int valid = (left < kDenseStep ? left : kDenseStep) - 128 * kh;   // of this thread's 128 keys
       wait_d(S, &S.s_full[n & 1u], (n >> 1) & 1u);
       tc_fence_after();
       float mx = -INFINITY;
@@ -405,6 +405,7 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
     const float lse = (m - kBias + log2f(l)) * kLn2D;
     wait_d(S, &S.p_free, (n - 1) & 1u);
     tc_fence_after();
+    pdl_wait();   // own_out, own_lse
     const int t = 2 * g.pair + (int)rank;
     if (t >= a.n_q) continue;
     // the weights of this part and of the other part of the softmax
@@ -423,44 +424,51 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
       else if (a.lse)
         a.lse[tok_row + h] = total;
     }
-    // O through the warp's 8 KB of the P buffer, 64 channels at a time, so
-    // that each row leaves in 128-byte pieces
+    // O as 16-bit rows through the warp's 8 KB of the P buffer, 128 channels at
+    // a time, so that every row leaves in 256-byte pieces: bf16 if it is the
+    // output, else (a partial, or this part of the softmax next to the other)
+    // fp16, whose rounding (2^-11 of a value) is below the output's (2^-8)
     uint8_t *stage = ps + warp * 8192;
     const int h0 = 32 * (warp & 1);
+    const bool final_rows = g.whole && !a.own_lse;
+    uint16_t *dst = g.whole ? reinterpret_cast<uint16_t *>(a.out) + (tok_row + h0) * D
+                            : reinterpret_cast<uint16_t *>(a.part) + (((int64_t)g.slot * 2 + rank) * H + h0) * D;
+    const int pc = lane & 15;
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 64) {
+    for (int c = 0; c < 256; c += 128) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
+      for (int e = 0; e < 4; ++e) {
         uint32_t u[32];
         tmem_ld32(row + kColOut + c + 32 * e, u);
         tmem_ld_wait();
+        uint32_t k[16];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-          *reinterpret_cast<float4 *>(stage + lane * 256 + (((8 * e + j) ^ (lane & 7)) << 4)) =
-              make_float4(__uint_as_float(u[4 * j]) * wd, __uint_as_float(u[4 * j + 1]) * wd,
-                          __uint_as_float(u[4 * j + 2]) * wd, __uint_as_float(u[4 * j + 3]) * wd);
+        for (int j = 0; j < 16; ++j) {
+          const float x = __uint_as_float(u[2 * j]) * wd, y = __uint_as_float(u[2 * j + 1]) * wd;
+          k[j] = final_rows ? bf16x2_bits(x, y) : half2_bits(x, y);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint4 *>(stage + lane * 256 + (((4 * e + j) ^ (lane & 7)) << 4)) =
+              make_uint4(k[4 * j], k[4 * j + 1], k[4 * j + 2], k[4 * j + 3]);
       }
       __syncwarp();
-      const int pc = lane & 15;
-#pragma unroll 4
+#pragma unroll 8
       for (int rr = 0; rr < 32; rr += 2) {
         const int r = rr + (lane >> 4);
-        float4 o = *reinterpret_cast<const float4 *>(stage + r * 256 + ((pc ^ (r & 7)) << 4));
-        const int d = 256 * kh + c + 4 * pc;
-        if (g.whole) {
-          const int64_t at = (tok_row + h0 + r) * D + d;
-          if (a.own_lse) {
-            const float x = __shfl_sync(0xffffffffu, wo, r);
-            const float4 y = *reinterpret_cast<const float4 *>(a.own_out + at);
-            o = make_float4(fmaf(x, y.x, o.x), fmaf(x, y.y, o.y), fmaf(x, y.z, o.z), fmaf(x, y.w, o.w));
-          }
-          const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x, o.y), hi = __floats2bfloat162_rn(o.z, o.w);
-          *reinterpret_cast<uint2 *>(a.out + at) =
-              make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
-        } else {
-          const int64_t at = (((int64_t)g.slot * 2 + rank) * H + h0 + r) * D + d;
-          *reinterpret_cast<uint2 *>(a.part + at) = make_uint2(half2_bits(o.x, o.y), half2_bits(o.z, o.w));
+        uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 256 + ((pc ^ (r & 7)) << 4));
+        const int64_t at = (int64_t)r * D + 256 * kh + c + 8 * pc;
+        if (g.whole && a.own_lse) {
+          const float x = __shfl_sync(0xffffffffu, wo, r);
+          const float4 *own = reinterpret_cast<const float4 *>(a.own_out + (tok_row + h0) * D + at);
+          const float4 y = own[0], z = own[1];
+          const float2 f0 = half2_floats(v.x), f1 = half2_floats(v.y), f2 = half2_floats(v.z), f3 = half2_floats(v.w);
+          v = make_uint4(bf16x2_bits(fmaf(x, y.x, f0.x), fmaf(x, y.y, f0.y)),
+                         bf16x2_bits(fmaf(x, y.z, f1.x), fmaf(x, y.w, f1.y)),
+                         bf16x2_bits(fmaf(x, z.x, f2.x), fmaf(x, z.y, f2.y)),
+                         bf16x2_bits(fmaf(x, z.z, f3.x), fmaf(x, z.w, f3.y)));
         }
+        *reinterpret_cast<uint4 *>(dst + at) = v;
       }
       __syncwarp();
     }
@@ -491,7 +499,14 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
     S.abort = 0;
     fence_barrier_init();
   }
-  pdl_wait();   // past here the kernel before this one is complete (programmatic launch)
+  // Past pdl_wait the kernel before this one is complete (programmatic launch).
+  // Behind the sparse readout of the same call (own_lse) nothing but its
+  // results needs that wait, and it has itself waited for everything before
+  // it when it lets this kernel start: the two run side by side, and only the
+  // segments' ends wait.  (Their CTAs cannot share an SM, whose shared memory
+  // each of them fills, so neither can they share its tensor memory.)
+  if (!a.own_lse) pdl_wait();
+  const DenseWalk walk = dense_walk(a, w, lane);
   __syncthreads();
   if (warp == kMmaWarpD) {
     tmem_alloc_pair(&S.tmem_base, 512);
@@ -504,15 +519,11 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
   const uint32_t tmem = S.tmem_base;
 
   if (warp < kSoftWarps) {
-    setmaxnreg_inc<kRegsSoft>();
-    dense_softmax(a, S, qs, ps, tmem, w, rank, tid, lane, warp);
+    dense_softmax(a, S, qs, ps, tmem, w, walk, rank, tid, lane, warp);
   } else if (warp < kMmaWarpD) {
-    setmaxnreg_inc<kRegsDeq>();
-    dense_dequant(a, S, qs, ring, w, rank, tid - kSoftWarps * 32, lane);
+    dense_dequant(a, S, qs, ring, w, walk, rank, tid - kSoftWarps * 32, lane);
   } else {
-    setmaxnreg_dec<kRegsMmaD>();
-    const DenseWalk walk = dense_walk(a, w, lane);
-    if (rank == 0 && warp == kMmaWarpD && elect_one()) dense_products(a, S, qs, ps, ring, tmem, w, walk);
+    if (rank == 0 && elect_one()) dense_products(a, S, qs, ps, ring, tmem, w, walk);
     __syncwarp();
   }
   tc_fence_before();
@@ -527,23 +538,23 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
 
 // Merges the pairs that several workers share, with the weights exp(lse_i -
 // lse), lse the log-sum-exp over all their partials (and the other part of the
-// softmax).  Only a pair across a range's start is shared, so there are at
-// most workers - 1: the CTAs of worker w's start take the pair if that is its
-// first such start, for one token and two heads each; four warps per head
-// take every fourth partial.  Partials are normalised fp16 rows, within the
-// entries' +-2688; their rounding (2^-11 of a value) is below the output's
-// (2^-8).  The CTAs past those write the sequences without entries.
-constexpr int kCombineHeads = 2, kCombineWarps = 4;
-constexpr int kCombineCtas = 2 * (H / kCombineHeads);   // per worker
+// softmax).  kByPair (fewer pairs than workers): kCtas CTAs for each pair.
+// Otherwise at most one pair lies across each range's start: kCtas CTAs for
+// each worker take the pair across its start, if that is the pair's first.  A
+// CTA takes kHeads heads of one token, kWarps warps per head, each every
+// kWarps-th partial: eight warps where a pair has many partials, one where it
+// has two or three.  The CTAs past those write the sequences without entries.
+template <bool kByPair>
+struct Combine {
+  static constexpr int kHeads = kByPair ? 1 : 8, kWarps = kByPair ? 8 : 1;
+  static constexpr int kCtas = 2 * (H / kHeads);
+};
 constexpr int kEmptyCtas = 64;
 
 __device__ __forceinline__ void put_row16(const DenseArgs &a, int64_t row, int lane, const float (&o)[16]) {
   uint32_t u[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-    u[i] = *reinterpret_cast<const uint32_t *>(&v);
-  }
+  for (int i = 0; i < 8; ++i) u[i] = bf16x2_bits(o[2 * i], o[2 * i + 1]);
   uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * D + lane * 16);
   dst[0] = make_uint4(u[0], u[1], u[2], u[3]);
   dst[1] = make_uint4(u[4], u[5], u[6], u[7]);
@@ -560,45 +571,56 @@ __device__ __forceinline__ void rest_rows(const DenseArgs &a, int64_t row0, int6
   }
 }
 
-__global__ void __launch_bounds__(kCombineHeads * kCombineWarps * 32) dense_combine_kernel(const DenseArgs a) {
-  __shared__ float red[kCombineHeads][kCombineWarps][D];
+template <bool kByPair>
+__global__ void __launch_bounds__(256) dense_combine_kernel(const DenseArgs a) {
+  using C = Combine<kByPair>;
+  __shared__ float red[kByPair ? C::kWarps : 1][D];
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int64_t before, total;
-  int workers;
-  dense_units(a, 0, lane, before, total, workers);
-  const int w = blockIdx.x / kCombineCtas;
-  if (w >= a.workers) {
-    const int warps = blockDim.x >> 5, ctas = gridDim.x - a.workers * kCombineCtas;
-    const int me = (blockIdx.x - a.workers * kCombineCtas) * warps + warp;
+  const int64_t pairs = (a.n_q + 1) / 2;
+  const int groups = kByPair ? (int)(a.seqs * pairs) : a.workers;
+  const int group = blockIdx.x / C::kCtas, cta = blockIdx.x - group * C::kCtas;
+  if (group >= groups) {
+    const int ctas = gridDim.x - groups * C::kCtas, me = (blockIdx.x - groups * C::kCtas) * 8 + warp;
     for (int b = 0; b < a.seqs; ++b)
-      if (dense_len(a, b) == 0) rest_rows(a, (int64_t)b * a.n_q * H, (int64_t)a.n_q * H, me, ctas * warps, lane);
+      if (dense_len(a, b) == 0) rest_rows(a, (int64_t)b * a.n_q * H, (int64_t)a.n_q * H, me, ctas * 8, lane);
     return;
   }
-  if (w == 0 || w >= workers) return;
-  // the pair that holds the range's first unit
-  const int64_t at = dense_range(total, workers, w), pairs = (a.n_q + 1) / 2;
-  int b = 0;
-  int64_t seq0 = 0, steps = dense_steps(dense_len(a, 0));
-  while (at >= seq0 + pairs * steps) {
-    seq0 += pairs * steps;
-    steps = dense_steps(dense_len(a, ++b));
+  // the pair, its first unit and its steps
+  int b = kByPair ? (int)(group / pairs) : 0;
+  int64_t before, total, pair, u0;
+  int workers, steps;
+  dense_units(a, b, lane, before, total, workers);
+  if (kByPair) {
+    pair = group - b * pairs;
+    steps = dense_steps(dense_len(a, b));
+    if (steps == 0) return;
+    u0 = before + pair * steps;
+  } else {
+    if (group == 0 || group >= workers) return;
+    const int64_t at = dense_range(total, workers, group);
+    steps = dense_steps(dense_len(a, 0));
+    while (at >= before + pairs * steps) {
+      before += pairs * steps;
+      steps = dense_steps(dense_len(a, ++b));
+    }
+    pair = (at - before) / steps;
+    u0 = before + pair * steps;
+    if (at == u0) return;   // no pair lies across this start
   }
-  const int64_t pair = (at - seq0) / steps, u0 = seq0 + pair * steps;
   const int w0 = dense_worker(total, workers, u0);
-  if (at == u0 || w0 != w - 1) return;   // no shared pair, or the CTAs of an earlier start have it
-  const int w1 = dense_worker(total, workers, u0 + steps - 1);
-  const int cta = blockIdx.x - w * kCombineCtas;
-  const int r = cta & 1, hw = warp / kCombineWarps, part = warp % kCombineWarps;
-  const int head = (cta >> 1) * kCombineHeads + hw;
+  const int n = dense_worker(total, workers, u0 + steps - 1) - w0 + 1;   // partials
+  if (n == 1 || (!kByPair && w0 != group - 1)) return;   // finished by its worker; an earlier start's
+  const int r = cta & 1, hw = warp / C::kWarps, part = warp % C::kWarps;
+  const int head = (cta >> 1) * C::kHeads + hw;
   const int64_t t = 2 * pair + r;
   if (t >= a.n_q) return;
   const int64_t row = ((int64_t)b * a.n_q + t) * H + head;
-  const int n = w1 - w0 + 1;
-  auto part_row = [&](int i) {   // partial i of the pair
-    const int slot = 2 * (w0 + i) + (i == 0 && dense_range(total, workers, w0) < u0 ? 1 : 0);
-    return ((int64_t)slot * 2 + r) * H + head;
-  };
+  // partial i's row: slot 2 (w0 + i), but the first one's is odd where the
+  // pair starts inside the range
+  const int64_t row0 = ((int64_t)4 * w0 + r) * H + head;
+  const int64_t odd = dense_range(total, workers, w0) < u0 ? 2 * H : 0;
+  auto part_row = [&](int i) { return row0 + (int64_t)i * (4 * H) + (i == 0 ? odd : 0); };
   constexpr int kPer = (kDenseWorkers + 31) / 32;
   float e[kPer], own = a.own_lse ? a.own_lse[row] : -INFINITY, mx = own;
 #pragma unroll
@@ -622,41 +644,69 @@ __global__ void __launch_bounds__(kCombineHeads * kCombineWarps * 32) dense_comb
 #pragma unroll
   for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
   if (part == 0 && a.own_out) {
+    const float4 *src = reinterpret_cast<const float4 *>(a.own_out + row * D + lane * 16);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) acc[i] = own * a.own_out[row * D + lane * 16 + i];
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = src[i];
+      acc[4 * i] = own * v.x;
+      acc[4 * i + 1] = own * v.y;
+      acc[4 * i + 2] = own * v.z;
+      acc[4 * i + 3] = own * v.w;
+    }
   }
+#pragma unroll 1
+  for (int i0 = part; i0 < n; i0 += 4 * C::kWarps) {   // four partials in flight
+    uint4 v[4][2];
+    float f[4];
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-#pragma unroll 4
-    for (int i = part; i < 32; i += kCombineWarps) {
-      const float f = __shfl_sync(0xffffffffu, e[j], i);
-      if (32 * j + i < n) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.part + part_row(32 * j + i) * D + lane * 16);
-        const uint4 x = src[0], y = src[1];
-        const uint32_t u[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * C::kWarps;
+      v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+      if (i < n) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.part + part_row(i) * D + lane * 16);
+        v[k][0] = src[0];
+        v[k][1] = src[1];
+      }
+      f[k] = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&u[k]));
-          acc[2 * k] = fmaf(f, v.x, acc[2 * k]);
-          acc[2 * k + 1] = fmaf(f, v.y, acc[2 * k + 1]);
-        }
+      for (int j = 0; j < kPer; ++j) {
+        const float x = __shfl_sync(0xffffffffu, e[j], i & 31);
+        if (i >> 5 == j) f[k] = x;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t u[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 x = half2_floats(u[j]);
+        acc[2 * j] = fmaf(f[k], x.x, acc[2 * j]);
+        acc[2 * j + 1] = fmaf(f[k], x.y, acc[2 * j + 1]);
       }
     }
   }
+  const float inv = 1.0f / sum;
+  if constexpr (kByPair) {
+    // thread (part, lane) adds up channels 2 tid, 2 tid + 1 over the warps
 #pragma unroll
-  for (int i = 0; i < 16; ++i) red[hw][part][i * 32 + lane] = acc[i];
-  __syncthreads();
-  if (part == 0) {
-    const float inv = 1.0f / sum;
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4 *>(&red[part][lane * 16 + 4 * i]) =
+          make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    __syncthreads();
+    float x = 0.0f, y = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-#pragma unroll
-      for (int p = 1; p < kCombineWarps; ++p) acc[i] += red[hw][p][i * 32 + lane];
-      acc[i] *= inv;
+    for (int p = 0; p < C::kWarps; ++p) {
+      const float2 v = *reinterpret_cast<const float2 *>(&red[p][2 * tid]);
+      x += v.x;
+      y += v.y;
     }
+    reinterpret_cast<uint32_t *>(a.out + row * D)[tid] = bf16x2_bits(x * inv, y * inv);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] *= inv;
     put_row16(a, row, lane, acc);
-    if (lane == 0 && a.lse) a.lse[row] = mx + logf(sum);
   }
+  if (part == 0 && lane == 0 && a.lse) a.lse[row] = mx + logf(sum);
 }
 
 // Every token when the prefix has no entry.
@@ -668,14 +718,6 @@ __global__ void __launch_bounds__(256) dense_rest_kernel(const DenseArgs a) {
 }
 
 }  // namespace
-
-cudaError_t dense_take_error(unsigned int *bits) {
-  unsigned int v = 0, zero = 0;
-  cudaError_t e = cudaMemcpyFromSymbol(&v, g_dev_error, sizeof(v));
-  if (e == cudaSuccess && v) e = cudaMemcpyToSymbol(g_dev_error, &zero, sizeof(zero));
-  *bits = v;
-  return e;
-}
 
 namespace {
 
@@ -698,7 +740,7 @@ cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.kv = kv;
   a.n_vis = n_vis;
-  a.n_max = n_max;
+  a.n_max = (int32_t)n_max;
   a.cap = cap;
   a.seqs = seqs;
   a.n_q = n_q;
@@ -725,8 +767,12 @@ cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n
   e = launch_pdl(dense_attn_kernel, dim3((unsigned)(2 * a.workers)), dim3(kThreadsD), kSmemD, stream, 2u, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  e = launch_pdl(dense_combine_kernel, dim3((unsigned)(a.workers * kCombineCtas + (n_vis ? kEmptyCtas : 0))),
-                 dim3(kCombineHeads * kCombineWarps * 32), 0, stream, 0u, a);
+  const int64_t pairs = (int64_t)seqs * ((n_q + 1) / 2);
+  const unsigned empty = n_vis ? kEmptyCtas : 0;
+  e = pairs < a.workers ? launch_pdl(dense_combine_kernel<true>, dim3((unsigned)pairs * Combine<true>::kCtas + empty),
+                                     dim3(256), 0, stream, 0u, a)
+                        : launch_pdl(dense_combine_kernel<false>, dim3((unsigned)a.workers * Combine<false>::kCtas + empty),
+                                     dim3(256), 0, stream, 0u, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -21,7 +21,8 @@ struct DenseArgs {
   const __nv_bfloat16 *q;      // [seqs][n_q][64][512]
   const uint8_t *kv;           // [seqs][cap][288]
   const int32_t *n_vis;        // [seqs], or NULL: n_max entries each
-  int64_t n_max, cap;
+  int64_t cap;
+  int32_t n_max;
   int32_t seqs, n_q;
   int32_t workers;
   __nv_bfloat16 *out;          // [seqs][n_q][64][512]
@@ -32,14 +33,14 @@ struct DenseArgs {
   float *part_lse;             // [2 workers][2 tokens][64] their natural log-sum-exps
 };
 
-__device__ __forceinline__ int64_t dense_len(const DenseArgs &a, int b) {
+__device__ __forceinline__ int dense_len(const DenseArgs &a, int b) {
   if (!a.n_vis) return a.n_max;
-  const int64_t n = __ldg(a.n_vis + b);
+  const int n = __ldg(a.n_vis + b);
   if (n < 0 || n > a.n_max) set_error(CSA2_DEV_ERR_NVIS);
   return n < 0 ? 0 : n > a.n_max ? a.n_max : n;
 }
 
-__device__ __forceinline__ int64_t dense_steps(int64_t n) { return (n + kDenseStep - 1) / kDenseStep; }
+__device__ __forceinline__ int dense_steps(int n) { return n / kDenseStep + (n % kDenseStep ? 1 : 0); }
 
 // Units of sequences [0, b) and of all sequences, and how many workers have
 // a range (a.workers, but no more than there are units: no range is empty);
@@ -48,14 +49,14 @@ __device__ __forceinline__ void dense_units(const DenseArgs &a, int b, int lane,
                                             int &workers) {
   const int64_t pairs = (a.n_q + 1) / 2;
   if (!a.n_vis) {
-    before = b * pairs * dense_steps(a.n_max);
-    total = a.seqs * pairs * dense_steps(a.n_max);
+    before = (int64_t)b * pairs * dense_steps(a.n_max);
+    total = (int64_t)a.seqs * pairs * dense_steps(a.n_max);
     workers = (int)(total < a.workers ? total : a.workers);
     return;
   }
   int64_t x = 0, y = 0;
   for (int i = lane; i < a.seqs; i += 32) {
-    const int64_t s = dense_steps(dense_len(a, i));
+    const int s = dense_steps(dense_len(a, i));
     y += s;
     if (i < b) x += s;
   }
@@ -83,14 +84,13 @@ struct DenseWalk {
   int64_t at, end;        // the unit that comes next, the range's end
   int64_t start;          // the range's first unit
   int64_t seq0;           // first unit of sequence b
-  int b;
-  int64_t len, steps;     // of sequence b
+  int b, len, steps;      // the sequence, its entries and steps
 };
 
 struct DenseSegment {
   int b, pair;
-  int64_t len;            // entries of the sequence
-  int64_t s0, s1;         // steps [s0, s1) of the pair
+  int len;                // entries of the sequence
+  int s0, s1;             // steps [s0, s1) of the pair
   bool whole;             // every step of the pair
   int slot;               // partial slot otherwise
 };
@@ -123,9 +123,9 @@ __device__ __forceinline__ bool dense_next(const DenseArgs &a, int w, DenseWalk 
   g.b = k.b;
   g.pair = (int)(rel / k.steps);
   g.len = k.len;
-  g.s0 = rel - (int64_t)g.pair * k.steps;
-  const int64_t left = k.steps - g.s0;
-  g.s1 = g.s0 + (left < k.end - k.at ? left : k.end - k.at);
+  g.s0 = (int)(rel - (int64_t)g.pair * k.steps);
+  const int64_t left = k.end - k.at;
+  g.s1 = left < k.steps - g.s0 ? g.s0 + (int)left : k.steps;
   g.whole = g.s0 == 0 && g.s1 == k.steps;
   g.slot = 2 * w + (k.at == k.start ? 0 : 1);
   k.at += g.s1 - g.s0;

@@ -243,10 +243,8 @@ cudaError_t launch_indexer_k_read(const uint8_t *k_fp4, int64_t batch, int64_t c
 // Dense readout of seqs x n_q tokens over the first n_vis[b] (NULL: n_max)
 // entries of their sequence, merged with own_out / own_lse (fp32 rows and
 // log-sum-exps of another part of each token's softmax) unless NULL.
-// Scratch for up to `tokens` query tokens over up to n_max entries each; the
-// unit's own device error word, read and cleared.
+// Scratch for up to `tokens` query tokens over up to n_max entries each.
 size_t dense_scratch_bytes(int64_t tokens, int64_t n_max);
-cudaError_t dense_take_error(unsigned int *bits);
 cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n_vis, int64_t n_max, int64_t cap,
                               int32_t seqs, int32_t n_q, void *out, float *lse, const float *own_out,
                               const float *own_lse, void *scratch, int num_sms, cudaStream_t stream, int *launches);
