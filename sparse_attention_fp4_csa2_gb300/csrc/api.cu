@@ -730,7 +730,7 @@ extern "C" csa2_status csa2_cross_attn(int32_t batch, int32_t n_q, const void *q
     return CSA2_ERR_UNSUPPORTED;
   if (ws_bytes < dense_scratch_bytes((int64_t)batch * n_q, n_max)) return CSA2_ERR_WORKSPACE;
   int launches = 0;
-  if (launch_dense_attn(q, kv, n_vis, n_max, cap, batch, n_q, out, lse, nullptr, nullptr, ws, num_sms(),
+  if (launch_dense_attn(q, kv, n_vis, n_max, cap, batch, n_q, out, lse, nullptr, nullptr, 0, ws, num_sms(),
                         reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
     return CSA2_ERR_CUDA;
   g_last_launches = launches;
@@ -760,6 +760,7 @@ extern "C" csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch
                                  wsb + L.attn_off, ws_bytes - L.attn_off, st, &launches);
   if (s != CSA2_OK) return s;
   if (launch_dense_attn(q, prefix_kv, nullptr, n_prefix, n_prefix, 1, batch, out, lse, own_out, own_lse,
+                        attn_ctas(batch, params->index_topk, params->sliding_window, params->attn_kernel),
                         wsb + L.part_off, num_sms(), st, &launches) != cudaSuccess)
     return CSA2_ERR_CUDA;
   g_last_launches = launches;

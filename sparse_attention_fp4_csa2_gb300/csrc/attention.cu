@@ -1056,6 +1056,12 @@ size_t attn_scratch_bytes(int32_t problems, int32_t K, int32_t W, int32_t kernel
   return 256;   // the chunks of a token combine through distributed shared memory
 }
 
+int attn_ctas(int32_t problems, int32_t K, int32_t W, int32_t kernel) {
+  const int sms = device_sms();
+  const int64_t ctas = (int64_t)problems * choose_chunks(problems, K, W, kernel, sms);
+  return (int)(ctas < sms ? ctas : sms);
+}
+
 cudaError_t launch_sparse_attn(AttnArgs a, void *scratch, cudaStream_t stream, int *launches) {
   if (a.problems <= 0) return cudaSuccess;
   const int sms = device_sms();

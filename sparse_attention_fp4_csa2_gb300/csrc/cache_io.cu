@@ -47,10 +47,23 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
   return r;
 }
 
-// Lane l owns channels 16 l .. + 15: it loads 32 bytes, rotates them if they
-// are RoPE channels (lane j evaluates frequency j; products and sums rounded
-// separately), and stores 16 bytes of codes.  One warp per block for a decode
-// step's few rows, so that they spread over the SMs.
+// x / s by the reciprocal r = fl(1 / s) and one correction with the exact
+// remainder (P. Markstein, "Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): the correctly rounded quotient, unless
+// it lies within 2^-46 of the middle of two floats.  s, r normal.
+__device__ __forceinline__ float quotient(float x, float s, float r) {
+  const float q = x * r;
+  return fmaf(fmaf(-q, s, x), r, q);
+}
+
+// A warp writes R rows, one after the other, all loads first.  Lane l owns
+// channels 16 l .. + 15: it loads 32 bytes, rotates them if they are RoPE
+// channels (lane j evaluates frequency j; products and sums rounded
+// separately), and stores 16 bytes of codes.  What bounds it is instruction
+// issue and the loads' latency, not HBM (32,768 rows: 50 MB, 7.5 us at the
+// copy rate): one rounded division per channel alone was a third of the
+// instructions.
+template <int R>
 __global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat16 *__restrict__ latent, int64_t n,
                                                               const int64_t *__restrict__ pos,
                                                               const int64_t *__restrict__ slot,
@@ -58,53 +71,81 @@ __global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat1
                                                               int64_t rows, const RopeTurns turns) {
   pdl_wait();   // the inputs' producer is complete past here (programmatic launch)
   const int lane = threadIdx.x & 31;
-  const int64_t e = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (e >= n) return;
-  const int64_t row = slot[e];
-  const int64_t p = pos ? pos[e] : 0;
-  if (row < 0 || row >= rows || p < 0 || p >= kMaxRopePos) {
-    if (lane == 0) set_error(CSA2_DEV_ERR_INDEX);
-    return;
-  }
-  const uint4 *src = reinterpret_cast<const uint4 *>(latent + e * D + lane * 16);
-  const uint4 u0 = __ldg(src), u1 = __ldg(src + 1);
-  const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-  float x[16];
+  const int64_t e0 = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * R;
+  uint4 u[R][2];
+  int64_t row[R], p[R];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-  if (pos) {
-    float cj, sj;
-    rope_cos_sin(turns.step[lane], p, cj, sj);
-    const int jbase = (lane - (D - ROPE_DIM) / 16) * 8;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int from = (jbase + i) & 31;
-      const float c = __shfl_sync(0xffffffffu, cj, from);
-      const float s = __shfl_sync(0xffffffffu, sj, from);
-      if (lane >= (D - ROPE_DIM) / 16) {
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-        x[2 * i + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
-      }
+  for (int r = 0; r < R; ++r) {
+    row[r] = -1;
+    p[r] = 0;
+    if (e0 + r < n) {
+      const uint4 *src = reinterpret_cast<const uint4 *>(latent + (e0 + r) * D + lane * 16);
+      u[r][0] = ld_nc_v4(src);
+      u[r][1] = ld_nc_v4(src + 1);
+      row[r] = __ldg(slot + e0 + r);
+      if (pos) p[r] = __ldg(pos + e0 + r);
     }
   }
-  float amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+  for (int r = 0; r < R; ++r) {
+    if (e0 + r >= n) return;
+    if (row[r] < 0 || row[r] >= rows || p[r] < 0 || p[r] >= kMaxRopePos) {
+      if (lane == 0) set_error(CSA2_DEV_ERR_INDEX);
+      continue;
+    }
+    const uint32_t w[8] = {u[r][0].x, u[r][0].y, u[r][0].z, u[r][0].w, u[r][1].x, u[r][1].y, u[r][1].z, u[r][1].w};
+    float x[16];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float scale = __fdiv_rn(amax, 448.0f);
-  uint32_t q[4] = {0, 0, 0, 0};
-  if (scale > 0.0f) {
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    if (pos) {
+      float cj, sj;
+      rope_cos_sin(turns.step[lane], p[r], cj, sj);
+      const int jbase = (lane - (D - ROPE_DIM) / 16) * 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      q[i >> 1] |= cvt_e4m3x2(__fdiv_rn(x[2 * i + 1], scale), __fdiv_rn(x[2 * i], scale)) << (16 * (i & 1));
+      for (int i = 0; i < 8; ++i) {
+        const int from = (jbase + i) & 31;
+        const float c = __shfl_sync(0xffffffffu, cj, from);
+        const float s = __shfl_sync(0xffffffffu, sj, from);
+        if (lane >= (D - ROPE_DIM) / 16) {
+          const float a = x[2 * i], b = x[2 * i + 1];
+          x[2 * i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+          x[2 * i + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+        }
+      }
+    }
+    float amax = 0.0f;   // NaNs do not count
+#pragma unroll
+    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    const float scale = __fdiv_rn(amax, 448.0f);
+    uint32_t q[4] = {0, 0, 0, 0};
+    if (scale >= 0x1p-100f && scale <= 0x1p+100f) {
+      const float inv = __frcp_rn(scale);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        q[i >> 1] |= cvt_e4m3x2(quotient(x[2 * i + 1], scale, inv), quotient(x[2 * i], scale, inv)) << (16 * (i & 1));
+    } else if (scale > 0.0f) {
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        float lo = 0.0f, hi = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j == i) {
+            lo = x[2 * j];
+            hi = x[2 * j + 1];
+          }
+        const uint32_t c = cvt_e4m3x2(__fdiv_rn(hi, scale), __fdiv_rn(lo, scale)) << (16 * (i & 1));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (j == i >> 1) q[j] |= c;
+      }
+    }
+    *reinterpret_cast<uint4 *>(swa + row[r] * D + lane * 16) = make_uint4(q[0], q[1], q[2], q[3]);
+    if (lane == 0) swa_scale[row[r]] = scale;
   }
-  *reinterpret_cast<uint4 *>(swa + row * D + lane * 16) = make_uint4(q[0], q[1], q[2], q[3]);
-  if (lane == 0) swa_scale[row] = scale;
 }
 
 __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
@@ -133,6 +174,15 @@ struct ReadArgs {
   int64_t cap, total;      // rows per sequence, batch * k
   int64_t k;
 };
+
+// (sequence, place) of output row i.
+__device__ __forceinline__ void locate(const ReadArgs &a, int64_t i, int64_t &b, int64_t &j) {
+  if (a.total >> 32)
+    b = i / a.k;
+  else
+    b = (uint32_t)i / (uint32_t)a.k;   // a 64-bit division is four times the instructions
+  j = i - b * a.k;
+}
 
 // One output piece of 8 channels: its codes and its scale.
 struct Piece {
@@ -187,21 +237,22 @@ __global__ void __launch_bounds__(256) cache_read_kernel(const ReadArgs a) {
   const int piece = FMT == kFmtIk ? lane & 15 : lane;
   const int64_t first = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * (R * kRows) + sub;
   if (first - sub >= a.total) return;
-  int64_t row[R];
+  int64_t row[R], b, j;
   Piece p[R][kHalves];
+  locate(a, first, b, j);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int64_t i = first + r * kRows;
     row[r] = -1;
     if (i < a.total) {
-      const int64_t b = i / a.k;
-      const int64_t id = a.idx ? (int64_t)__ldg(a.idx + i) : i - b * a.k;
+      const int64_t id = a.idx ? (int64_t)__ldg(a.idx + i) : j;
       if (id >= a.cap) {
         if (piece == 0) set_error(CSA2_DEV_ERR_INDEX);
       } else if (id >= 0) {
         row[r] = b * a.cap + id;
       }
     }
+    for (j += kRows; j >= a.k; j -= a.k) ++b;
   }
 #pragma unroll
   for (int r = 0; r < R; ++r)
@@ -234,10 +285,12 @@ cudaError_t launch_read(const ReadArgs &a, cudaStream_t stream) {
 
 cudaError_t launch_swa_quant_write(const void *latent, int64_t n, const int64_t *pos, const int64_t *slot, uint8_t *swa,
                                    float *swa_scale, int64_t rows, float rope_theta, cudaStream_t stream) {
-  // 1 / (2 pi) = 0x0.28BE60DB9391054A7F09D5F47D4D3770... (binary expansion)
-  constexpr uint64_t kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;
-  RopeTurns turns = {};
-  if (pos) {
+  // the frequencies of the last theta of this host thread (32 powers: 4 us)
+  thread_local RopeTurns turns = {};
+  thread_local float theta = 0.0f;
+  if (pos && theta != rope_theta) {
+    // 1 / (2 pi) = 0x0.28BE60DB9391054A7F09D5F47D4D3770... (binary expansion)
+    constexpr uint64_t kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;
     for (int j = 0; j < ROPE_DIM / 2; ++j) {
       const float inv = (float)std::pow((double)rope_theta, -(2.0 * j) / (double)ROPE_DIM);
       int ex;
@@ -247,11 +300,15 @@ cudaError_t launch_swa_quant_write(const void *latent, int64_t n, const int64_t 
       const int sh = 24 - ex;
       turns.step[j] = sh >= 128 ? 0 : (uint64_t)(prod >> sh);
     }
+    theta = rope_theta;
   }
-  const int warps = n <= 1024 ? 1 : 8;
-  const int64_t blocks = (n + warps - 1) / warps;
-  return launch_pdl(swa_quant_write_kernel, dim3((unsigned)blocks), dim3(warps * 32), 0, stream, 0u,
-                    static_cast<const __nv_bfloat16 *>(latent), n, pos, slot, swa, swa_scale, rows, turns);
+  const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(latent);
+  // a decode step's few rows: one warp per block, so that they spread over the SMs
+  if (n <= 1024)
+    return launch_pdl(swa_quant_write_kernel<1>, dim3((unsigned)n), dim3(32), 0, stream, 0u, src, n, pos, slot, swa,
+                      swa_scale, rows, turns);
+  return launch_pdl(swa_quant_write_kernel<2>, dim3((unsigned)((n + 15) / 16)), dim3(256), 0, stream, 0u, src, n, pos,
+                    slot, swa, swa_scale, rows, turns);
 }
 
 cudaError_t launch_kv_read(const uint8_t *kv, int64_t batch, int64_t cap, const int32_t *idx, int64_t k, void *out,

@@ -20,7 +20,10 @@
 //
 // Warps of a CTA: 0-3 softmax (one thread per tensor-memory lane: a head and
 // half of the step's keys), 4-11 dequantisation (entries loaded into registers
-// a step ahead), 12 the products (in the even CTA).  The products' order is
+// a step ahead), 12 the products (in the even CTA) and the
+// copies of Q, which start as soon as the last product with the Q before is
+// done.  The first loads are sent before the CTA pair's set-up is awaited.
+// The products' order is
 //   S(0), S(1), O(0), S(2), O(1), ...
 // so that the softmax of one step runs beside the next step's first product.
 //
@@ -35,7 +38,7 @@ namespace {
 
 constexpr int kSoftWarps = 4, kDeqWarps = 8;
 constexpr int kMmaWarpD = kSoftWarps + kDeqWarps;
-constexpr int kThreadsD = (kMmaWarpD + 1) * 32;   // 128 registers a thread, no role spills
+constexpr int kThreadsD = (kMmaWarpD + 1) * 32;   // 128 registers a thread
 constexpr int kSlots = 8;
 constexpr int kSlotBytes = 16384;             // 128 keys x 64 channels, or 32 keys x 256 channels
 constexpr int kQBytesD = H * D * 2;
@@ -53,7 +56,7 @@ constexpr uint32_t kIdescO = idesc_f16(0, 0, /*B MN-major*/ 1, 256, 128);
 
 struct __align__(16) CtlD {
   uint64_t full[kSlots], free[kSlots];        // full, q_full, p_full: both CTAs arrive at the even CTA
-  uint64_t q_full, q_free, s_full[2], p_full, p_free, done;
+  uint64_t q_raw, q_full, q_free, s_full[2], p_full, p_free, done;
   uint32_t tmem_base;
   volatile uint32_t abort;
   float red[2][128];
@@ -128,110 +131,143 @@ __device__ __forceinline__ void put32(uint32_t at, const uint4 &v, uint32_t sc, 
   }
 }
 
-// Q of a token, bf16 -> fp16 (zeros for the missing token of an odd count).
-template <int T>
-__device__ __forceinline__ void convert_q(const DenseArgs &a, const DenseSegment &g, uint32_t rank, uint8_t *qs, int i0) {
+// Waits until both CTAs of the pair have set up their barriers and tensor
+// memory (each thread once).
+__device__ __forceinline__ uint32_t pair_ready(const CtlD &S) {
+  tc_fence_before();
+  bar_named(2, kThreadsD);
+  cluster_sync();
+  tc_fence_after();
+  return S.tmem_base;
+}
+
+// Q of this CTA's token of a segment: eight boxes of [64 heads][64 channels],
+// bf16, each a 128B-swizzled column of the Q region; completes q_raw.
+__device__ __forceinline__ void load_q(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, uint8_t *qs,
+                                       const DenseSegment &g, uint32_t rank) {
   const int t = 2 * g.pair + (int)rank;
-  const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((int64_t)g.b * a.n_q + t) * (H * D));
+  if (t >= a.n_q) {   // the missing token of an odd count: zeros, written by convert_q
+    mbar_arrive(&S.q_raw);
+    return;
+  }
+  mbar_arrive_expect_tx(&S.q_raw, (uint32_t)kQBytesD);
+  const int32_t y = (int32_t)(((int64_t)g.b * a.n_q + t) * H);
 #pragma unroll 1
-  for (; i0 < H * D / 8; i0 += T * 8) {
-    uint4 u[8];
+  for (int c = 0; c < 8; ++c) tma_load_2d(qs + c * kAtomD, &tm_q, 64 * c, y, &S.q_raw);
+}
+
+// Q in place from bf16 to fp16 (two-byte slots of the same layout), by
+// kThreads threads.
+template <int kThreads>
+__device__ __forceinline__ void convert_q(const DenseArgs &a, const DenseSegment &g, uint32_t rank, uint8_t *qs, int t) {
+  const bool zero = 2 * g.pair + (int)rank >= a.n_q;
+  uint4 *q = reinterpret_cast<uint4 *>(qs);
+#pragma unroll 4
+  for (int i = t; i < kQBytesD / 16; i += kThreads) {
+    const uint4 v = q[i];
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) u[i] = t < a.n_q ? ld_nc_v4(src + i0 + i * T) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = i0 + i * T, r = at >> 6, c = at & 63;
-      const uint32_t x[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-      uint32_t h[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) h[j] = half2_bits(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
-      *reinterpret_cast<uint4 *>(qs + (c >> 3) * kAtomD + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-          make_uint4(h[0], h[1], h[2], h[3]);
-    }
+    for (int j = 0; j < 4; ++j)
+      h[j] = zero ? 0u : half2_bits(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
+    q[i] = make_uint4(h[0], h[1], h[2], h[3]);
   }
   fence_proxy_async_smem();
   __syncwarp();
 }
 
-__device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ring, int w, DenseWalk walk,
-                              uint32_t rank, int pt, int lane) {
+__device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ring, int w, DenseWalk walk, uint32_t rank,
+                              int pt, int lane) {
   const int warp = pt >> 5, key4 = lane >> 3, c8 = lane & 7;
   const int o = c8 >> 1;
   const bool o1 = o & 1, o2 = o & 2;
   const uint32_t z = (uint32_t)((4 * (c8 & 1)) ^ key4 ^ o) << 4;
   const uint32_t k_at = smem_u32(ring) + (uint32_t)(o * kSlotBytes + (16 * warp + key4) * 128) + z;
   const uint32_t v_at = smem_u32(ring) + (uint32_t)(warp * kSlotBytes + o * 4096 + key4 * 128) + z;
-  const uint32_t full_at = dsmem_addr(&S.full[0], 0), q_full_at = dsmem_addr(&S.q_full, 0);
-  DenseSegment g;
+  const uint32_t full_at = dsmem_addr(&S.full[0], 0);
   uint32_t round = 0;   // 8-slot rounds so far
   uint32_t item = 0;
   DeqRegs kr, vr;
-  while (dense_next(a, w, walk, g)) {
-    const uint8_t *base = a.kv + (int64_t)g.b * a.cap * ENTRY_BYTES;
-    auto load_piece = [&](DeqRegs &r, int i, int n, int half) {   // channels 256 half + 32 c8 .. of entry n
-      r.v[i] = make_uint4(0, 0, 0, 0);
-      r.sc[i] = 0;
-      if (n < g.len) {
-        const uint8_t *e = base + (int64_t)n * ENTRY_BYTES;
-        r.v[i] = ld_nc_v4(e + 128 * half + 16 * c8);
-        r.sc[i] = ld_nc_u16(e + 256 + 16 * half + 2 * c8);
-      }
-    };
-    auto load_k = [&](int step) {   // [channel half][4 keys]
+  auto load_piece = [&](DeqRegs &r, int i, const uint8_t *base, int len, int n, int half) {
+    r.v[i] = make_uint4(0, 0, 0, 0);
+    r.sc[i] = 0;
+    if (n < len) {
+      const uint8_t *e = base + (int64_t)n * ENTRY_BYTES;
+      r.v[i] = ld_nc_v4(e + 128 * half + 16 * c8);
+      r.sc[i] = ld_nc_u16(e + 256 + 16 * half + 2 * c8);
+    }
+  };
+  auto load_k = [&](int b, int len, int step) {   // [channel half][4 keys]
+    const uint8_t *base = a.kv + (int64_t)b * a.cap * ENTRY_BYTES;
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        load_piece(kr, i, step * kDenseStep + (int)rank * 128 + 16 * warp + 4 * (i & 3) + key4, i >> 2);
-    };
-    auto load_v = [&](int step) {   // [4 keys]
+    for (int i = 0; i < 8; ++i)
+      load_piece(kr, i, base, len, step * kDenseStep + (int)rank * 128 + 16 * warp + 4 * (i & 3) + key4, i >> 2);
+  };
+  auto load_v = [&](int b, int len, int step) {   // [4 keys]
+    const uint8_t *base = a.kv + (int64_t)b * a.cap * ENTRY_BYTES;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) load_piece(vr, i, step * kDenseStep + 32 * warp + 4 * i + key4, (int)rank);
-    };
-    auto emit_k = [&]() {
+    for (int i = 0; i < 8; ++i) load_piece(vr, i, base, len, step * kDenseStep + 32 * warp + 4 * i + key4, (int)rank);
+  };
+  auto emit_k = [&]() {
 #pragma unroll
-      for (int hc = 0; hc < 2; ++hc) {
-        if (round)
+    for (int hc = 0; hc < 2; ++hc) {
+      if (round)
 #pragma unroll
-          for (int s = 0; s < 4; ++s) wait_d(S, &S.free[4 * hc + s], (round - 1) & 1u);
+        for (int s = 0; s < 4; ++s) wait_d(S, &S.free[4 * hc + s], (round - 1) & 1u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          put32((k_at + (uint32_t)(4 * hc * kSlotBytes + i * 512)) ^ (uint32_t)((i & 1) << 6), kr.v[4 * hc + i],
-                kr.sc[4 * hc + i], o1, o2);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane < 4) mbar_arrive_pair(full_at + 8 * (4 * hc + lane), 1);
-      }
-      ++round;
-    };
-    auto emit_v = [&]() {
-      if (round) wait_d(S, &S.free[warp], (round - 1) & 1u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        put32((v_at + (uint32_t)(i * 512)) ^ (uint32_t)((i & 1) << 6), vr.v[i], vr.sc[i], o1, o2);
+      for (int i = 0; i < 4; ++i)
+        put32((k_at + (uint32_t)(4 * hc * kSlotBytes + i * 512)) ^ (uint32_t)((i & 1) << 6), kr.v[4 * hc + i],
+              kr.sc[4 * hc + i], o1, o2);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive_pair(full_at + 8 * warp, kDeqWarps);
-      ++round;
-    };
+      if (lane < 4) mbar_arrive_pair(full_at + 8 * (4 * hc + lane), 1);
+    }
+    ++round;
+  };
+  auto emit_v = [&]() {
+    if (round) wait_d(S, &S.free[warp], (round - 1) & 1u);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      put32((v_at + (uint32_t)(i * 512)) ^ (uint32_t)((i & 1) << 6), vr.v[i], vr.sc[i], o1, o2);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_pair(full_at + 8 * warp, kDeqWarps);
+    ++round;
+  };
 
-    load_k(g.s0);
-    load_v(g.s0);
+  DenseSegment g, next;
+  bool more = dense_next(a, w, walk, g);
+  if (more) {
+    load_k(g.b, g.len, g.s0);
+    load_v(g.b, g.len, g.s0);
+  }
+  pair_ready(S);
+  while (more) {
+    more = dense_next(a, w, walk, next);
     if (item) {   // the first segment's Q is the softmax warps' (they have nothing else to do then)
-      wait_d(S, &S.q_free, (item - 1) & 1u);
+      wait_d(S, &S.q_raw, item & 1u);
       convert_q<kDeqWarps * 32>(a, g, rank, qs, pt);
-      if (lane == 0) mbar_arrive_pair(q_full_at, 1);
+      if (lane == 0) mbar_arrive_pair(dsmem_addr(&S.q_full, 0), 1);
     }
     ++item;
-
     emit_k();
-    if (g.s0 + 1 < g.s1) load_k(g.s0 + 1);
+    if (g.s0 + 1 < g.s1)
+      load_k(g.b, g.len, g.s0 + 1);
 #pragma unroll 1
     for (int i = g.s0; i < g.s1; ++i) {
       if (i + 1 < g.s1) {
         emit_k();
-        if (i + 2 < g.s1) load_k(i + 2);
+        if (i + 2 < g.s1)
+          load_k(g.b, g.len, i + 2);
       }
       emit_v();
-      if (i + 1 < g.s1) load_v(i + 1);
+      if (i + 1 < g.s1)
+        load_v(g.b, g.len, i + 1);
+    }
+    g = next;
+    if (more) {
+      load_k(g.b, g.len, g.s0);
+      load_v(g.b, g.len, g.s0);
     }
   }
   // every slot this CTA filled has been read, and no commit is still to
@@ -239,19 +275,19 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
   if (round)
 #pragma unroll 1
     for (int s = 0; s < kSlots; ++s) wait_d(S, &S.free[s], (round - 1) & 1u);
-  if (item) wait_d(S, &S.q_free, (item - 1) & 1u);
 }
 
 // ---------------------------------------------------------------- products
-__device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ps, uint8_t *ring, uint32_t tmem,
-                               int w, DenseWalk walk) {
+// One thread of the even CTA.  `g`: the first segment, whose Q is on its way;
+// the next one's is sent for when the last S of a segment is done.
+__device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, uint8_t *qs, uint8_t *ps,
+                               uint8_t *ring, uint32_t tmem, int w, DenseWalk walk, DenseSegment g, bool more) {
   const uint64_t qd = smem_desc(smem_u32(qs), 16, 1024);
   const uint64_t pd = smem_desc(smem_u32(ps), 16, 1024);
   const uint64_t kd = smem_desc(smem_u32(ring), 16, 1024);
   const uint64_t vd = smem_desc(smem_u32(ring), 4096, 1024);
-  DenseSegment g;
   uint32_t round = 0, item = 0, n = 0;
-  while (dense_next(a, w, walk, g)) {
+  while (more) {
     const int steps = g.s1 - g.s0;
     auto scores = [&](uint32_t tile) {
 #pragma unroll 1
@@ -275,6 +311,11 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
       if (i + 1 < steps) {
         scores((n + 1) & 1u);
         if (i + 2 == steps) mma_commit_pair(&S.q_free);
+      }
+      if (i + 1 == steps) {
+        more = dense_next(a, w, walk, g);
+        wait_pair(S, &S.q_free, (item - 1) & 1u);
+        if (more && !S.abort) load_q(a, S, tm_q, qs, g, 0);
       }
       wait_pair(S, &S.p_full, n & 1u);
       tc_fence_after();
@@ -300,25 +341,44 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t
   mbar_wait_cluster(&S.done, 0);
 }
 
+// The odd CTA's part in it: its own token's Q.
+__device__ void dense_odd_queries(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, uint8_t *qs, int w,
+                                  DenseWalk walk, DenseSegment g, bool more) {
+  uint32_t item = 0;
+  while (more) {
+    wait_d(S, &S.q_free, item & 1u);
+    ++item;
+    more = dense_next(a, w, walk, g);
+    if (more && !S.abort) load_q(a, S, tm_q, qs, g, 1);
+  }
+}
+
 // ----------------------------------------------------------------- softmax
 // Thread tid holds head tid % 64: of S the keys 128 (tid / 64) .. + 127 of a
 // step, of O the channels 256 (tid / 64) .. + 255.
-__device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t *ps, uint32_t tmem, int w, DenseWalk walk,
-                              uint32_t rank, int tid, int lane, int warp) {
+__device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_out, const CUtensorMap &tm_part,
+                              uint8_t *qs, uint8_t *ps, int w, DenseWalk walk, uint32_t rank, int tid, int lane,
+                              int warp) {
+  pair_ready(S);
+  {
+    DenseWalk peek = walk;
+    DenseSegment first;
+    if (dense_next(a, w, peek, first)) {
+      wait_d(S, &S.q_raw, 0);
+      convert_q<kSoftWarps * 32>(a, first, rank, qs, tid);
+      if (lane == 0) mbar_arrive_pair(dsmem_addr(&S.q_full, 0), kDeqWarps / kSoftWarps);
+    }
+  }
+  const uint32_t tmem = S.tmem_base;
   const uint32_t p_full_at = dsmem_addr(&S.p_full, 0);
   const uint32_t row = tmem + ((uint32_t)(32 * warp) << 16);
   const int h = tid & 63, kh = tid >> 6;
   uint8_t *prow = ps + 2 * kh * kAtomD + h * 128;
   DenseSegment g;
-  {
-    DenseWalk peek = walk;
-    if (dense_next(a, w, peek, g)) {
-      convert_q<kSoftWarps * 32>(a, g, rank, qs, tid);
-      if (lane == 0) mbar_arrive_pair(dsmem_addr(&S.q_full, 0), kDeqWarps / kSoftWarps);
-    }
-  }
   uint32_t n = 0;
-  while (dense_next(a, w, walk, g)) {
+  DenseSegment next;
+  bool more = dense_next(a, w, walk, g);
+  for (; more; g = next) {
     float m = 0.0f, l = 0.0f;
 #pragma unroll 1
     for (int i = g.s0; i < g.s1; ++i, ++n) {
@@ -329,18 +389,21 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
       tc_fence_after();
       float mx = -INFINITY;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t u[32];
-        tmem_ld32(st + c, u);
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t u[2][32];
+        tmem_ld32(st + c, u[0]);
+        tmem_ld32(st + c + 32, u[1]);
         tmem_ld_wait();
-        if (c + 32 <= valid) {
+        float m2[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (c + 64 <= valid) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(u[j]));
+          for (int j = 0; j < 64; ++j) m2[j & 3] = fmaxf(m2[j & 3], __uint_as_float(u[j >> 5][j & 31]));
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (c + j < valid) mx = fmaxf(mx, __uint_as_float(u[j]));
+          for (int j = 0; j < 64; ++j)
+            if (c + j < valid) m2[j & 3] = fmaxf(m2[j & 3], __uint_as_float(u[j >> 5][j & 31]));
         }
+        mx = fmaxf(mx, fmaxf(fmaxf(m2[0], m2[1]), fmaxf(m2[2], m2[3])));
       }
       S.red[n & 1u][tid] = mx;
       bar_named(1, 128);
@@ -395,7 +458,7 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(p_full_at);
+      if (lane == 0) mbar_arrive_pair(p_full_at, 1);
     }
     // ------------------------------------------------------------ segment end
     S.red[n & 1u][tid] = l;
@@ -403,6 +466,7 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
     l += S.red[n & 1u][tid ^ 64];
     bar_named(1, 128);   // red is written again by the next step
     const float lse = (m - kBias + log2f(l)) * kLn2D;
+    more = dense_next(a, w, walk, next);
     wait_d(S, &S.p_free, (n - 1) & 1u);
     tc_fence_after();
     pdl_wait();   // own_out, own_lse
@@ -424,59 +488,68 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
       else if (a.lse)
         a.lse[tok_row + h] = total;
     }
-    // O as 16-bit rows through the warp's 8 KB of the P buffer, 128 channels at
-    // a time, so that every row leaves in 256-byte pieces: bf16 if it is the
-    // output, else (a partial, or this part of the softmax next to the other)
-    // fp16, whose rounding (2^-11 of a value) is below the output's (2^-8)
-    uint8_t *stage = ps + warp * 8192;
-    const int h0 = 32 * (warp & 1);
-    const bool final_rows = g.whole && !a.own_lse;
-    uint16_t *dst = g.whole ? reinterpret_cast<uint16_t *>(a.out) + (tok_row + h0) * D
-                            : reinterpret_cast<uint16_t *>(a.part) + (((int64_t)g.slot * 2 + rank) * H + h0) * D;
-    const int pc = lane & 15;
+    // O as 16-bit rows through the warp's 8 KB of the P buffer and tensor
+    // copies of 32 rows by 64 channels (stores from the registers, a row per
+    // lane, or staged rows read back for coalesced stores keep the load / store
+    // pipe, which is full anyway, 3.3 and 3.9 us a segment): bf16 if it is the
+    // output, fp16 for a partial, whose rounding (2^-11 of a value) is below
+    // the output's (2^-8)
+    const float *own = g.whole && a.own_lse ? a.own_out + (tok_row + h) * D + 256 * kh : nullptr;
+    const CUtensorMap *tm = g.whole ? &tm_out : &tm_part;
+    const int32_t y = (int32_t)(g.whole ? tok_row : ((int64_t)g.slot * 2 + rank) * H) + 32 * (warp & 1);
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 128) {
+    for (int c = 0; c < 256; c += 64) {
+      uint8_t *stage = ps + warp * 8192 + (c & 64) * 64;
+      if (c >= 128) {   // the copy out of this half two pieces ago has read it
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+      }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 64; e += 32) {
         uint32_t u[32];
-        tmem_ld32(row + kColOut + c + 32 * e, u);
+        tmem_ld32(row + kColOut + c + e, u);
         tmem_ld_wait();
-        uint32_t k[16];
+        float x[32];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float x = __uint_as_float(u[2 * j]) * wd, y = __uint_as_float(u[2 * j + 1]) * wd;
-          k[j] = final_rows ? bf16x2_bits(x, y) : half2_bits(x, y);
+        for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(u[j]) * wd;
+        if (own) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 4) {
+            const float4 o = *reinterpret_cast<const float4 *>(own + c + e + j);
+            x[j] = fmaf(wo, o.x, x[j]);
+            x[j + 1] = fmaf(wo, o.y, x[j + 1]);
+            x[j + 2] = fmaf(wo, o.z, x[j + 2]);
+            x[j + 3] = fmaf(wo, o.w, x[j + 3]);
+          }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4 *>(stage + lane * 256 + (((4 * e + j) ^ (lane & 7)) << 4)) =
-              make_uint4(k[4 * j], k[4 * j + 1], k[4 * j + 2], k[4 * j + 3]);
-      }
-      __syncwarp();
-#pragma unroll 8
-      for (int rr = 0; rr < 32; rr += 2) {
-        const int r = rr + (lane >> 4);
-        uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 256 + ((pc ^ (r & 7)) << 4));
-        const int64_t at = (int64_t)r * D + 256 * kh + c + 8 * pc;
-        if (g.whole && a.own_lse) {
-          const float x = __shfl_sync(0xffffffffu, wo, r);
-          const float4 *own = reinterpret_cast<const float4 *>(a.own_out + (tok_row + h0) * D + at);
-          const float4 y = own[0], z = own[1];
-          const float2 f0 = half2_floats(v.x), f1 = half2_floats(v.y), f2 = half2_floats(v.z), f3 = half2_floats(v.w);
-          v = make_uint4(bf16x2_bits(fmaf(x, y.x, f0.x), fmaf(x, y.y, f0.y)),
-                         bf16x2_bits(fmaf(x, y.z, f1.x), fmaf(x, y.w, f1.y)),
-                         bf16x2_bits(fmaf(x, z.x, f2.x), fmaf(x, z.y, f2.y)),
-                         bf16x2_bits(fmaf(x, z.z, f3.x), fmaf(x, z.w, f3.y)));
+        for (int j = 0; j < 4; ++j) {
+          uint32_t k[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            k[i] = g.whole ? bf16x2_bits(x[8 * j + 2 * i], x[8 * j + 2 * i + 1])
+                           : half2_bits(x[8 * j + 2 * i], x[8 * j + 2 * i + 1]);
+          *reinterpret_cast<uint4 *>(stage + lane * 128 + (((e / 8 + j) ^ (lane & 7)) << 4)) =
+              make_uint4(k[0], k[1], k[2], k[3]);
         }
-        *reinterpret_cast<uint4 *>(dst + at) = v;
       }
+      fence_proxy_async_smem();
       __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(tm, 256 * kh + c, y, stage);
+        bulk_commit();
+      }
     }
+    if (lane == 0) bulk_wait_read<0>();   // the next P may be written (after the next maximum's barrier)
+    __syncwarp();
     tc_fence_before();   // O is read before the next segment's products (ordered by p_full)
   }
+  if (lane == 0) bulk_wait<0>();
 }
 
-__global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArgs a) {
+__global__ void __launch_bounds__(kThreadsD, 1)
+    dense_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_out,
+                      const __grid_constant__ CUtensorMap tm_part, const DenseArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *qs = base, *ps = qs + kQBytesD, *ring = ps + kPBytes;
@@ -484,11 +557,12 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_ctarank();
   const int w = blockIdx.x >> 1;
-  if (tid == 0) {
+  if (warp == kMmaWarpD && lane == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&S.full[s], 2 * kDeqWarps);
       mbar_init(&S.free[s], 1);
     }
+    mbar_init(&S.q_raw, 1);
     mbar_init(&S.q_full, 2 * kDeqWarps);
     mbar_init(&S.q_free, 1);
     mbar_init(&S.s_full[0], 1);
@@ -498,6 +572,7 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
     mbar_init(&S.done, 1);
     S.abort = 0;
     fence_barrier_init();
+    prefetch_tmap(&tm_q);
   }
   // Past pdl_wait the kernel before this one is complete (programmatic launch).
   // Behind the sparse readout of the same call (own_lse) nothing but its
@@ -507,23 +582,26 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
   // each of them fills, so neither can they share its tensor memory.)
   if (!a.own_lse) pdl_wait();
   const DenseWalk walk = dense_walk(a, w, lane);
-  __syncthreads();
-  if (warp == kMmaWarpD) {
-    tmem_alloc_pair(&S.tmem_base, 512);
-    tmem_relinquish_pair();
-  }
-  tc_fence_before();
-  __syncthreads();
-  cluster_sync();   // both CTAs' barriers and tensor memory are set up
-  tc_fence_after();
-  const uint32_t tmem = S.tmem_base;
-
   if (warp < kSoftWarps) {
-    dense_softmax(a, S, qs, ps, tmem, w, walk, rank, tid, lane, warp);
+    dense_softmax(a, S, tm_out, tm_part, qs, ps, w, walk, rank, tid, lane, warp);
   } else if (warp < kMmaWarpD) {
     dense_dequant(a, S, qs, ring, w, walk, rank, tid - kSoftWarps * 32, lane);
   } else {
-    if (rank == 0 && elect_one()) dense_products(a, S, qs, ps, ring, tmem, w, walk);
+    __syncwarp();
+    DenseWalk ahead = walk;
+    DenseSegment g;
+    const bool more = dense_next(a, w, ahead, g);
+    if (more && lane == 0) load_q(a, S, tm_q, qs, g, rank);
+    __syncwarp();
+    tmem_alloc_pair(&S.tmem_base, 512);
+    tmem_relinquish_pair();
+    const uint32_t tmem = pair_ready(S);
+    if (elect_one()) {
+      if (rank == 0)
+        dense_products(a, S, tm_q, qs, ps, ring, tmem, w, ahead, g, more);
+      else
+        dense_odd_queries(a, S, tm_q, qs, w, ahead, g, more);
+    }
     __syncwarp();
   }
   tc_fence_before();
@@ -532,23 +610,19 @@ __global__ void __launch_bounds__(kThreadsD, 1) dense_attn_kernel(const DenseArg
   pdl_release();
   if (warp == kMmaWarpD) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, 512);
+    tmem_dealloc_pair(S.tmem_base, 512);
   }
 }
 
 // Merges the pairs that several workers share, with the weights exp(lse_i -
 // lse), lse the log-sum-exp over all their partials (and the other part of the
-// softmax).  kByPair (fewer pairs than workers): kCtas CTAs for each pair.
-// Otherwise at most one pair lies across each range's start: kCtas CTAs for
-// each worker take the pair across its start, if that is the pair's first.  A
-// CTA takes kHeads heads of one token, kWarps warps per head, each every
-// kWarps-th partial: eight warps where a pair has many partials, one where it
-// has two or three.  The CTAs past those write the sequences without entries.
-template <bool kByPair>
-struct Combine {
-  static constexpr int kHeads = kByPair ? 1 : 8, kWarps = kByPair ? 8 : 1;
-  static constexpr int kCtas = 2 * (H / kHeads);
-};
+// softmax).  With fewer pairs than workers, a group of CTAs takes each pair;
+// otherwise at most one pair lies across each range's start and a group for
+// each worker takes the pair across its start, if that is the pair's first.  A
+// CTA takes one token and 8 / a.split of its heads, a.split warps per head,
+// each every a.split-th partial, four of them in flight (about as many warps
+// as bring every partial in one or two rounds: a pair has workers / pairs
+// partials).  The CTAs past the groups write the sequences without entries.
 constexpr int kEmptyCtas = 64;
 
 __device__ __forceinline__ void put_row16(const DenseArgs &a, int64_t row, int lane, const float (&o)[16]) {
@@ -571,27 +645,28 @@ __device__ __forceinline__ void rest_rows(const DenseArgs &a, int64_t row0, int6
   }
 }
 
-template <bool kByPair>
-__global__ void __launch_bounds__(256) dense_combine_kernel(const DenseArgs a) {
-  using C = Combine<kByPair>;
-  __shared__ float red[kByPair ? C::kWarps : 1][D];
-  pdl_wait();
+__global__ void __launch_bounds__(256, 3) dense_combine_kernel(const DenseArgs a) {
+  __shared__ float red[8][D];
+  // (n_vis is older than the dense kernel: it may be read before the wait)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t pairs = (a.n_q + 1) / 2;
-  const int groups = kByPair ? (int)(a.seqs * pairs) : a.workers;
-  const int group = blockIdx.x / C::kCtas, cta = blockIdx.x - group * C::kCtas;
+  const bool by_pair = a.seqs * pairs < a.workers;
+  const int groups = by_pair ? (int)(a.seqs * pairs) : a.workers;
+  const int heads = 8 / a.split, ctas = 2 * (H / heads);   // per CTA, per group
+  const int group = blockIdx.x / ctas, cta = blockIdx.x - group * ctas;
   if (group >= groups) {
-    const int ctas = gridDim.x - groups * C::kCtas, me = (blockIdx.x - groups * C::kCtas) * 8 + warp;
+    pdl_wait();
+    const int rest = gridDim.x - groups * ctas, me = (blockIdx.x - groups * ctas) * 8 + warp;
     for (int b = 0; b < a.seqs; ++b)
-      if (dense_len(a, b) == 0) rest_rows(a, (int64_t)b * a.n_q * H, (int64_t)a.n_q * H, me, ctas * 8, lane);
+      if (dense_len(a, b) == 0) rest_rows(a, (int64_t)b * a.n_q * H, (int64_t)a.n_q * H, me, rest * 8, lane);
     return;
   }
   // the pair, its first unit and its steps
-  int b = kByPair ? (int)(group / pairs) : 0;
+  int b = by_pair ? (int)(group / pairs) : 0;
   int64_t before, total, pair, u0;
   int workers, steps;
   dense_units(a, b, lane, before, total, workers);
-  if (kByPair) {
+  if (by_pair) {
     pair = group - b * pairs;
     steps = dense_steps(dense_len(a, b));
     if (steps == 0) return;
@@ -610,9 +685,9 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseArgs a) {
   }
   const int w0 = dense_worker(total, workers, u0);
   const int n = dense_worker(total, workers, u0 + steps - 1) - w0 + 1;   // partials
-  if (n == 1 || (!kByPair && w0 != group - 1)) return;   // finished by its worker; an earlier start's
-  const int r = cta & 1, hw = warp / C::kWarps, part = warp % C::kWarps;
-  const int head = (cta >> 1) * C::kHeads + hw;
+  if (n == 1 || (!by_pair && w0 != group - 1)) return;   // finished by its worker; an earlier start's
+  const int r = cta & 1, hw = warp / a.split, part = warp - hw * a.split;
+  const int head = (cta >> 1) * heads + hw;
   const int64_t t = 2 * pair + r;
   if (t >= a.n_q) return;
   const int64_t row = ((int64_t)b * a.n_q + t) * H + head;
@@ -621,7 +696,24 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseArgs a) {
   const int64_t row0 = ((int64_t)4 * w0 + r) * H + head;
   const int64_t odd = dense_range(total, workers, w0) < u0 ? 2 * H : 0;
   auto part_row = [&](int i) { return row0 + (int64_t)i * (4 * H) + (i == 0 ? odd : 0); };
-  constexpr int kPer = (kDenseWorkers + 31) / 32;
+  // this warp's partials, kMine loads in flight, the first ones beside the
+  // log-sum-exps'
+  pdl_wait();   // the dense kernel's partials
+  constexpr int kPer = (kDenseWorkers + 31) / 32, kMine = 4;
+  uint4 v[kMine][2];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+      const int i = i0 + k * a.split;
+      v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
+      if (i < n) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.part + part_row(i) * D + lane * 16);
+        v[k][0] = src[0];
+        v[k][1] = src[1];
+      }
+    }
+  };
+  load(part);
   float e[kPer], own = a.own_lse ? a.own_lse[row] : -INFINITY, mx = own;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -647,64 +739,57 @@ __global__ void __launch_bounds__(256) dense_combine_kernel(const DenseArgs a) {
     const float4 *src = reinterpret_cast<const float4 *>(a.own_out + row * D + lane * 16);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float4 v = src[i];
-      acc[4 * i] = own * v.x;
-      acc[4 * i + 1] = own * v.y;
-      acc[4 * i + 2] = own * v.z;
-      acc[4 * i + 3] = own * v.w;
+      const float4 o = src[i];
+      acc[4 * i] = own * o.x;
+      acc[4 * i + 1] = own * o.y;
+      acc[4 * i + 2] = own * o.z;
+      acc[4 * i + 3] = own * o.w;
     }
   }
 #pragma unroll 1
-  for (int i0 = part; i0 < n; i0 += 4 * C::kWarps) {   // four partials in flight
-    uint4 v[4][2];
-    float f[4];
+  for (int i0 = part;;) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int i = i0 + k * C::kWarps;
-      v[k][0] = v[k][1] = make_uint4(0, 0, 0, 0);
-      if (i < n) {
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.part + part_row(i) * D + lane * 16);
-        v[k][0] = src[0];
-        v[k][1] = src[1];
-      }
-      f[k] = 0.0f;
+    for (int k = 0; k < kMine; ++k) {
+      const int i = i0 + k * a.split;
+      float f = 0.0f;   // partials past n: e = 0
 #pragma unroll
       for (int j = 0; j < kPer; ++j) {
         const float x = __shfl_sync(0xffffffffu, e[j], i & 31);
-        if (i >> 5 == j) f[k] = x;
+        if (i >> 5 == j) f = x;
       }
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
       const uint32_t u[8] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w, v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const float2 x = half2_floats(u[j]);
-        acc[2 * j] = fmaf(f[k], x.x, acc[2 * j]);
-        acc[2 * j + 1] = fmaf(f[k], x.y, acc[2 * j + 1]);
+        acc[2 * j] = fmaf(f, x.x, acc[2 * j]);
+        acc[2 * j + 1] = fmaf(f, x.y, acc[2 * j + 1]);
       }
     }
+    i0 += kMine * a.split;
+    if (i0 >= n) break;
+    load(i0);
   }
   const float inv = 1.0f / sum;
-  if constexpr (kByPair) {
-    // thread (part, lane) adds up channels 2 tid, 2 tid + 1 over the warps
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<float4 *>(&red[part][lane * 16 + 4 * i]) =
-          make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-    __syncthreads();
-    float x = 0.0f, y = 0.0f;
-#pragma unroll
-    for (int p = 0; p < C::kWarps; ++p) {
-      const float2 v = *reinterpret_cast<const float2 *>(&red[p][2 * tid]);
-      x += v.x;
-      y += v.y;
-    }
-    reinterpret_cast<uint32_t *>(a.out + row * D)[tid] = bf16x2_bits(x * inv, y * inv);
-  } else {
+  if (a.split == 1) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] *= inv;
     put_row16(a, row, lane, acc);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<float4 *>(&red[warp][lane * 16 + 4 * i]) =
+          make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
+    __syncthreads();   // (t, the one exit above, is the CTA's)
+    // the head's warps add up a share of its channels each
+    for (int c = 2 * (32 * part + lane); c < D; c += 64 * a.split) {
+      float x = 0.0f, y = 0.0f;
+      for (int p = 0; p < a.split; ++p) {
+        const float2 u = *reinterpret_cast<const float2 *>(&red[hw * a.split + p][c]);
+        x += u.x;
+        y += u.y;
+      }
+      *reinterpret_cast<uint32_t *>(a.out + row * D + c) = bf16x2_bits(x * inv, y * inv);
+    }
   }
   if (part == 0 && lane == 0 && a.lse) a.lse[row] = mx + logf(sum);
 }
@@ -735,7 +820,8 @@ size_t dense_scratch_bytes(int64_t tokens, int64_t n_max) {
 
 cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n_vis, int64_t n_max, int64_t cap,
                               int32_t seqs, int32_t n_q, void *out, float *lse, const float *own_out,
-                              const float *own_lse, void *scratch, int num_sms, cudaStream_t stream, int *launches) {
+                              const float *own_lse, int own_ctas, void *scratch, int num_sms, cudaStream_t stream,
+                              int *launches) {
   DenseArgs a;
   a.q = static_cast<const __nv_bfloat16 *>(q);
   a.kv = kv;
@@ -748,7 +834,18 @@ cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n
   int64_t workers = dense_workers((int64_t)seqs * n_q, n_max);
   workers = workers < most ? workers : most;
   workers = workers < num_sms / 2 ? workers : num_sms / 2;
+  // Beside the own part's kernel: the workers that fit next to its CTAs, if
+  // fewer of them end sooner than all of them after it (its few microseconds
+  // of latency are about kOwnUnits of theirs).
+  constexpr int64_t kOwnUnits = 5;
+  const int64_t beside = (num_sms - own_ctas) / 2;
+  if (own_ctas > 0 && beside >= 1 && beside < workers &&
+      (most + beside - 1) / beside <= (most + workers - 1) / workers + kOwnUnits)
+    workers = beside;
   a.workers = (int32_t)(workers < 1 ? 1 : workers);
+  const int64_t pairs = (int64_t)seqs * ((n_q + 1) / 2), groups = pairs < a.workers ? pairs : a.workers;
+  a.split = 1;   // warps per head of the combine: about four partials each
+  while (a.split < 8 && groups * a.split * 4 < a.workers) a.split *= 2;
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lse = lse;
   a.own_out = own_out;
@@ -756,23 +853,25 @@ cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n
   a.part = static_cast<__half *>(scratch);
   a.part_lse = reinterpret_cast<float *>(a.part + (size_t)2 * a.workers * 2 * H * D);
   if (most == 0) {
-    const int64_t rows = (int64_t)seqs * n_q * H;
-    const cudaError_t e = launch_pdl(dense_rest_kernel, dim3((unsigned)(rows < 4096 ? (rows + 7) / 8 : 512)), dim3(256), 0,
+    const int64_t rest = (int64_t)seqs * n_q * H;
+    const cudaError_t e = launch_pdl(dense_rest_kernel, dim3((unsigned)(rest < 4096 ? (rest + 7) / 8 : 512)), dim3(256), 0,
                                      stream, 0u, a);
     if (e == cudaSuccess) ++*launches;
     return e;
   }
+  const int64_t rows = (int64_t)seqs * n_q * H;
+  CUtensorMap tm_q, tm_out, tm_part;   // (the partials' fp16 are copied as any 16-bit type)
+  if (!make_tmap_bf16(&tm_q, q, D, rows, H) || !make_tmap_bf16(&tm_out, out, D, rows, 32) ||
+      !make_tmap_bf16(&tm_part, a.part, D, (int64_t)a.workers * 4 * H, 32))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(dense_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemD);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(dense_attn_kernel, dim3((unsigned)(2 * a.workers)), dim3(kThreadsD), kSmemD, stream, 2u, a);
+  e = launch_pdl(dense_attn_kernel, dim3((unsigned)(2 * a.workers)), dim3(kThreadsD), kSmemD, stream, 2u, tm_q, tm_out,
+                 tm_part, a);
   if (e != cudaSuccess) return e;
   ++*launches;
-  const int64_t pairs = (int64_t)seqs * ((n_q + 1) / 2);
-  const unsigned empty = n_vis ? kEmptyCtas : 0;
-  e = pairs < a.workers ? launch_pdl(dense_combine_kernel<true>, dim3((unsigned)pairs * Combine<true>::kCtas + empty),
-                                     dim3(256), 0, stream, 0u, a)
-                        : launch_pdl(dense_combine_kernel<false>, dim3((unsigned)a.workers * Combine<false>::kCtas + empty),
-                                     dim3(256), 0, stream, 0u, a);
+  e = launch_pdl(dense_combine_kernel, dim3((unsigned)(groups * 2 * (H / (8 / a.split)) + (n_vis ? kEmptyCtas : 0))),
+                 dim3(256), 0, stream, 0u, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -25,6 +25,7 @@ struct DenseArgs {
   int32_t n_max;
   int32_t seqs, n_q;
   int32_t workers;
+  int32_t split;               // combine: warps per head (1, 2, 4 or 8)
   __nv_bfloat16 *out;          // [seqs][n_q][64][512]
   float *lse;                  // [seqs][n_q][64] or NULL
   const float *own_out;        // another part of each token's softmax to merge in
@@ -70,12 +71,20 @@ __device__ __forceinline__ void dense_units(const DenseArgs &a, int b, int lane,
   workers = (int)(total < a.workers ? total : a.workers);
 }
 
+// a / b for a >= 0, b > 0: in 32 bits where they fit (a 64-bit division takes
+// some hundred instructions, several of them in a row before the first load).
+__device__ __forceinline__ int64_t dense_div(int64_t a, int64_t b) {
+  return (a | b) >> 32 ? a / b : (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 // Worker w's range starts at unit floor(w total / workers).
-__device__ __forceinline__ int64_t dense_range(int64_t total, int workers, int w) { return total * w / workers; }
+__device__ __forceinline__ int64_t dense_range(int64_t total, int workers, int w) {
+  return dense_div(total * w, workers);
+}
 
 // The worker whose range holds unit u.
 __device__ __forceinline__ int dense_worker(int64_t total, int workers, int64_t u) {
-  return (int)(((u + 1) * workers - 1) / total);
+  return (int)dense_div((u + 1) * workers - 1, total);
 }
 
 // A worker's walk over its range, one segment (a pair and its steps inside
@@ -121,7 +130,7 @@ __device__ __forceinline__ bool dense_next(const DenseArgs &a, int w, DenseWalk 
   }
   const int64_t rel = k.at - k.seq0;
   g.b = k.b;
-  g.pair = (int)(rel / k.steps);
+  g.pair = (int)dense_div(rel, k.steps);
   g.len = k.len;
   g.s0 = (int)(rel - (int64_t)g.pair * k.steps);
   const int64_t left = k.end - k.at;

@@ -227,6 +227,8 @@ size_t attn_scratch_bytes(int32_t problems, int32_t K, int32_t W, int32_t kernel
 // Reads and clears the readout's own device error word (that unit is
 // compiled as whole-program device code).
 cudaError_t attn_take_error(unsigned int *bits);
+// CTAs of a readout of `problems` tokens.
+int attn_ctas(int32_t problems, int32_t K, int32_t W, int32_t kernel);
 cudaError_t launch_sparse_attn(AttnArgs a, void *scratch, cudaStream_t stream, int *launches);
 
 // Sliding-window rows as FP8 (pos NULL: no RoPE) and the caches' read-backs
@@ -242,11 +244,13 @@ cudaError_t launch_indexer_k_read(const uint8_t *k_fp4, int64_t batch, int64_t c
 
 // Dense readout of seqs x n_q tokens over the first n_vis[b] (NULL: n_max)
 // entries of their sequence, merged with own_out / own_lse (fp32 rows and
-// log-sum-exps of another part of each token's softmax) unless NULL.
+// log-sum-exps of another part of each token's softmax, which the readout
+// right before it on the stream computes on own_ctas CTAs) unless NULL.
 // Scratch for up to `tokens` query tokens over up to n_max entries each.
 size_t dense_scratch_bytes(int64_t tokens, int64_t n_max);
 cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n_vis, int64_t n_max, int64_t cap,
                               int32_t seqs, int32_t n_q, void *out, float *lse, const float *own_out,
-                              const float *own_lse, void *scratch, int num_sms, cudaStream_t stream, int *launches);
+                              const float *own_lse, int own_ctas, void *scratch, int num_sms, cudaStream_t stream,
+                              int *launches);
 
 }  // namespace csa2

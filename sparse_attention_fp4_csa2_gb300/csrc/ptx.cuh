@@ -234,6 +234,28 @@ __device__ __forceinline__ void tma_load_2d_mc(void *dst, const void *tmap, int3
       : "memory");
 }
 
+// 2-D tiled tensor copy shared -> global (box and swizzle from the tensor map)
+// as part of the thread's current bulk group.  x and y not negative, x *
+// elem_size a multiple of 16 bytes.
+__device__ __forceinline__ void tma_store_2d(const void *tmap, int32_t x, int32_t y, const void *src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(tmap), "r"(x),
+               "r"(y), "r"(smem_u32(src))
+               : "memory");
+}
+
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+
+// Until at most N of this thread's bulk groups still read shared memory
+// (bulk_wait_read) or are incomplete (bulk_wait).
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void bulk_wait() {
+  asm volatile("cp.async.bulk.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The same with an L2 cache policy (createpolicy below) for the loaded lines.
 __device__ __forceinline__ void tma_load_2d_hint(void *dst, const void *tmap, int32_t x, int32_t y, uint64_t *bar,
                                                  uint64_t policy) {

@@ -257,6 +257,8 @@ CROSS = [
     (9, 2, 130, [130, 129, 128, 127, 1, 2, 0, 64, 65]),
     (1, 3, 30000, [29999]),
     (2, 100, 8, [8, 7]),
+    (80, 2, 6000, [100] * 40 + [6000, 0] + [256] * 38),   # more pairs than workers, one of them shared by many
+    (1, 301, 5000, [4321]),
 ]
 
 
