@@ -57,12 +57,13 @@ __device__ __forceinline__ float quotient(float x, float s, float r) {
 }
 
 // A warp writes R rows, one after the other, all loads first.  Lane l owns
-// channels 16 l .. + 15: it loads 32 bytes, rotates them if they are RoPE
-// channels (lane j evaluates frequency j; products and sums rounded
-// separately), and stores 16 bytes of codes.  What bounds it is instruction
-// issue and the loads' latency, not HBM (32,768 rows: 50 MB, 7.5 us at the
-// copy rate): one rounded division per channel alone was a third of the
-// instructions.
+// channels 16 l .. + 15: it loads 32 bytes and stores 16 bytes of codes.  The
+// RoPE pairs, which lanes 28 to 31 hold, pass through shared memory so that
+// lane j rotates pair j (products and sums rounded separately).  Instruction
+// issue and the loads' latency bound it, not HBM: 32,768 rows (50 MB, 7.5 us
+// at the copy rate) took 22.5 us with a rounded division per channel and
+// shuffled rotations, 14.0 us in this form.  One row per warp is slower for
+// many rows (14.6 us) and the same for a decode step's 32 (1.9 us).
 template <int R>
 __global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat16 *__restrict__ latent, int64_t n,
                                                               const int64_t *__restrict__ pos,
@@ -70,6 +71,7 @@ __global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat1
                                                               uint8_t *__restrict__ swa, float *__restrict__ swa_scale,
                                                               int64_t rows, const RopeTurns turns) {
   pdl_wait();   // the inputs' producer is complete past here (programmatic launch)
+  __shared__ __align__(16) float tails[8][ROPE_DIM];
   const int lane = threadIdx.x & 31;
   const int64_t e0 = ((int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)) * R;
   uint4 u[R][2];
@@ -103,18 +105,30 @@ __global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat1
     if (pos) {
       float cj, sj;
       rope_cos_sin(turns.step[lane], p[r], cj, sj);
-      const int jbase = (lane - (D - ROPE_DIM) / 16) * 8;
+      // lanes 28 .. 31 hold the 32 pairs: each lane takes its own through shared memory
+      float *tail = tails[threadIdx.x >> 5];
+      if (lane >= (D - ROPE_DIM) / 16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int from = (jbase + i) & 31;
-        const float c = __shfl_sync(0xffffffffu, cj, from);
-        const float s = __shfl_sync(0xffffffffu, sj, from);
-        if (lane >= (D - ROPE_DIM) / 16) {
-          const float a = x[2 * i], b = x[2 * i + 1];
-          x[2 * i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-          x[2 * i + 1] = __fadd_rn(__fmul_rn(a, s), __fmul_rn(b, c));
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<float4 *>(tail + (lane - (D - ROPE_DIM) / 16) * 16 + 4 * i) =
+              make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+      }
+      __syncwarp();
+      const float2 v = *reinterpret_cast<const float2 *>(tail + 2 * lane);
+      *reinterpret_cast<float2 *>(tail + 2 * lane) =
+          make_float2(__fsub_rn(__fmul_rn(v.x, cj), __fmul_rn(v.y, sj)), __fadd_rn(__fmul_rn(v.x, sj), __fmul_rn(v.y, cj)));
+      __syncwarp();
+      if (lane >= (D - ROPE_DIM) / 16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float4 o = *reinterpret_cast<const float4 *>(tail + (lane - (D - ROPE_DIM) / 16) * 16 + 4 * i);
+          x[4 * i] = o.x;
+          x[4 * i + 1] = o.y;
+          x[4 * i + 2] = o.z;
+          x[4 * i + 3] = o.w;
         }
       }
+      __syncwarp();
     }
     float amax = 0.0f;   // NaNs do not count
 #pragma unroll
