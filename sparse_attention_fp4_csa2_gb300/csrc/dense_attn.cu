@@ -469,7 +469,7 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm
     more = dense_next(a, w, walk, next);
     wait_d(S, &S.p_free, (n - 1) & 1u);
     tc_fence_after();
-    pdl_wait();   // own_out, own_lse
+    if (g.whole) pdl_wait();   // own_out, own_lse
     const int t = 2 * g.pair + (int)rank;
     if (t >= a.n_q) continue;
     // the weights of this part and of the other part of the softmax
@@ -545,6 +545,7 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm
     tc_fence_before();   // O is read before the next segment's products (ordered by p_full)
   }
   if (lane == 0) bulk_wait<0>();
+  pdl_wait();   // the combine reads own_out too: this kernel's end is also the end of the one beside it
 }
 
 __global__ void __launch_bounds__(kThreadsD, 1)
@@ -575,11 +576,12 @@ __global__ void __launch_bounds__(kThreadsD, 1)
     prefetch_tmap(&tm_q);
   }
   // Past pdl_wait the kernel before this one is complete (programmatic launch).
-  // Behind the sparse readout of the same call (own_lse) nothing but its
-  // results needs that wait, and it has itself waited for everything before
-  // it when it lets this kernel start: the two run side by side, and only the
-  // segments' ends wait.  (Their CTAs cannot share an SM, whose shared memory
-  // each of them fills, so neither can they share its tensor memory.)
+  // Behind the sparse readout of the same call (own_lse) only its results need
+  // that wait, and it has itself waited for everything before it when it lets
+  // this kernel start: the two run side by side, and the wait comes where a
+  // whole pair's rows are merged with its own part, and at the kernel's end.
+  // (Their CTAs cannot share an SM, whose shared memory each of them fills, so
+  // neither can they share its tensor memory.)
   if (!a.own_lse) pdl_wait();
   const DenseWalk walk = dense_walk(a, w, lane);
   if (warp < kSoftWarps) {
