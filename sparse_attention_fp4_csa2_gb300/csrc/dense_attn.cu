@@ -658,9 +658,15 @@ __global__ void __launch_bounds__(256, 3) dense_combine_kernel(const DenseArgs a
   const int group = blockIdx.x / ctas, cta = blockIdx.x - group * ctas;
   if (group >= groups) {
     pdl_wait();
-    const int rest = gridDim.x - groups * ctas, me = (blockIdx.x - groups * ctas) * 8 + warp;
-    for (int b = 0; b < a.seqs; ++b)
-      if (dense_len(a, b) == 0) rest_rows(a, (int64_t)b * a.n_q * H, (int64_t)a.n_q * H, me, rest * 8, lane);
+    // every warps-th token's length per lane: neighbours go to different CTAs
+    const int rest = gridDim.x - groups * ctas, warps = rest * 8, me = warp * rest + blockIdx.x - groups * ctas;
+    const int64_t tokens = (int64_t)a.seqs * a.n_q;
+    for (int64_t t0 = me; t0 < tokens; t0 += 32 * (int64_t)warps) {
+      const int64_t t = t0 + (int64_t)lane * warps;
+      uint32_t empty = __ballot_sync(0xffffffffu, t < tokens && dense_len(a, (int)((uint32_t)t / (uint32_t)a.n_q)) == 0);
+      for (; empty; empty &= empty - 1)
+        rest_rows(a, (t0 + (int64_t)(__ffs(empty) - 1) * warps) * H, H, 0, 1, lane);
+    }
     return;
   }
   // the pair, its first unit and its steps
@@ -676,12 +682,9 @@ __global__ void __launch_bounds__(256, 3) dense_combine_kernel(const DenseArgs a
   } else {
     if (group == 0 || group >= workers) return;
     const int64_t at = dense_range(total, workers, group);
-    steps = dense_steps(dense_len(a, 0));
-    while (at >= before + pairs * steps) {
-      before += pairs * steps;
-      steps = dense_steps(dense_len(a, ++b));
-    }
-    pair = (at - before) / steps;
+    dense_find(a, at, lane, b, before);
+    steps = dense_steps(dense_len(a, b));
+    pair = dense_div(at - before, steps);
     u0 = before + pair * steps;
     if (at == u0) return;   // no pair lies across this start
   }

@@ -87,6 +87,37 @@ __device__ __forceinline__ int dense_worker(int64_t total, int workers, int64_t 
   return (int)dense_div((u + 1) * workers - 1, total);
 }
 
+// The sequence that holds unit u and its first unit; a whole warp calls it (32
+// lengths at a time: with a length per step, the last worker of 4,096 short
+// sequences would set out 80 us late).
+__device__ __forceinline__ void dense_find(const DenseArgs &a, int64_t u, int lane, int &b, int64_t &seq0) {
+  const int64_t pairs = (a.n_q + 1) / 2;
+  if (!a.n_vis) {
+    const int64_t s = pairs * dense_steps(a.n_max);
+    b = (int)dense_div(u, s);
+    seq0 = b * s;
+    return;
+  }
+  int64_t base = 0;
+  for (int c = 0;; c += 32) {   // u is a unit: some sequence below holds it
+    int64_t x = c + lane < a.seqs ? pairs * dense_steps(dense_len(a, c + lane)) : 0;
+    const int64_t own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, u < base + x);
+    if (past) {
+      const int from = __ffs(past) - 1;
+      b = c + from;
+      seq0 = base + __shfl_sync(0xffffffffu, x - own, from);
+      return;
+    }
+    base += __shfl_sync(0xffffffffu, x, 31);
+  }
+}
+
 // A worker's walk over its range, one segment (a pair and its steps inside
 // the range) at a time.
 struct DenseWalk {
@@ -106,14 +137,38 @@ struct DenseSegment {
 
 __device__ __forceinline__ DenseWalk dense_walk(const DenseArgs &a, int w, int lane) {
   DenseWalk k;
-  int64_t before, total;
-  int workers;
-  dense_units(a, 0, lane, before, total, workers);
-  k.start = k.at = w < workers ? dense_range(total, workers, w) : 0;
-  k.end = w < workers ? dense_range(total, workers, w + 1) : 0;
   k.seq0 = 0;
-  k.b = 0;
-  k.len = k.at < k.end ? dense_len(a, 0) : 0;
+  k.b = k.len = 0;
+  if (a.n_vis && a.seqs <= 32) {   // one length per lane, one scan
+    const int len = lane < a.seqs ? dense_len(a, lane) : 0;
+    const int64_t own = (int64_t)((a.n_q + 1) / 2) * dense_steps(len);
+    int64_t x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    const int64_t total = __shfl_sync(0xffffffffu, x, 31);
+    const int workers = (int)(total < a.workers ? total : a.workers);
+    k.start = k.at = w < workers ? dense_range(total, workers, w) : 0;
+    k.end = w < workers ? dense_range(total, workers, w + 1) : 0;
+    const uint32_t past = __ballot_sync(0xffffffffu, k.at < x);
+    if (past) {
+      k.b = __ffs(past) - 1;
+      k.seq0 = __shfl_sync(0xffffffffu, x - own, k.b);
+      k.len = __shfl_sync(0xffffffffu, len, k.b);
+    }
+  } else {
+    int64_t before, total;
+    int workers;
+    dense_units(a, 0, lane, before, total, workers);
+    k.start = k.at = w < workers ? dense_range(total, workers, w) : 0;
+    k.end = w < workers ? dense_range(total, workers, w + 1) : 0;
+    if (k.at < k.end) {
+      dense_find(a, k.at, lane, k.b, k.seq0);
+      k.len = dense_len(a, k.b);
+    }
+  }
   k.steps = dense_steps(k.len);
   return k;
 }

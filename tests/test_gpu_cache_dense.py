@@ -259,6 +259,7 @@ CROSS = [
     (2, 100, 8, [8, 7]),
     (80, 2, 6000, [100] * 40 + [6000, 0] + [256] * 38),   # more pairs than workers, one of them shared by many
     (1, 301, 5000, [4321]),
+    (700, 1, 300, [(37 * i) % 301 for i in range(700)]),  # many short sequences, some empty
 ]
 
 
