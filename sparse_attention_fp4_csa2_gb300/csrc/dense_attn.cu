@@ -341,11 +341,27 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &t
   mbar_wait_cluster(&S.done, 0);
 }
 
-// The odd CTA's part in it: its own token's Q.
-__device__ void dense_odd_queries(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, uint8_t *qs, int w,
-                                  DenseWalk walk, DenseSegment g, bool more) {
+// One thread of the odd CTA: its own token's Q, and what the combine has to
+// know of a pair that starts in this worker's range and ends in another's (the
+// range's last pair at most).
+__device__ void dense_odd(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, uint8_t *qs, int w, DenseWalk walk,
+                          DenseSegment g, bool more, int64_t total, int workers) {
+  const int pairs = (a.n_q + 1) / 2;
+  const bool by_pair = (int64_t)a.seqs * pairs < a.workers;
+  if (!by_pair) a.shared[w].n = 0;
   uint32_t item = 0;
   while (more) {
+    if (g.s0 == 0 && (by_pair || !g.whole)) {
+      // (a segment that reaches its pair's end is whole here)
+      const int steps = dense_steps(g.len);
+      const int64_t u0 = g.whole ? 0 : walk.end - g.s1;
+      DenseShared d;
+      d.token = g.b * a.n_q + 2 * g.pair;
+      d.tokens = 2 * g.pair + 1 < a.n_q ? 2 : 1;
+      d.slot = g.slot;
+      d.n = g.whole ? 0 : dense_worker(total, workers, u0 + steps - 1) - w + 1;
+      a.shared[by_pair ? g.b * pairs + g.pair : w] = d;
+    }
     wait_d(S, &S.q_free, item & 1u);
     ++item;
     more = dense_next(a, w, walk, g);
@@ -583,7 +599,9 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   // (Their CTAs cannot share an SM, whose shared memory each of them fills, so
   // neither can they share its tensor memory.)
   if (!a.own_lse) pdl_wait();
-  const DenseWalk walk = dense_walk(a, w, lane);
+  int64_t total;
+  int workers;
+  const DenseWalk walk = dense_walk(a, w, lane, total, workers);
   if (warp < kSoftWarps) {
     dense_softmax(a, S, tm_out, tm_part, qs, ps, w, walk, rank, tid, lane, warp);
   } else if (warp < kMmaWarpD) {
@@ -602,7 +620,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
       if (rank == 0)
         dense_products(a, S, tm_q, qs, ps, ring, tmem, w, ahead, g, more);
       else
-        dense_odd_queries(a, S, tm_q, qs, w, ahead, g, more);
+        dense_odd(a, S, tm_q, qs, w, ahead, g, more, total, workers);
     }
     __syncwarp();
   }
@@ -619,9 +637,8 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 // Merges the pairs that several workers share, with the weights exp(lse_i -
 // lse), lse the log-sum-exp over all their partials (and the other part of the
 // softmax).  With fewer pairs than workers, a group of CTAs takes each pair;
-// otherwise at most one pair lies across each range's start and a group for
-// each worker takes the pair across its start, if that is the pair's first.  A
-// CTA takes one token and 8 / a.split of its heads, a.split warps per head,
+// otherwise at most one shared pair starts in each range, and a group takes it;
+// dense_odd says which and how many partials it has.  A CTA takes one token and 8 / a.split of its heads, a.split warps per head,
 // each every a.split-th partial, four of them in flight (about as many warps
 // as bring every partial in one or two rounds: a pair has workers / pairs
 // partials).  The CTAs past the groups write the sequences without entries.
@@ -649,11 +666,10 @@ __device__ __forceinline__ void rest_rows(const DenseArgs &a, int64_t row0, int6
 
 __global__ void __launch_bounds__(256, 3) dense_combine_kernel(const DenseArgs a) {
   __shared__ float red[8][D];
-  // (n_vis is older than the dense kernel: it may be read before the wait)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t pairs = (a.n_q + 1) / 2;
-  const bool by_pair = a.seqs * pairs < a.workers;
-  const int groups = by_pair ? (int)(a.seqs * pairs) : a.workers;
+  const int64_t pairs = (int64_t)a.seqs * ((a.n_q + 1) / 2);
+  const bool by_pair = pairs < a.workers;
+  const int groups = by_pair ? (int)pairs : a.workers;
   const int heads = 8 / a.split, ctas = 2 * (H / heads);   // per CTA, per group
   const int group = blockIdx.x / ctas, cta = blockIdx.x - group * ctas;
   if (group >= groups) {
@@ -669,41 +685,20 @@ __global__ void __launch_bounds__(256, 3) dense_combine_kernel(const DenseArgs a
     }
     return;
   }
-  // the pair, its first unit and its steps
-  int b = by_pair ? (int)(group / pairs) : 0;
-  int64_t before, total, pair, u0;
-  int workers, steps;
-  dense_units(a, b, lane, before, total, workers);
-  if (by_pair) {
-    pair = group - b * pairs;
-    steps = dense_steps(dense_len(a, b));
-    if (steps == 0) return;
-    u0 = before + pair * steps;
-  } else {
-    if (group == 0 || group >= workers) return;
-    const int64_t at = dense_range(total, workers, group);
-    dense_find(a, at, lane, b, before);
-    steps = dense_steps(dense_len(a, b));
-    pair = dense_div(at - before, steps);
-    u0 = before + pair * steps;
-    if (at == u0) return;   // no pair lies across this start
-  }
-  const int w0 = dense_worker(total, workers, u0);
-  const int n = dense_worker(total, workers, u0 + steps - 1) - w0 + 1;   // partials
-  if (n == 1 || (!by_pair && w0 != group - 1)) return;   // finished by its worker; an earlier start's
-  const int r = cta & 1, hw = warp / a.split, part = warp - hw * a.split;
+  // (older than the dense kernel: read before the wait) a pair without entries
+  if (by_pair && dense_len(a, group / ((a.n_q + 1) / 2)) == 0) return;
+  pdl_wait();   // the dense kernel's partials
+  const int4 d = *reinterpret_cast<const int4 *>(a.shared + group);   // DenseShared
+  const int n = d.w, r = cta & 1;
+  if (n == 0 || r >= d.y) return;
+  const int hw = warp / a.split, part = warp - hw * a.split;
   const int head = (cta >> 1) * heads + hw;
-  const int64_t t = 2 * pair + r;
-  if (t >= a.n_q) return;
-  const int64_t row = ((int64_t)b * a.n_q + t) * H + head;
-  // partial i's row: slot 2 (w0 + i), but the first one's is odd where the
-  // pair starts inside the range
-  const int64_t row0 = ((int64_t)4 * w0 + r) * H + head;
-  const int64_t odd = dense_range(total, workers, w0) < u0 ? 2 * H : 0;
+  const int64_t row = ((int64_t)d.x + r) * H + head;
+  // partial i's row: the first one's slot, then the even ones
+  const int64_t row0 = ((int64_t)2 * (d.z & ~1) + r) * H + head, odd = (d.z & 1) * 2 * H;
   auto part_row = [&](int i) { return row0 + (int64_t)i * (4 * H) + (i == 0 ? odd : 0); };
   // this warp's partials, kMine loads in flight, the first ones beside the
   // log-sum-exps'
-  pdl_wait();   // the dense kernel's partials
   constexpr int kPer = (kDenseWorkers + 31) / 32, kMine = 4;
   uint4 v[kMine][2];
   auto load = [&](int i0) {
@@ -820,7 +815,8 @@ int64_t dense_workers(int64_t tokens, int64_t n_max) {
 }  // namespace
 
 size_t dense_scratch_bytes(int64_t tokens, int64_t n_max) {
-  return (size_t)dense_workers(tokens, n_max) * 2 * 2 * H * (D * sizeof(__half) + sizeof(float));
+  return (size_t)dense_workers(tokens, n_max) *
+         (2 * 2 * H * (D * sizeof(__half) + sizeof(float)) + sizeof(DenseShared));
 }
 
 cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n_vis, int64_t n_max, int64_t cap,
@@ -857,6 +853,7 @@ cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n
   a.own_lse = own_lse;
   a.part = static_cast<__half *>(scratch);
   a.part_lse = reinterpret_cast<float *>(a.part + (size_t)2 * a.workers * 2 * H * D);
+  a.shared = reinterpret_cast<DenseShared *>(a.part_lse + (size_t)2 * a.workers * 2 * H);
   if (most == 0) {
     const int64_t rest = (int64_t)seqs * n_q * H;
     const cudaError_t e = launch_pdl(dense_rest_kernel, dim3((unsigned)(rest < 4096 ? (rest + 7) / 8 : 512)), dim3(256), 0,

@@ -17,6 +17,13 @@ namespace csa2 {
 constexpr int kDenseStep = 256;      // entries per unit
 constexpr int kDenseWorkers = 76;    // most workers (one CTA pair per two SMs)
 
+// A pair that several workers share, for the combine: its first token, how many
+// tokens it has, its first partial's slot (the following ones are the even
+// slots of the following workers) and how many partials (0: no such pair).
+struct __align__(16) DenseShared {
+  int32_t token, tokens, slot, n;
+};
+
 struct DenseArgs {
   const __nv_bfloat16 *q;      // [seqs][n_q][64][512]
   const uint8_t *kv;           // [seqs][cap][288]
@@ -32,6 +39,7 @@ struct DenseArgs {
   const float *own_lse;        // (fp32 rows and natural log-sum-exps), or NULL
   __half *part;                // [2 workers][2 tokens][64][512] normalised partials
   float *part_lse;             // [2 workers][2 tokens][64] their natural log-sum-exps
+  DenseShared *shared;         // [workers], by pair if there are fewer pairs than workers, else by first worker
 };
 
 __device__ __forceinline__ int dense_len(const DenseArgs &a, int b) {
@@ -43,31 +51,18 @@ __device__ __forceinline__ int dense_len(const DenseArgs &a, int b) {
 
 __device__ __forceinline__ int dense_steps(int n) { return n / kDenseStep + (n % kDenseStep ? 1 : 0); }
 
-// Units of sequences [0, b) and of all sequences, and how many workers have
-// a range (a.workers, but no more than there are units: no range is empty);
-// a whole warp calls it.
-__device__ __forceinline__ void dense_units(const DenseArgs &a, int b, int lane, int64_t &before, int64_t &total,
-                                            int &workers) {
-  const int64_t pairs = (a.n_q + 1) / 2;
+// The units of all sequences, and how many workers have a range (a.workers,
+// but no more than there are units: no range is empty); a whole warp calls it.
+__device__ __forceinline__ void dense_units(const DenseArgs &a, int lane, int64_t &total, int &workers) {
+  int64_t steps = 0;
   if (!a.n_vis) {
-    before = (int64_t)b * pairs * dense_steps(a.n_max);
-    total = (int64_t)a.seqs * pairs * dense_steps(a.n_max);
-    workers = (int)(total < a.workers ? total : a.workers);
-    return;
-  }
-  int64_t x = 0, y = 0;
-  for (int i = lane; i < a.seqs; i += 32) {
-    const int s = dense_steps(dense_len(a, i));
-    y += s;
-    if (i < b) x += s;
-  }
+    steps = (int64_t)a.seqs * dense_steps(a.n_max);
+  } else {
+    for (int i = lane; i < a.seqs; i += 32) steps += dense_steps(dense_len(a, i));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    x += __shfl_xor_sync(0xffffffffu, x, o);
-    y += __shfl_xor_sync(0xffffffffu, y, o);
+    for (int o = 16; o > 0; o >>= 1) steps += __shfl_xor_sync(0xffffffffu, steps, o);
   }
-  before = x * pairs;
-  total = y * pairs;
+  total = steps * ((a.n_q + 1) / 2);
   workers = (int)(total < a.workers ? total : a.workers);
 }
 
@@ -135,7 +130,9 @@ struct DenseSegment {
   int slot;               // partial slot otherwise
 };
 
-__device__ __forceinline__ DenseWalk dense_walk(const DenseArgs &a, int w, int lane) {
+// The walk of worker w, the units of all pairs and the workers that have a
+// range; a whole warp calls it.
+__device__ __forceinline__ DenseWalk dense_walk(const DenseArgs &a, int w, int lane, int64_t &total, int &workers) {
   DenseWalk k;
   k.seq0 = 0;
   k.b = k.len = 0;
@@ -148,8 +145,8 @@ __device__ __forceinline__ DenseWalk dense_walk(const DenseArgs &a, int w, int l
       const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
       if (lane >= o) x += y;
     }
-    const int64_t total = __shfl_sync(0xffffffffu, x, 31);
-    const int workers = (int)(total < a.workers ? total : a.workers);
+    total = __shfl_sync(0xffffffffu, x, 31);
+    workers = (int)(total < a.workers ? total : a.workers);
     k.start = k.at = w < workers ? dense_range(total, workers, w) : 0;
     k.end = w < workers ? dense_range(total, workers, w + 1) : 0;
     const uint32_t past = __ballot_sync(0xffffffffu, k.at < x);
@@ -159,9 +156,7 @@ __device__ __forceinline__ DenseWalk dense_walk(const DenseArgs &a, int w, int l
       k.len = __shfl_sync(0xffffffffu, len, k.b);
     }
   } else {
-    int64_t before, total;
-    int workers;
-    dense_units(a, 0, lane, before, total, workers);
+    dense_units(a, lane, total, workers);
     k.start = k.at = w < workers ? dense_range(total, workers, w) : 0;
     k.end = w < workers ? dense_range(total, workers, w + 1) : 0;
     if (k.at < k.end) {

@@ -83,9 +83,9 @@ def test_prefix_refusals(c2, change, want):
 
 def test_workspaces(c2):
     p = c2.Params.make()
-    # two partials of two tokens (64 rows of 512 fp16 and a log-sum-exp) per
-    # worker: one worker at least, one per 256 entries of a token, 76 at most
-    unit = 2 * 2 * 64 * (512 * 2 + 4)
+    # two partials of two tokens (64 rows of 512 fp16 and a log-sum-exp) and
+    # 16 bytes for the combine per worker: one worker at least, one per 256 entries of a token, 76 at most
+    unit = 2 * 2 * 64 * (512 * 2 + 4) + 16
     for tokens, n, workers in ((1, 0, 1), (1, 256, 1), (1, 257, 2), (3, 1000, 12), (5000, 1, 76), (1 << 24, 1 << 31, 76)):
         assert c2.workspace_bytes(c2.OP_CROSS, tokens, n, p) == workers * unit
     one, many = (c2.workspace_bytes(c2.OP_PREFIX, b, 1 << 20, p) for b in (1, 65))
