@@ -449,27 +449,33 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm
       }
       const float off = kBias - m;
 #pragma unroll 1
-      for (int c = 0; c < 128; c += 32) {
-        uint32_t u[32];
-        tmem_ld32(st + c, u);
+      for (int c = 0; c < 128; c += 64) {
+        uint32_t u[2][32];
+        tmem_ld32(st + c, u[0]);
+        tmem_ld32(st + c + 32, u[1]);
         tmem_ld_wait();
-        uint32_t pk[16];
-#pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float x0 = fmaf(__uint_as_float(u[j]), kLogitD, off), x1 = fmaf(__uint_as_float(u[j + 1]), kLogitD, off);
-          if (c + 32 > valid) {
-            if (c + j >= valid) x0 = -INFINITY;
-            if (c + j + 1 >= valid) x1 = -INFINITY;
-          }
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          l += p0 + p1;
-          pk[j >> 1] = half2_bits(p0, p1);
-        }
         uint8_t *dst = prow + (c >> 6) * kAtomD;
+        float l0 = 0.0f, l1 = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          *reinterpret_cast<uint4 *>(dst + (((((c & 63) >> 3) + j) ^ (h & 7)) << 4)) =
-              make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+        for (int q = 0; q < 8; ++q) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 8 * q + 2 * j;
+            float x0 = fmaf(__uint_as_float(u[e >> 5][e & 31]), kLogitD, off);
+            float x1 = fmaf(__uint_as_float(u[e >> 5][(e & 31) + 1]), kLogitD, off);
+            if (c + 64 > valid) {
+              if (c + e >= valid) x0 = -INFINITY;
+              if (c + e + 1 >= valid) x1 = -INFINITY;
+            }
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            l0 += p0;
+            l1 += p1;
+            pk[j] = half2_bits(p0, p1);
+          }
+          *reinterpret_cast<uint4 *>(dst + ((q ^ (h & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        l += l0 + l1;
       }
       fence_proxy_async_smem();
       tc_fence_before();
