@@ -239,7 +239,9 @@ __device__ __forceinline__ uint4 decode_piece(const Piece &p) {
 // Output rows in pieces of 8 channels (16 bytes), 64 per entry and window
 // row (lane l stores pieces l and 32 + l) and 16 per indexer key (half a warp
 // each, so a warp step covers two keys).  A warp takes R consecutive steps
-// and issues all their loads before the first store.
+// and issues all their loads before the first store.  HBM bounds it for many
+// rows: 262,144 main-KV entries in order (344 MB) in 54.4 us, 6.32 TB/s, 0.93 of
+// the copy rate; few rows are a launch (1.3 us in a graph for 128 window rows).
 template <int FMT, int R>
 __global__ void __launch_bounds__(256) cache_read_kernel(const ReadArgs a) {
   pdl_wait();

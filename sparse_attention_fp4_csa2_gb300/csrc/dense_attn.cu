@@ -4,28 +4,38 @@
 //   o_h = sum_n softmax_n(q_h . k_n / sqrt(512)) k_n,
 // key = value = the dequantised 512-d entry (E2M1 x E4M3, exact in fp16).
 //
-// Per (token, entry) this is 4 * 64 * 512 flop on 288 bytes, so it is bound by
-// the tensor cores.  A pair of tokens, one per CTA of a two-CTA cluster, runs
-// on tcgen05 cta_group::2 with M = 128 (64 heads of each token) and N = 256,
-// the only single-token-per-SM shape that reaches the full rate (64 clocks per
-// K = 16 step measured; N = 128 takes 58 of its ideal 32, and a one-CTA M = 64
-// N = 256 takes 155): S = Q K^T for a step of 256 entries in 32 such steps,
-// O += P V in 2 x 16.  Each CTA then needs the keys of its half of the step
-// over all 512 channels (B of the first product), and its half of the channels
-// over all 256 keys (B of the second).  The 512-channel fp32 accumulator takes
-// half of the tensor memory and two S tiles the rest, so nothing larger fits,
-// and Q takes 64 KB of shared memory and P 32 KB, so a dequantised step cannot
-// stay until its second use: entries are dequantised twice, streamed through
-// one ring of 16 KB slots in the order in which the products consume them.
+// Per (token, entry) this is 4 * 64 * 512 flop on 288 bytes, so two tokens or
+// more are bound by the tensor cores.  A pair of tokens, one per CTA of a
+// two-CTA cluster, runs on tcgen05 cta_group::2 with M = 128 (64 heads of each
+// token) and N = 256: S = Q K^T for a step of 256 entries in 32 instructions,
+// O += P V in 32, 64 clocks each.  Each CTA then needs the keys of its half of
+// the step over all 512 channels (B of the first product) and its half of the
+// channels over all 256 keys (B of the second).  The 512-channel fp32
+// accumulator takes half of the tensor memory and two S tiles the rest, so no
+// larger tile fits; Q takes 64 KB of shared memory and P 32 KB, so a
+// dequantised step cannot stay until its second use: entries are dequantised
+// twice, streamed through one ring of 16 KB slots in the order in which the
+// products consume them.
 //
 // Warps of a CTA: 0-3 softmax (one thread per tensor-memory lane: a head and
 // half of the step's keys), 4-11 dequantisation (entries loaded into registers
-// a step ahead), 12 the products (in the even CTA) and the
-// copies of Q, which start as soon as the last product with the Q before is
-// done.  The first loads are sent before the CTA pair's set-up is awaited.
-// The products' order is
+// a step ahead), 12 the products (in the even CTA) and the copies of Q, which
+// start as soon as the last product with the Q before is done.  The first
+// loads are sent before the CTA pair's set-up is awaited.  The products' order
+// is
 //   S(0), S(1), O(0), S(2), O(1), ...
 // so that the softmax of one step runs beside the next step's first product.
+//
+// What bounds it: the L1 / shared-memory data pipe of the SM, which is full.  A
+// step passes 2,816 wavefronts of tensor-core operands (P is read once for two
+// products), 2,750 of fp16 stores (K, V, P) and 2,330 of arriving entry sectors
+// (32 bytes each) in 8,030 clocks, against 4,096 of the products alone.
+// Measured: 2 x 512 tokens over 16,384 entries 1.74 ms (1,267 TFLOP/s, 0.66 of a
+// bf16 library product's burst rate); 32 tokens over 65,536 entries 228 us
+// (1,205); one token over 65,536 30 us, of which four steps take 16 and the
+// first entries' arrival, the last rows' way out and the combine the rest.
+// Between two pairs the products rest about 3 us: the accumulator has to be read
+// out before the next pair's first product into it.
 //
 // Every wait is bounded; after one runs out every role falls through its
 // waits, the CTAs meet at the end and the output is undefined
