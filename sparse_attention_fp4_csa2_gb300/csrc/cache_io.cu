@@ -50,10 +50,11 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2(float hi, float lo) {
 // x / s by the reciprocal r = fl(1 / s) and one correction with the exact
 // remainder (P. Markstein, "Computation of elementary functions on the IBM
 // RISC System/6000 processor", 1990): the correctly rounded quotient, unless
-// it lies within 2^-46 of the middle of two floats.  s, r normal.
+// it lies within 2^-46 of the middle of two floats.  s, r normal and positive;
+// a zero keeps its sign.
 __device__ __forceinline__ float quotient(float x, float s, float r) {
   const float q = x * r;
-  return fmaf(fmaf(-q, s, x), r, q);
+  return copysignf(fmaf(fmaf(-q, s, x), r, q), x);
 }
 
 // A warp writes R rows, one after the other, all loads first.  Lane l owns

@@ -135,6 +135,25 @@ def test_swa_write_matches_torch_without_rope(c2):
     assert torch.equal(swa, (lat.float() / s[:, None]).to(torch.float8_e4m3fn).view(torch.uint8))
 
 
+def test_swa_write_every_bf16_value(c2):
+    """Every finite bf16 value, signed zeros and subnormals among them, in rows
+    of like magnitudes: the codes and scales of torch's IEEE division and cast."""
+    v = torch.arange(65536, device="cuda").to(torch.int32).to(torch.int16).view(torch.bfloat16)
+    v = v[torch.isfinite(v)]
+    v = v[v.float().abs().argsort()]
+    v = torch.cat([v, v[-(-v.numel() % D):]]).view(-1, D) if v.numel() % D else v.view(-1, D)
+    n = v.shape[0]
+    swa = torch.zeros(n, D, dtype=torch.uint8, device="cuda")
+    scale = torch.zeros(n, device="cuda")
+    c2.swa_quant_write(v.contiguous(), torch.arange(n, device="cuda"), swa, scale)
+    s = v.float().abs().amax(-1) / torch.full((), 448.0, device="cuda")
+    assert torch.equal(scale, s)
+    live = s > 0
+    y = (v.float()[live] / s[live][:, None]).clamp(-448, 448)
+    assert torch.equal(swa[live], y.to(torch.float8_e4m3fn).view(torch.uint8))
+    assert (swa[~live] == 0).all()
+
+
 def test_swa_write_skips_bad_rows(c2):
     lat = torch.ones(4, D, device="cuda").bfloat16()
     slot = torch.tensor([0, -1, 8, 2], device="cuda")
