@@ -218,6 +218,12 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
 #pragma unroll
     for (int i = 0; i < 8; ++i) load_piece(vr, i, base, len, step * kDenseStep + 32 * warp + 4 * i + key4, (int)rank);
   };
+  // A slot is free again when the products of its round before are done.  The
+  // parity alone cannot tell that round from the second one before it.  After a
+  // V round a warp has seen its own slot's barrier only, so K's waits go in slot
+  // order: slot 0's arrival comes from a V product behind every product of the
+  // K round before.  (This takes the commits of the issuing thread to arrive in
+  // order: a later slot's is four instructions or more, 256 clocks, ahead.)
   auto emit_k = [&]() {
 #pragma unroll
     for (int hc = 0; hc < 2; ++hc) {
@@ -288,6 +294,14 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
 }
 
 // ---------------------------------------------------------------- products
+// A Q copy still in flight when the roles have fallen through after a wait that
+// ran out must land before the CTA's memory goes.  Copy i completes phase i of
+// q_raw and is sent for after i - 1 has landed, so the last one's parity is
+// enough.  Bounded, and not cut short by S.abort.
+__device__ __forceinline__ void drain_q(CtlD &S, uint32_t copies) {
+  if (copies) mbar_wait(&S.q_raw, (copies - 1) & 1u);
+}
+
 // One thread of the even CTA.  `g`: the first segment, whose Q is on its way;
 // the next one's is sent for when the last S of a segment is done.
 __device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, uint8_t *qs, uint8_t *ps,
@@ -296,7 +310,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &t
   const uint64_t pd = smem_desc(smem_u32(ps), 16, 1024);
   const uint64_t kd = smem_desc(smem_u32(ring), 16, 1024);
   const uint64_t vd = smem_desc(smem_u32(ring), 4096, 1024);
-  uint32_t round = 0, item = 0, n = 0;
+  uint32_t round = 0, item = 0, n = 0, copies = more ? 1u : 0u;
   while (more) {
     const int steps = g.s1 - g.s0;
     auto scores = [&](uint32_t tile) {
@@ -325,7 +339,10 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &t
       if (i + 1 == steps) {
         more = dense_next(a, w, walk, g);
         wait_pair(S, &S.q_free, (item - 1) & 1u);
-        if (more && !S.abort) load_q(a, S, tm_q, qs, g, 0);
+        if (more && !S.abort) {
+          load_q(a, S, tm_q, qs, g, 0);
+          ++copies;
+        }
       }
       wait_pair(S, &S.p_full, n & 1u);
       tc_fence_after();
@@ -349,6 +366,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &t
   // every product has completed before the teardown, also after a wait ran out
   mma_commit_pair(&S.done);
   mbar_wait_cluster(&S.done, 0);
+  drain_q(S, copies);
 }
 
 // One thread of the odd CTA: its own token's Q, and what the combine has to
@@ -359,7 +377,7 @@ __device__ void dense_odd(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, 
   const int pairs = (a.n_q + 1) / 2;
   const bool by_pair = (int64_t)a.seqs * pairs < a.workers;
   if (!by_pair) a.shared[w].n = 0;
-  uint32_t item = 0;
+  uint32_t item = 0, copies = more ? 1u : 0u;
   while (more) {
     if (g.s0 == 0 && (by_pair || !g.whole)) {
       // (a segment that reaches its pair's end is whole here)
@@ -375,8 +393,14 @@ __device__ void dense_odd(const DenseArgs &a, CtlD &S, const CUtensorMap &tm_q, 
     wait_d(S, &S.q_free, item & 1u);
     ++item;
     more = dense_next(a, w, walk, g);
-    if (more && !S.abort) load_q(a, S, tm_q, qs, g, 1);
+    if (more && !S.abort) {
+      load_q(a, S, tm_q, qs, g, 1);
+      ++copies;
+    }
   }
+  // no product reads this CTA's memory past here, also after a wait ran out
+  mbar_wait_cluster(&S.done, 0);
+  drain_q(S, copies);
 }
 
 // ----------------------------------------------------------------- softmax
@@ -654,10 +678,11 @@ __global__ void __launch_bounds__(kThreadsD, 1)
 // lse), lse the log-sum-exp over all their partials (and the other part of the
 // softmax).  With fewer pairs than workers, a group of CTAs takes each pair;
 // otherwise at most one shared pair starts in each range, and a group takes it;
-// dense_odd says which and how many partials it has.  A CTA takes one token and 8 / a.split of its heads, a.split warps per head,
-// each every a.split-th partial, four of them in flight (about as many warps
-// as bring every partial in one or two rounds: a pair has workers / pairs
-// partials).  The CTAs past the groups write the sequences without entries.
+// dense_odd says which and how many partials it has.  A CTA takes one token
+// and 8 / a.split of its heads, a.split warps per head, each every a.split-th
+// partial, four of them in flight (about as many warps as bring every partial
+// in one or two rounds: a pair has workers / pairs partials).  The CTAs past
+// the groups write the sequences without entries.
 constexpr int kEmptyCtas = 64;
 
 __device__ __forceinline__ void put_row16(const DenseArgs &a, int64_t row, int lane, const float (&o)[16]) {
@@ -795,7 +820,7 @@ __global__ void __launch_bounds__(256, 3) dense_combine_kernel(const DenseArgs a
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4 *>(&red[warp][lane * 16 + 4 * i]) =
           make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
-    __syncthreads();   // (t, the one exit above, is the CTA's)
+    __syncthreads();   // (the exits above are taken by the whole CTA)
     // the head's warps add up a share of its channels each
     for (int c = 2 * (32 * part + lane); c < D; c += 64 * a.split) {
       float x = 0.0f, y = 0.0f;
