@@ -493,3 +493,25 @@ def test_offsets_past_32_bits(c2):
     back = torch.empty(B, 1, D, dtype=torch.bfloat16, device="cuda")
     c2.kv_read(kv, back, idx=torch.full((B, 1), cap - 1, dtype=torch.int32, device="cuda"))
     assert torch.equal(back[2, 0].double(), kv64(tail[0]))
+
+
+def test_binding_refusals_on_the_gpu(c2):
+    """Tensors of another dtype, shape, layout or device are refused before anything runs."""
+    kv = entries(c2, 8, 80).view(1, 8, ENTRY)
+    out = torch.empty(1, 4, D, dtype=torch.bfloat16, device="cuda")
+    idx = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    for bad in (dict(kv=kv[:, ::2]), dict(kv=kv.cpu()), dict(kv=kv[..., :256]), dict(out=out.float()), dict(out=out[..., ::2]),
+                dict(idx=idx.long()), dict(idx=idx[:, :3]), dict(idx=idx.cpu())):
+        a = dict(kv=kv, out=out, idx=idx) | bad
+        with pytest.raises(c2.Csa2Error):
+            c2.kv_read(a["kv"], a["out"], idx=a["idx"])
+    q = queries((1, 2), 81)
+    o = torch.empty_like(q)
+    nv = torch.tensor([8], dtype=torch.int32, device="cuda")
+    ws = c2.workspace(c2.OP_CROSS, 2, 8, c2.Params.make())
+    for bad in (dict(q=q.half()), dict(q=q.transpose(0, 1)), dict(nv=nv.long()), dict(n=9), dict(ws=ws[:1024]), dict(ws=ws[16:]),
+                dict(o=o[:, :1])):
+        a = dict(q=q, nv=nv, n=8, ws=ws, o=o) | bad
+        with pytest.raises(c2.Csa2Error):
+            c2.cross_attn(a["q"], kv, a["nv"], a["n"], a["o"], a["ws"])
+    assert c2.get_device_status() == 0
