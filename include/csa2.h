@@ -32,9 +32,10 @@
  *    allocates or frees memory.  Between calls it keeps only a per-device
  *    error word (see csa2_get_device_status), the per-thread launch count of
  *    the last call (csa2_last_launch_count), the process-wide top-K kernel
- *    choice (csa2_set_topk_kernel) and, on each device that has run
- *    csa2_hier_pool_select_static, that call's static scratch array, which
- *    holds the last call's contents.
+ *    choice (csa2_set_topk_kernel), each host thread's table of RoPE
+ *    frequencies for the last rope_theta given to csa2_swa_quant_write and, on
+ *    each device that has run csa2_hier_pool_select_static, that call's static
+ *    scratch array, which holds the last call's contents.
  *  - Every call is asynchronous on `stream` (NULL = legacy default stream) and
  *    returns CSA2_OK once its kernels are enqueued.  Host-side validation
  *    failures return an error code without launching anything.
@@ -388,12 +389,13 @@ csa2_status csa2_indexer_k_read(const uint8_t *k_fp4, int32_t batch, int64_t cap
  *   q         bf16 [batch][n_q][64][512], 16-byte aligned (|q| below 65504)
  *   kv        uint8 [batch][cap][288], 16-byte aligned (NULL when n_max is 0)
  *   n_vis     int32 [batch], 0 <= n_vis[b] <= n_max <= cap (checked on device)
- *   n_max     host-side bound on n_vis, sizes the launch
+ *   n_max     host-side bound on n_vis, sizes the launch; above 2^31 - 512, or
+ *             with batch * n_q above 2^24, CSA2_ERR_UNSUPPORTED
  *   out       bf16 [batch][n_q][64][512] (out), 16-byte aligned;
  *             lse fp32 [batch][n_q][64] or NULL (out)
- *   ws        at least csa2_workspace_bytes(CSA2_OP_CROSS, ...) bytes,
- *             256-byte aligned, any contents; calls that may overlap on the
- *             GPU need their own
+ *   ws        at least csa2_workspace_bytes(CSA2_OP_CROSS, batch * n_q, n_max,
+ *             params) bytes (any valid params), 256-byte aligned, any
+ *             contents; calls that may overlap on the GPU need their own
  * batch == 0 or n_q == 0 is a no-op.
  */
 csa2_status csa2_cross_attn(int32_t batch, int32_t n_q, const void *q, const uint8_t *kv, int64_t cap,
@@ -407,7 +409,8 @@ csa2_status csa2_cross_attn(int32_t batch, int32_t n_q, const void *q, const uin
  * {swa[b][t] : t < swa_len[b]}.  The prefix's entries are read for two
  * sequences at a time and never copied per sequence.
  *   prefix_kv uint8 [n_prefix][288], 16-byte aligned (NULL when n_prefix is 0)
- *   n_prefix  entries of the prefix, all visible to every sequence
+ *   n_prefix  entries of the prefix, all visible to every sequence; above
+ *             2^31 - 512 CSA2_ERR_UNSUPPORTED
  *   out       bf16 [batch][64][512] (out), 16-byte aligned; lse fp32 [batch][64] or NULL
  *   ws        at least csa2_workspace_bytes(CSA2_OP_PREFIX, batch, n_prefix,
  *             params) bytes, 256-byte aligned, any contents; calls that may

@@ -37,6 +37,9 @@ __device__ __forceinline__ uint32_t smem_u32(const void *p) {
 // calls it before its first global-memory access and before it allocates
 // tensor memory, so a CTA dispatched early holds only shared memory and
 // registers while it waits, and no two kernels past their waits run at once.
+// (One exception: the dense readout behind the sparse readout of the same call
+// reads only what was complete before that one started, and waits where it
+// merges the two and at its end; their CTAs cannot share an SM.)
 // pdl_release (griddepcontrol.launch_dependents) lets the next kernel's CTAs
 // be dispatched once every CTA of this grid has issued it or exited (the
 // first thread of a CTA to issue it counts for the CTA).  The readout
