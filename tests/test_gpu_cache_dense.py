@@ -515,3 +515,45 @@ def test_binding_refusals_on_the_gpu(c2):
         with pytest.raises(c2.Csa2Error):
             c2.cross_attn(a["q"], kv, a["nv"], a["n"], a["o"], a["ws"])
     assert c2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("batch,n_prefix", [(201, 300), (153, 256), (305, 1)])
+def test_prefix_odd_batch_with_whole_pairs(c2, batch, n_prefix):
+    """More pairs than workers: most pairs are whole in one range and merged with
+    their own part there, the last pair has one token, some own parts are empty."""
+    own = [((16, 8), (0, 0), (3, 0), (0, 5))[b % 4] for b in range(batch)]
+    args = prefix_inputs(c2, batch, n_prefix, 16, 8, 90, own)
+    out, lse = run_prefix(c2, *args)
+    assert c2.get_device_status() == 0
+    check_out(out, lse, *prefix_ref(*args[1:]))
+
+
+@pytest.mark.parametrize("batch,n_q,cap,lens", [(3, 3, 700, [257, 0, 700]), (1, 1, 600, [511]), (90, 3, 300, None)])
+def test_cross_attn_stays_inside_its_buffers(c2, batch, n_q, cap, lens):
+    """A workspace of exactly the size asked for, outputs between guard rows, and
+    every byte past a sequence's length 0xFF (scales that are NaN)."""
+    lens = lens or [(37 * b) % (cap + 1) for b in range(batch)]
+    kv = entries(c2, batch * cap, 95).view(batch, cap, ENTRY)
+    for b, n in enumerate(lens):
+        kv[b, n:] = 0xFF
+    q = queries((batch, n_q), 96)
+    rows = batch * n_q
+    out = torch.full((rows + 2, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((rows + 2, H), 7.0, device="cuda")
+    size = c2.workspace_bytes(c2.OP_CROSS, rows, cap, c2.Params.make())
+    buf = torch.full((size + 512,), 0xAB, dtype=torch.uint8, device="cuda")
+    start = -buf.data_ptr() % 256
+    ws = buf[start:start + size]
+    nv = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    c2.cross_attn(q, kv, nv, cap, out[1:-1].view(batch, n_q, H, D), ws, lse=lse[1:-1].view(batch, n_q, H))
+    assert c2.get_device_status() == 0
+    assert (buf[:start] == 0xAB).all() and (buf[start + size:] == 0xAB).all()
+    assert (out[0] == 7).all() and (out[-1] == 7).all() and (lse[0] == 7).all() and (lse[-1] == 7).all()
+    for b, n in enumerate(lens):
+        o, l = out[1:-1].view(batch, n_q, H, D)[b], lse[1:-1].view(batch, n_q, H)[b]
+        if n == 0:
+            assert (o == 0).all() and (l == -float("inf")).all()
+            continue
+        for t in range(n_q):
+            ro, rl = attend64(q[b, t].double(), kv64(kv[b, :n]))
+            check_out(o[t][None], l[t][None], ro[None], rl[None])
