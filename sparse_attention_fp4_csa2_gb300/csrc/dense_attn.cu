@@ -30,9 +30,9 @@
 // step passes 2,816 wavefronts of tensor-core operands (P is read once for two
 // products), 2,750 of fp16 stores (K, V, P) and 2,330 of arriving entry sectors
 // (32 bytes each) in 8,030 clocks, against 4,096 of the products alone.
-// Measured: 2 x 512 tokens over 16,384 entries 1.74 ms (1,267 TFLOP/s, 0.66 of a
-// bf16 library product's burst rate); 32 tokens over 65,536 entries 228 us
-// (1,205); one token over 65,536 30 us, of which four steps take 16 and the
+// Measured: 2 x 512 tokens over 16,384 entries 1.67 ms (1,320 TFLOP/s, 0.69 of a
+// bf16 library product's burst rate); 32 tokens over 65,536 entries 226 us
+// (1,216); one token over 65,536 30 us, of which four steps take 16 and the
 // first entries' arrival, the last rows' way out and the combine the rest.
 // Between two pairs the products rest about 3 us: the accumulator has to be read
 // out before the next pair's first product into it.
