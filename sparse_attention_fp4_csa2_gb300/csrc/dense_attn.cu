@@ -41,6 +41,7 @@
 // waits, the CTAs meet at the end and the output is undefined
 // (CSA2_DEV_ERR_TIMEOUT).
 #include "dense_plan.cuh"
+#include "dense_ring.h"
 
 namespace csa2 {
 
@@ -65,7 +66,8 @@ constexpr uint32_t kIdescS = idesc_f16(0, 0, 0, 256, 128);
 constexpr uint32_t kIdescO = idesc_f16(0, 0, /*B MN-major*/ 1, 256, 128);
 
 struct __align__(16) CtlD {
-  uint64_t full[kSlots], free[kSlots];        // full, q_full, p_full: both CTAs arrive at the even CTA
+  uint64_t full[kSlots];                      // full, q_full, p_full: both CTAs arrive at the even CTA
+  uint64_t free[kRingSets][kSlots];
   uint64_t q_raw, q_full, q_free, s_full[2], p_full, p_free, done;
   uint32_t tmem_base;
   volatile uint32_t abort;
@@ -218,18 +220,15 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
 #pragma unroll
     for (int i = 0; i < 8; ++i) load_piece(vr, i, base, len, step * kDenseStep + 32 * warp + 4 * i + key4, (int)rank);
   };
-  // A slot is free again when the products of its round before are done.  The
-  // parity alone cannot tell that round from the second one before it.  After a
-  // V round a warp has seen its own slot's barrier only, so K's waits go in slot
-  // order: slot 0's arrival comes from a V product behind every product of the
-  // K round before.  (This takes the commits of the issuing thread to arrive in
-  // order: a later slot's is four instructions or more, 256 clocks, ahead.)
+  // A slot is free again when the products of its round before are done (in
+  // every wait of dense_ring.h's protocol the round before is the one meant).
+  auto wait_free = [&](int s) { wait_d(S, &S.free[ring_set(round - 1)][s], ring_parity(round - 1)); };
   auto emit_k = [&]() {
 #pragma unroll
     for (int hc = 0; hc < 2; ++hc) {
       if (round)
 #pragma unroll
-        for (int s = 0; s < 4; ++s) wait_d(S, &S.free[4 * hc + s], (round - 1) & 1u);
+        for (int s = 0; s < 4; ++s) wait_free(4 * hc + s);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         put32((k_at + (uint32_t)(4 * hc * kSlotBytes + i * 512)) ^ (uint32_t)((i & 1) << 6), kr.v[4 * hc + i],
@@ -241,7 +240,7 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
     ++round;
   };
   auto emit_v = [&]() {
-    if (round) wait_d(S, &S.free[warp], (round - 1) & 1u);
+    if (round) wait_free(warp);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       put32((v_at + (uint32_t)(i * 512)) ^ (uint32_t)((i & 1) << 6), vr.v[i], vr.sc[i], o1, o2);
@@ -290,7 +289,7 @@ __device__ void dense_dequant(const DenseArgs &a, CtlD &S, uint8_t *qs, uint8_t 
   // arrive here, before the CTA ends
   if (round)
 #pragma unroll 1
-    for (int s = 0; s < kSlots; ++s) wait_d(S, &S.free[s], (round - 1) & 1u);
+    for (int s = 0; s < kSlots; ++s) wait_free(s);
 }
 
 // ---------------------------------------------------------------- products
@@ -321,7 +320,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &t
         const uint64_t qa = qd + (uint64_t)(s * kAtomD >> 4), kb = kd + (uint64_t)(s * kSlotBytes >> 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) mma_f16_pair(tmem + tile * 128, qa + 2 * i, kb + 2 * i, kIdescS, (s | i) ? 1u : 0u);
-        mma_commit_pair(&S.free[s]);
+        mma_commit_pair(&S.free[ring_set(round)][s]);
       }
       ++round;
       mma_commit_pair(&S.s_full[tile]);
@@ -357,7 +356,7 @@ __device__ void dense_products(const DenseArgs &a, CtlD &S, const CUtensorMap &t
         mma_f16_pair_a_last(tmem + kColOut + 128, pa, vb + 512, kIdescO, acc);
         mma_f16_pair_a_fill(tmem + kColOut, pa + 2, vb + 128, kIdescO, 1u);
         mma_f16_pair_a_last(tmem + kColOut + 128, pa + 2, vb + 512 + 128, kIdescO, 1u);
-        mma_commit_pair(&S.free[s]);
+        mma_commit_pair(&S.free[ring_set(round)][s]);
       }
       ++round;
       mma_commit_pair(&S.p_free);
@@ -617,7 +616,7 @@ __global__ void __launch_bounds__(kThreadsD, 1)
   if (warp == kMmaWarpD && lane == 0) {
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&S.full[s], 2 * kDeqWarps);
-      mbar_init(&S.free[s], 1);
+      for (int i = 0; i < kRingSets; ++i) mbar_init(&S.free[i][s], 1);
     }
     mbar_init(&S.q_raw, 1);
     mbar_init(&S.q_full, 2 * kDeqWarps);
