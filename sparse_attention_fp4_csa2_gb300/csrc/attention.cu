@@ -14,9 +14,8 @@
 // to fill the SMs -- one of C <= 8 chunks of them (a chunk takes an equal
 // share of the top-K list and of the SWA rows).  With C = 1 the CTAs are
 // persistent and walk the items; with C > 1 the C chunks of a token are the
-// CTAs of one thread-block cluster: each loads a share of the token's Q for
-// all of them (TMA multicast), and they merge their partial results through
-// distributed shared memory.
+// CTAs of one thread-block cluster, which merge their partial results through
+// distributed shared memory (each loads the token's Q for itself).
 //
 // Inside a CTA an item's keys go through in blocks of up to 128 (a single
 // block of up to 160 when every CTA holds one item).  Per block:
@@ -485,22 +484,6 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, Ctl &S, const CUtensor
   }
 }
 
-// C > 1: the cluster's CTAs share one token, so CTA `rank` loads the column
-// pairs p = rank (mod C) once for all of them (multicast); every CTA armed
-// its four Q barriers before the cluster barrier that precedes this call.
-__device__ __forceinline__ void load_q_cluster(const AttnArgs &a, Ctl &S, const CUtensorMap &tm_q, uint8_t *qs,
-                                               int item) {
-  const int tok = item / a.C;
-  const int rank = item - tok * a.C;
-  const int64_t gp = a.p0 + tok;
-  const uint16_t mask = (uint16_t)((1u << a.C) - 1u);
-#pragma unroll 1
-  for (int p = rank; p < 4; p += a.C) {
-    tma_load_2d_mc(qs + 2 * p * kAtom, &tm_q, 2 * p * 64, (int32_t)(gp * H), &S.q_full[p], mask);
-    tma_load_2d_mc(qs + (2 * p + 1) * kAtom, &tm_q, (2 * p + 1) * 64, (int32_t)(gp * H), &S.q_full[p], mask);
-  }
-}
-
 template <bool kSingle>
 __global__ void __launch_bounds__(kThreads, 1)
     sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const AttnArgs a) {
@@ -519,10 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first_item = blockIdx.x;
   const int stride = gridDim.x;
 
-  // The MMA warp's lane 0 sets up the barriers first.  C > 1: a cluster
-  // barrier then orders every CTA's set-up before any Q multicast into it;
-  // every thread arrives at once and awaits it once later (before its next
-  // arrive).
+  // The MMA warp's lane 0 sets up the barriers first.  C > 1: the combine's
+  // first cluster barrier orders every CTA's set-up before another one's
+  // copies into it.
   if (warp == kMmaWarp && lane == 0) {
     for (int p = 0; p < 4; ++p) {
       mbar_init(&S.q_full[p], 1);
@@ -539,14 +521,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&S.cols_free[p], 1);
     }
     S.abort = 0;
-    // C > 1: Q arrives by multicast from the cluster's CTAs (one item per CTA)
-    if (a.C > 1)
-      for (int p = 0; p < 4; ++p) mbar_arrive_expect_tx(&S.q_full[p], (uint32_t)(2 * kAtom));
     fence_barrier_init();
     prefetch_tmap(&tm_q);
   }
   __syncwarp();
-  if (a.C > 1) cluster_arrive();
   // the previous kernel in the stream is complete past here (programmatic
   // launch: everything above touches only this CTA's shared memory)
   pdl_enter();
@@ -571,13 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     tmem_alloc(&S.tmem_base, kTmemCols);
     tmem_relinquish();
-    if (a.C > 1) cluster_wait();
-    if (lane == 0 && first_item < items) {
-      if (a.C > 1)
-        load_q_cluster(a, S, tm_q, qs, first_item);
-      else
-        load_q(a, S, tm_q, qs, first_item);
-    }
+    if (lane == 0 && first_item < items) load_q(a, S, tm_q, qs, first_item);
   }
   RowBuf b0;
   b0.kind = 0;
@@ -604,7 +576,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int r = 128 + (ht >> 1), hcp = ht & 1;
       const bool rows = ht < 64 && first_item < items && r < a.Bk;   // loaded into b0 at the start
       __syncwarp();
-      if (a.C > 1) cluster_wait();
       if (first_item < items) {
 #pragma unroll 1
         for (int p = 0; p < 4; ++p) {
@@ -627,7 +598,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     } else {
       __syncwarp();
-      if (a.C > 1) cluster_wait();
       uint32_t n = 0;
       for (int item = first_item; item < items; item += stride, ++n) {
 #pragma unroll 1
@@ -722,9 +692,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-    if (a.C > 1) cluster_wait();
     if constexpr (kSingle) {
-      // Q (multicast or local TMA) lands before the gathered rows: this
+      // Q lands before the gathered rows: this
       // thread's share of it first, while the rows are on their way
       if (first_item < items) {
 #pragma unroll 1

@@ -225,18 +225,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst, const void *tmap, int32_t
       : "memory");
 }
 
-// The same box delivered to every CTA of the cluster in `mask`, at the same
-// shared-memory offset, each arrival counted on that CTA's barrier at `bar`'s
-// offset (so every destination's barrier must be initialised first).
-__device__ __forceinline__ void tma_load_2d_mc(void *dst, const void *tmap, int32_t x, int32_t y, uint64_t *bar,
-                                               uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
-      "[%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(smem_u32(bar)), "h"(mask)
-      : "memory");
-}
-
 // 2-D tiled tensor copy shared -> global (box and swizzle from the tensor map)
 // as part of the thread's current bulk group.  x and y not negative, x *
 // elem_size a multiple of 16 bytes.
