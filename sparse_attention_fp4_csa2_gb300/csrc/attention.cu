@@ -329,6 +329,10 @@ __device__ __forceinline__ void cluster_combine(const AttnArgs &a, Ctl &S, uint8
   const int q4 = warp & 3, wh = warp >> 2;
   const uint32_t s_row = tmem + ((uint32_t)(32 * q4) << 16);
 
+  // inv_l / mfin / lfin, which warps 0 .. 3 wrote, are visible (the products'
+  // end alone does not say so: a chunk without keys takes the divide's slow
+  // path, whose first fetch of instructions can outlast them)
+  bar_named(1, kWorkers);
   if (tid == 0) mbar_arrive_expect_tx(&S.comb, (uint32_t)(C - 1) * (slot + 2 * H * 4));
   if (tid < H) {
     mlr[rank][0][tid] = S.mfin[tid];   // sent to the peers from here, and this CTA's own
