@@ -157,6 +157,9 @@ __global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat1
         for (int j = 0; j < 4; ++j)
           if (j == i >> 1) q[j] |= c;
       }
+    } else {   // zeros, but a NaN beside nothing else stays one
+#pragma unroll
+      for (int i = 0; i < 16; ++i) q[i >> 2] |= (x[i] != x[i] ? 0x7Fu : 0u) << (8 * (i & 3));
     }
     *reinterpret_cast<uint4 *>(swa + row[r] * D + lane * 16) = make_uint4(q[0], q[1], q[2], q[3]);
     if (lane == 0) swa_scale[row[r]] = scale;
