@@ -30,7 +30,7 @@
 // step passes 2,816 wavefronts of tensor-core operands (P is read once for two
 // products), 2,750 of fp16 stores (K, V, P) and 2,330 of arriving entry sectors
 // (32 bytes each) in 8,030 clocks, against 4,096 of the products alone.
-// Measured: 2 x 512 tokens over 16,384 entries 1.67 ms (1,320 TFLOP/s, 0.69 of a
+// Measured: 2 x 512 tokens over 16,384 entries 1.66 ms (1,325 TFLOP/s, 0.69 of a
 // bf16 library product's burst rate); 32 tokens over 65,536 entries 226 us
 // (1,216); one token over 65,536 30 us, of which four steps take 16 and the
 // first entries' arrival, the last rows' way out and the combine the rest.
@@ -58,9 +58,11 @@ constexpr int kAtomD = H * 128;               // 64 rows x 128 bytes (Q, P)
 constexpr uint32_t kColOut = 256;             // tensor memory: S tiles at 0 and 128, O at 256
 constexpr float kLogitD = 0.06375871295460785f;   // log2(e) / sqrt(512)
 constexpr float kLn2D = 0.69314718055994531f;
-// P = 2^(x - m + kBias) with a reference m that is raised only when a step
-// exceeds it by 2^kLazyD: at most 2^15 (fp16), and a key 2^-31 below the
-// reference still counts, so 64K such keys lose less than 2^-15 of the sum.
+// P = 2^((s - m) kLogitD + kBias), s = q . k, with a reference m that is raised
+// only when a step exceeds it by 2^kLazyD: at most 2^15 (fp16), and a key 2^-31
+// below the reference still counts, so 64K such keys lose less than 2^-15 of
+// the sum.  The difference comes before the scale: of scaled products of 2^24
+// and more, one rounding against the reference is whole powers of two.
 constexpr float kLazyD = 8.0f, kBias = 7.0f;
 constexpr uint32_t kIdescS = idesc_f16(0, 0, 0, 256, 128);
 constexpr uint32_t kIdescO = idesc_f16(0, 0, /*B MN-major*/ 1, 256, 128);
@@ -456,16 +458,16 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm
       }
       S.red[n & 1u][tid] = mx;
       bar_named(1, 128);
-      mx = fmaxf(mx, S.red[n & 1u][tid ^ 64]) * kLogitD;
+      mx = fmaxf(mx, S.red[n & 1u][tid ^ 64]);
       // O(n - 1) is complete: P is free, O may be rescaled
       if (n) wait_d(S, &S.p_free, (n - 1) & 1u);
       tc_fence_after();
       if (i == g.s0) {
         m = mx;
       } else {
-        const bool raise = mx > m + kLazyD;
+        const bool raise = mx > m + kLazyD / kLogitD;
         if (__any_sync(0xffffffffu, raise)) {
-          const float f = raise ? ex2_approx(m - mx) : 1.0f;
+          const float f = raise ? ex2_approx((m - mx) * kLogitD) : 1.0f;
           if (raise) m = mx;
           l *= f;
 #pragma unroll 1
@@ -480,7 +482,6 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm
           tmem_st_wait();
         }
       }
-      const float off = kBias - m;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 64) {
         uint32_t u[2][32];
@@ -495,8 +496,10 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int e = 8 * q + 2 * j;
-            float x0 = fmaf(__uint_as_float(u[e >> 5][e & 31]), kLogitD, off);
-            float x1 = fmaf(__uint_as_float(u[e >> 5][(e & 31) + 1]), kLogitD, off);
+            float x0, x1;
+            f32x2_unpack(f32x2_fma(f32x2_add(f32x2_pack(__uint_as_float(u[e >> 5][e & 31]),
+                                                        __uint_as_float(u[e >> 5][(e & 31) + 1])), f32x2_pack(-m, -m)),
+                                   f32x2_pack(kLogitD, kLogitD), f32x2_pack(kBias, kBias)), x0, x1);
             if (c + 64 > valid) {
               if (c + e >= valid) x0 = -INFINITY;
               if (c + e + 1 >= valid) x1 = -INFINITY;
@@ -520,7 +523,7 @@ __device__ void dense_softmax(const DenseArgs &a, CtlD &S, const CUtensorMap &tm
     bar_named(1, 128);
     l += S.red[n & 1u][tid ^ 64];
     bar_named(1, 128);   // red is written again by the next step
-    const float lse = (m - kBias + log2f(l)) * kLn2D;
+    const float lse = (m * kLogitD + (log2f(l) - kBias)) * kLn2D;
     more = dense_next(a, w, walk, next);
     wait_d(S, &S.p_free, (n - 1) & 1u);
     tc_fence_after();

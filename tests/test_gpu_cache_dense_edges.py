@@ -4,7 +4,8 @@ import math
 import pytest
 import torch
 
-from test_gpu_cache_dense import D, c2  # noqa: F401
+from test_gpu_cache_dense import (D, ENTRY, H, attend64, c2, check_out, entries, gen, kv64, prefix_inputs, prefix_ref,  # noqa: F401
+                                  queries, run_cross, run_prefix)
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +36,61 @@ def test_swa_write_nan_beside_zeros(c2, n):  # noqa: F811
     out = torch.empty(1, n, D, dtype=torch.bfloat16, device="cuda")
     c2.swa_read(swa.view(1, n, D), scale.view(1, n), out)
     assert torch.equal(torch.isnan(out[0]), want) and (out[0][~want] == 0).all()
+
+
+# ------------------------------------------------------------------- dense
+# factors on the queries (of the head's sharpness, 0.5 to 3) and the entries'
+# standard deviation: next to no logits at all, the usual ones, one key that takes
+# everything, logits past 2^28 (where a step of fp32 is whole powers of e)
+SCALES = [(1e-3, 1.0), (1.0, 0.01), (0.05, 100.0), (300.0, 30.0), (20000.0, 800.0)]
+
+
+@pytest.mark.parametrize("q_scale,std", SCALES)
+def test_cross_attn_of_any_size(c2, q_scale, std):  # noqa: F811
+    n, T = 1500, 3
+    kv = entries(c2, n, 100, std)
+    q = (queries((1, T), 101).float() * q_scale).clamp(-65000, 65000).bfloat16()
+    out, lse = run_cross(c2, q, kv.view(1, n, ENTRY), torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+    assert c2.get_device_status() == 0
+    check_out(out, lse, *attend64(q[0].double().view(-1, D), kv64(kv)))
+
+
+@pytest.mark.parametrize("q_scale,std", SCALES)
+def test_prefix_attn_of_any_size(c2, q_scale, std):  # noqa: F811
+    p, q, pre, kv, idx, swa, sc, sl = prefix_inputs(c2, 3, 900, 64, 16, 110, [(64, 16), (0, 0), (5, 1)])
+    pre = entries(c2, 900, 111, std)
+    kv = entries(c2, kv.shape[0] * kv.shape[1], 112, std).view_as(kv)
+    sc = sc * std
+    q = (q.float() * q_scale).clamp(-65000, 65000).bfloat16()
+    args = (q, pre, kv, idx, swa, sc, sl)
+    out, lse = run_prefix(c2, p, *args)
+    assert c2.get_device_status() == 0
+    check_out(out, lse, *prefix_ref(*args))
+
+
+@pytest.mark.parametrize("prefix", [False, True])
+def test_logits_past_two_to_the_29(c2, prefix):  # noqa: F811
+    """Queries and entries near the ends of their ranges: each head's logit for
+    one key, or for two equal ones, is about 3e9, the others' far below, and the
+    output is that key."""
+    n, K = 700, 64
+    g = gen(120)
+    sign = torch.where(torch.rand(H, D, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+    lat = torch.randn(n, D, generator=g, device="cuda") * 20
+    at = torch.randperm(n - 1, generator=g, device="cuda")[:H]
+    lat[at] = sign * 2000
+    lat[n - 1] = lat[at[0]]            # head 0 has two
+    pre = torch.zeros(n, ENTRY, dtype=torch.uint8, device="cuda")
+    rows = torch.arange(n, device="cuda")
+    c2.kv_quant_write(lat.bfloat16(), None, 1, torch.zeros_like(rows), rows, pre)
+    q = (sign * 60000).bfloat16()[None]
+    if prefix:
+        p, _, _, kv, idx, swa, sc, sl = prefix_inputs(c2, 1, 0, K, 8, 121)
+        args = (q, pre, kv, idx, swa, sc, sl)
+        out, lse = run_prefix(c2, p, *args)
+        ref = prefix_ref(*args)
+    else:
+        out, lse = run_cross(c2, q[None], pre[None], torch.tensor([n], dtype=torch.int32, device="cuda"), n)
+        ref = attend64(q[0].double(), kv64(pre))
+    assert c2.get_device_status() == 0
+    check_out(out, lse, *ref)
