@@ -171,10 +171,22 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// half2 (a pair of decoded codes) times an fp32 scale, rounded once to bf16.
+// x s rounded to odd: of the two floats around the product, which differ by
+// one in the last place unless it is exact, the one whose last bit is set (S.
+// Boldo, G. Melquiond, "Emulation of FMA and correctly rounded sums: proved
+// algorithms using rounding to odd", 2008).  A second rounding to fewer bits
+// is then the product's own.
+__device__ __forceinline__ float mul_odd(float x, float s) {
+  const float down = __fmul_rd(x, s), up = __fmul_ru(x, s);
+  return __float_as_uint(down) & 1 ? down : up;
+}
+
+// half2 (a pair of decoded codes) times a scale, rounded once to bf16.
+// EXACT: the products have at most 24 bits (E2M1 codes).
+template <bool EXACT>
 __device__ __forceinline__ uint32_t scaled_bf16x2(uint32_t h2, float scale) {
   const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h2));
-  return bf16x2(f.x * scale, f.y * scale);
+  return EXACT ? bf16x2(f.x * scale, f.y * scale) : bf16x2(mul_odd(f.x, scale), mul_odd(f.y, scale));
 }
 
 // UE8M0 byte -> 2^(b - 127) (255 is NaN).
@@ -236,8 +248,9 @@ __device__ __forceinline__ uint4 decode_piece(const Piece &p) {
   } else {
     e2m1x8_to_half2x4(p.c.x, h);
   }
-  return make_uint4(scaled_bf16x2(h[0], p.scale), scaled_bf16x2(h[1], p.scale), scaled_bf16x2(h[2], p.scale),
-                    scaled_bf16x2(h[3], p.scale));
+  constexpr bool kExact = FMT != kFmtSwa;
+  return make_uint4(scaled_bf16x2<kExact>(h[0], p.scale), scaled_bf16x2<kExact>(h[1], p.scale),
+                    scaled_bf16x2<kExact>(h[2], p.scale), scaled_bf16x2<kExact>(h[3], p.scale));
 }
 
 // Output rows in pieces of 8 channels (16 bytes), 64 per entry and window

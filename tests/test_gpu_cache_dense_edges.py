@@ -38,6 +38,52 @@ def test_swa_write_nan_beside_zeros(c2, n):  # noqa: F811
     assert torch.equal(torch.isnan(out[0]), want) and (out[0][~want] == 0).all()
 
 
+# ----------------------------------------------------------------- reading
+def bf16_of(v):
+    """64-bit values rounded once to bf16 (nearest even), as 64-bit values."""
+    step = torch.exp2((torch.frexp(v).exponent - 8).clamp_min(-133).double())
+    r = torch.round(v / step) * step
+    return torch.where(r.abs() > float(torch.finfo(torch.bfloat16).max), torch.copysign(torch.full_like(r, math.inf), r), r)
+
+
+def test_swa_read_rounds_once(c2):  # noqa: F811
+    """Scales that put code x scale next to the middle of two bf16 values, from
+    subnormal products to the largest, and every finite code."""
+    g = gen(130)
+    codes = torch.tensor([c for c in range(256) if c & 127 != 127], dtype=torch.uint8, device="cuda")
+    val = codes.view(torch.float8_e4m3fn).double()
+    n = 4000
+    pick = torch.randint(0, codes.numel(), (n,), generator=g, device="cuda")
+    mid = (torch.randint(128, 256, (n,), generator=g, device="cuda").double() + 0.5) * torch.exp2(
+        torch.randint(-140, 120, (n,), generator=g, device="cuda").double())
+    mid[:8] = torch.tensor([0.0, 2.0 ** -149, 2.0 ** -134, 3.4e38, 0.094815336 * 11, 0.88920456 * 11, 1.0, 2.0 ** -126], dtype=torch.float64)
+    pick[4:6] = int((val == 11).nonzero()[0])
+    scale = torch.where(val[pick] != 0, mid / val[pick].abs().clamp_min(2.0 ** -9), mid).float().abs()
+    swa = codes[torch.randint(0, codes.numel(), (n, D), generator=g, device="cuda")]
+    swa[:, :codes.numel()] = codes
+    swa[:, 300:400] = codes[pick][:, None]
+    out = torch.empty(1, n, D, dtype=torch.bfloat16, device="cuda")
+    c2.swa_read(swa.view(1, n, D), scale.view(1, n), out)
+    exact = swa.view(torch.float8_e4m3fn).double() * scale.double()[:, None]   # 28 bits
+    want = bf16_of(exact)
+    nan = torch.isnan(want)   # zero codes under the few scales that overflow to infinity
+    assert torch.equal(torch.isnan(out[0]), nan)
+    assert torch.equal(out[0].double()[~nan], want[~nan])
+    assert torch.equal(torch.signbit(out[0])[~nan], torch.signbit(exact)[~nan])
+    # the case is worth its name: a product rounded to fp32 first gives other values
+    assert (exact.float().bfloat16().double() != want)[~nan].any()
+
+
+def test_swa_read_infinities_and_nans(c2):  # noqa: F811
+    swa = torch.zeros(1, 3, D, dtype=torch.uint8, device="cuda")
+    swa[..., 1], swa[..., 2], swa[..., 3] = 0x38, 0xB8, 0x7F   # 1, -1, NaN
+    out = torch.empty(1, 3, D, dtype=torch.bfloat16, device="cuda")
+    c2.swa_read(swa, torch.tensor([[1.0, math.inf, math.nan]], device="cuda"), out)
+    assert out[0, 0, 1] == 1 and out[0, 0, 2] == -1 and torch.isnan(out[0, 0, 3])
+    assert out[0, 1, 1] == math.inf and out[0, 1, 2] == -math.inf and torch.isnan(out[0, 1, [0, 3]]).all()
+    assert torch.isnan(out[0, 2]).all()
+
+
 # ------------------------------------------------------------------- dense
 # factors on the queries (of the head's sharpness, 0.5 to 3) and the entries'
 # standard deviation: next to no logits at all, the usual ones, one key that takes
