@@ -389,7 +389,8 @@ csa2_status csa2_indexer_k_read(const uint8_t *k_fp4, int32_t batch, int64_t cap
  * read, whatever they hold.
  *   q         bf16 [batch][n_q][64][512], 16-byte aligned (|q| below 65504)
  *   kv        uint8 [batch][cap][288], 16-byte aligned (NULL when n_max is 0)
- *   n_vis     int32 [batch], 0 <= n_vis[b] <= n_max <= cap (checked on device)
+ *   n_vis     int32 [batch], 0 <= n_vis[b] <= n_max <= cap (checked on device);
+ *             the result is undefined if it changes while the call runs
  *   n_max     host-side bound on n_vis, sizes the launch; above 2^31 - 512, or
  *             with batch * n_q above 2^24, CSA2_ERR_UNSUPPORTED
  *   out       bf16 [batch][n_q][64][512] (out), 16-byte aligned;

@@ -77,14 +77,16 @@ __device__ __forceinline__ int64_t dense_range(int64_t total, int workers, int w
   return dense_div(total * w, workers);
 }
 
-// The worker whose range holds unit u.
+// The worker whose range holds unit u (the last one for any u past the line).
 __device__ __forceinline__ int dense_worker(int64_t total, int workers, int64_t u) {
-  return (int)dense_div((u + 1) * workers - 1, total);
+  return u < total ? (int)dense_div((u + 1) * workers - 1, total) : workers - 1;
 }
 
 // The sequence that holds unit u and its first unit; a whole warp calls it (32
 // lengths at a time: with a length per step, the last worker of 4,096 short
-// sequences would set out 80 us late).
+// sequences would set out 80 us late).  b = a.seqs if the lengths have shrunk
+// since they were counted: this walk and dense_next end then, whatever n_vis
+// holds while the call runs.
 __device__ __forceinline__ void dense_find(const DenseArgs &a, int64_t u, int lane, int &b, int64_t &seq0) {
   const int64_t pairs = (a.n_q + 1) / 2;
   if (!a.n_vis) {
@@ -94,7 +96,7 @@ __device__ __forceinline__ void dense_find(const DenseArgs &a, int64_t u, int la
     return;
   }
   int64_t base = 0;
-  for (int c = 0;; c += 32) {   // u is a unit: some sequence below holds it
+  for (int c = 0; c < a.seqs; c += 32) {
     int64_t x = c + lane < a.seqs ? pairs * dense_steps(dense_len(a, c + lane)) : 0;
     const int64_t own = x;
 #pragma unroll
@@ -111,6 +113,8 @@ __device__ __forceinline__ void dense_find(const DenseArgs &a, int64_t u, int la
     }
     base += __shfl_sync(0xffffffffu, x, 31);
   }
+  b = a.seqs;
+  seq0 = base;
 }
 
 // A worker's walk over its range, one segment (a pair and its steps inside
@@ -161,7 +165,10 @@ __device__ __forceinline__ DenseWalk dense_walk(const DenseArgs &a, int w, int l
     k.end = w < workers ? dense_range(total, workers, w + 1) : 0;
     if (k.at < k.end) {
       dense_find(a, k.at, lane, k.b, k.seq0);
-      k.len = dense_len(a, k.b);
+      if (k.b < a.seqs)
+        k.len = dense_len(a, k.b);
+      else
+        k.end = k.at;
     }
   }
   k.steps = dense_steps(k.len);
@@ -173,6 +180,7 @@ __device__ __forceinline__ bool dense_next(const DenseArgs &a, int w, DenseWalk 
   if (k.at >= k.end) return false;
   const int64_t pairs = (a.n_q + 1) / 2;
   while (k.at >= k.seq0 + pairs * k.steps) {   // at < end <= total: some sequence holds it
+    if (k.b + 1 >= a.seqs) return false;
     k.seq0 += pairs * k.steps;
     ++k.b;
     k.len = dense_len(a, k.b);
