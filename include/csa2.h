@@ -339,11 +339,11 @@ csa2_status csa2_hier_pool_select_static(const float *block_scores, const int32_
  * local cache stays FP8; [N] section 4), in the form csa2_sparse_attn reads.
  *   For row i: x = latent[i], with RoPE on channels 448..511 at position
  *   pos[i] as csa2_kv_quant_write rotates an entry (interleaved pairs, the
- *   same frequencies; cos and sin to 2 ulp of fp32), or as given when pos is
- *   NULL; scale = fl32(max |x| / 448); codes = E4M3_rne_satfinite(x / scale),
- *   all zero when the scale is zero.  A row that holds a NaN or an infinity
- *   has NaN codes in their places, whatever its scale (NaNs do not count for
- *   the maximum).
+ *   same frequencies; cos and sin within 2 ulp of fp32 plus 2^-39), or as given
+ *   when pos is NULL; scale = fl32(max |x| / 448); codes =
+ *   E4M3_rne_satfinite(x / scale), all zero when the scale is zero.  A row that
+ *   holds a NaN or an infinity has NaN codes in their places, whatever its
+ *   scale (NaNs do not count for the maximum).
  *   latent    bf16 [n][512], 16-byte aligned
  *   pos       int64 [n], 0 <= pos < 2^22, or NULL (no RoPE)
  *   slot      int64 [n] destination rows, distinct, 0 <= slot < rows (a slot

@@ -5,34 +5,26 @@
 // bound by HBM for many rows and by launch latency for a decode step's few.
 // One warp handles a row (half a warp an indexer key) and every load and
 // store of a warp covers contiguous 16-, 8- or 4-byte pieces.
-#include <cmath>
-
 #include "kernels.cuh"
+#include "rope_turns.h"
 
 namespace csa2 {
 
-namespace {
+static_assert(kRopePairs == ROPE_DIM / 2, "one frequency per rotated pair");
 
-// RoPE frequencies as fractions of a turn per position, in units of 2^-64
-// turns: floor(2^64 * inv_j / (2 pi)), inv_j = fl32(theta^(-2j/64)).
-struct RopeTurns {
-  uint64_t step[ROPE_DIM / 2];
-};
+namespace {
 
 // Positions of kv_quant_write: [0, 2^22).
 constexpr int64_t kMaxRopePos = int64_t(1) << 22;
 
-// cos and sin of position p's rotation for one frequency.  p * step wraps
-// modulo whole turns by itself, and its error is below 2^22 * 2^-64 turns, so
-// no double-precision reduction is needed (GB300 has few FP64 units: 32,768
-// rows of double sincos alone would take over 100 us against 7.5 us of
-// memory traffic).  The nearest quarter turn is taken out exactly; what is
-// left, at most an eighth of a turn, is rounded once to fp32 and goes
-// through sincospif, within 2 ulp of fp32 in all.
+// cos and sin of position p's rotation for one frequency: the phase in fixed
+// point (rope_turns.h, so no double-precision reduction is needed: GB300 has
+// few FP64 units, and 32,768 rows of double sincos alone would take over 100 us
+// against 7.5 us of memory traffic), the quarter turns taken out exactly and
+// the rest through sincospif: within 2 ulp of fp32 plus 2^-39.
 __device__ __forceinline__ void rope_cos_sin(uint64_t step, int64_t p, float &c, float &s) {
-  const uint64_t phase = step * (uint64_t)p;
-  const uint64_t quarter = (phase + (1ull << 61)) >> 62;
-  const float half_turns = __ll2float_rn((int64_t)(phase - (quarter << 62))) * 0x1p-63f;
+  uint32_t quarter;
+  const float half_turns = rope_phase(step, p, quarter);
   float sr, cr;
   sincospif(half_turns, &sr, &cr);
   const bool odd = quarter & 1;
@@ -322,17 +314,7 @@ cudaError_t launch_swa_quant_write(const void *latent, int64_t n, const int64_t 
   thread_local RopeTurns turns = {};
   thread_local float theta = 0.0f;
   if (pos && theta != rope_theta) {
-    // 1 / (2 pi) = 0x0.28BE60DB9391054A7F09D5F47D4D3770... (binary expansion)
-    constexpr uint64_t kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;
-    for (int j = 0; j < ROPE_DIM / 2; ++j) {
-      const float inv = (float)std::pow((double)rope_theta, -(2.0 * j) / (double)ROPE_DIM);
-      int ex;
-      const uint64_t m = (uint64_t)std::ldexp(std::frexp(inv, &ex), 24);   // inv = m * 2^(ex - 24), ex <= 1
-      const unsigned __int128 lo = (unsigned __int128)m * kLo;
-      const unsigned __int128 prod = (unsigned __int128)m * kHi + (uint64_t)(lo >> 64);   // 2^64 m / (2 pi)
-      const int sh = 24 - ex;
-      turns.step[j] = sh >= 128 ? 0 : (uint64_t)(prod >> sh);
-    }
+    turns = rope_turns(rope_theta);
     theta = rope_theta;
   }
   const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(latent);
