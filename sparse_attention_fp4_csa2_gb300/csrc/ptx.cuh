@@ -149,17 +149,13 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
   return false;
 }
 
-// Arrive on a barrier of any CTA of the cluster (`addr` from dsmem_addr).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-
-// The same n times, for a barrier whose phase tells the even CTA of a pair
-// that shared memory of THIS CTA is full: what it guards is read by this
-// CTA's own tensor core (tcgen05.mma of the pair), and the writers' proxy
-// fence has made it visible there, so the release stays at CTA scope.  (At
-// cluster scope it waits for the loads that the SM has in flight: 5.2 ms
-// against 2.7 in the dense readout of 2 x 512 tokens over 16K entries.)
+// Arrive n times on a barrier of any CTA of the cluster (`addr` from
+// dsmem_addr) whose phase tells the even CTA of a pair that shared memory of
+// THIS CTA is full: what it guards is read by this CTA's own tensor core
+// (tcgen05.mma of the pair), and the writers' proxy fence has made it visible
+// there, so the release stays at CTA scope.  (At cluster scope it waits for the
+// loads that the SM has in flight: 5.2 ms against 2.7 in an early form of the
+// dense readout, 2 x 512 tokens over 16K entries.)
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t addr, uint32_t n) {
   asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0], %1;" ::"r"(addr), "r"(n) : "memory");
 }
