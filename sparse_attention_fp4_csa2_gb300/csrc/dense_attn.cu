@@ -879,9 +879,12 @@ cudaError_t launch_dense_attn(const void *q, const uint8_t *kv, const int32_t *n
   workers = workers < most ? workers : most;
   workers = workers < num_sms / 2 ? workers : num_sms / 2;
   // Beside the own part's kernel: the workers that fit next to its CTAs, if
-  // fewer of them end sooner than all of them after it (its few microseconds
-  // of latency are about kOwnUnits of theirs).
-  constexpr int64_t kOwnUnits = 5;
+  // fewer of them end sooner than all of them after it.  Its latency is between
+  // three and four units of theirs (in graphs, beside it against after it: no
+  // units more, 1 sequence over 65,536 entries, 32.7 us against 43.6; three more,
+  // 16 over 10,001 47.1 against 52.3, 8 over 20,000 46.9 against 50.1; four more, 4
+  // over 131,072 85.1 against 82.2; eight more, 7 over 65,536 100.0 against 83.3).
+  constexpr int64_t kOwnUnits = 3;
   const int64_t beside = (num_sms - own_ctas) / 2;
   if (own_ctas > 0 && beside >= 1 && beside < workers &&
       (most + beside - 1) / beside <= (most + workers - 1) / workers + kOwnUnits)
