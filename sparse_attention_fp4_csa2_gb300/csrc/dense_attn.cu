@@ -28,11 +28,11 @@
 //
 // What bounds it: the L1 / shared-memory data pipe of the SM, which is full.  A
 // step passes 2,816 wavefronts of tensor-core operands (P is read once for two
-// products), 2,750 of fp16 stores (K, V, P) and 2,330 of arriving entry sectors
-// (32 bytes each) in 8,030 clocks, against 4,096 of the products alone.
-// Measured: 2 x 512 tokens over 16,384 entries 1.66 ms (1,325 TFLOP/s, 0.69 of a
-// bf16 library product's burst rate); 32 tokens over 65,536 entries 226 us
-// (1,216); one token over 65,536 30 us, of which four steps take 16 and the
+// products), 2,730 of fp16 stores (K, V, P) and 2,220 of arriving entry sectors
+// (32 bytes each) in 7,950 clocks, against 4,096 of the products alone.
+// Measured: 2 x 512 tokens over 16,384 entries 1.66 ms (1,321 TFLOP/s, 0.69 of a
+// bf16 library product's burst rate); 32 tokens over 65,536 entries 225 us
+// (1,224); one token over 65,536 31 us, of which four steps take 16 and the
 // first entries' arrival, the last rows' way out and the combine the rest.
 // Between two pairs the products rest about 3 us: the accumulator has to be read
 // out before the next pair's first product into it.
