@@ -663,7 +663,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       wait_ft(S, &S.done, 0);
     }
    }
-    if (a.C > 1) {   // the two cluster barriers of the combine
+    if (a.C > 1) {   // the two cluster barriers of the combine, by whole warps
+      __syncwarp();
       cluster_arrive();
       cluster_wait();
       cluster_arrive();
