@@ -22,7 +22,9 @@
  * sliding-window rows), csa2_kv_read, csa2_swa_read and csa2_indexer_k_read
  * (cache rows read back), csa2_cross_attn (query tokens over every entry of
  * another sequence), csa2_prefix_attn (the readout of a batch that shares a
- * long prefix); helpers csa2_workspace_bytes,
+ * long prefix), csa2_slot_map (a step's positions and cache rows from its
+ * lengths), csa2_window_attn (window-only layers, with sinks), csa2_tree_attn
+ * (drafted tokens); helpers csa2_workspace_bytes,
  * csa2_get_device_status, csa2_status_string, csa2_default_params,
  * csa2_entry_bytes, csa2_indexer_entry_bytes, csa2_last_launch_count,
  * csa2_set_profile_events, csa2_set_topk_kernel.
@@ -423,6 +425,103 @@ csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch, const voi
                              int64_t n_prefix, const uint8_t *kv, int64_t cap, const int32_t *topk_idx,
                              const uint8_t *swa, const float *swa_scale, const int32_t *swa_len, void *out, float *lse,
                              void *ws, size_t ws_bytes, csa2_stream_t stream);
+
+/*
+ * csa2_slot_map -- from the lengths of a step's requests, the positions and
+ * cache rows that the writers take and the counts that the readouts take.
+ * Sequence b holds ctx_len[b] tokens and gets new_len[b] more in this step; the
+ * step's tokens are packed, sequence after sequence.
+ *   cu        int32 [batch + 1] (out): exclusive prefix sums of new_len; tokens
+ *             cu[b] .. cu[b + 1] - 1 are sequence b's
+ *   tok_seq   int32 [n_tokens] (out): the token's sequence
+ *   pos       int64 [n_tokens] (out): its position, ctx_len[b] + (i - cu[b])
+ *   swa_slot  int64 [n_tokens] (out): its row of the window rings, b * swa_rows +
+ *             pos mod swa_rows (for csa2_swa_quant_write); -1 when a later token
+ *             of the same step takes that row
+ *   entry_cu  int32 [batch + 1] (out): the same sums of the main-KV entries that
+ *             the step completes (at m = 2 one per odd position it reaches)
+ *   entry_pos int64 [n_entries] (out): the entry's position, m e + m - 1
+ *   slot      int64 [n_entries] (out): its row, b * cap + e (for
+ *             csa2_kv_quant_write, csa2_kv_quant_write_ik, csa2_indexer_k_quant);
+ *             -1 when e >= cap
+ *   n_vis     int32 [batch] (out): entries after the step, at most cap
+ *   swa_len   int32 [batch] (out): ring rows that hold a token, at most swa_rows
+ *   m         1 or 2; cap entries and swa_rows >= 1 ring rows per sequence
+ *   n_tokens, n_entries: lengths of the outputs.  Places past the last token or
+ *             entry get -1 (which the writers skip, and report); tokens and
+ *             entries past the outputs' lengths are dropped.
+ * A negative length (taken as 0), dropped tokens or entries, and a sequence past
+ * its cap set CSA2_DEV_ERR_NVIS.  batch above 8192 is CSA2_ERR_UNSUPPORTED.
+ * batch == 0 is a no-op.
+ */
+csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *new_len, int32_t m, int64_t cap,
+                          int64_t swa_rows, int64_t n_tokens, int64_t n_entries, int32_t *cu, int32_t *tok_seq,
+                          int64_t *pos, int64_t *swa_slot, int32_t *entry_cu, int64_t *entry_pos, int64_t *slot,
+                          int32_t *n_vis, int32_t *swa_len, csa2_stream_t stream);
+
+/*
+ * csa2_window_attn -- the attention of a window-only layer ([N] section 2: the
+ * encoder's first two layers), for decode steps and prefill chunks alike: packed
+ * query tokens over their causal sliding window and the first n_sink tokens of
+ * their sequence, which stay visible.  Token i of sequence b (cu[b] <= i <
+ * cu[b + 1]) sits at position p = ctx_len[b] + i - cu[b] and sees positions
+ * max(p - W + 1, 0) .. p (W = params.sliding_window) and the sinks s < n_sink
+ * with s < p - W + 1 (one still inside the window is read from the ring); one
+ * softmax over both, logits q . k / sqrt(512), key = value = the row's 512
+ * dequantised channels, as in csa2_sparse_attn.  The step's own rows must be in
+ * the ring already.
+ *   q         bf16 [n_tokens][64][512], 16-byte aligned; taken in fp16 (|q| below
+ *             65504, parts below 2^-25 are lost)
+ *   cu        int32 [batch + 1], ctx_len int32 [batch] as csa2_slot_map
+ *   swa       uint8 E4M3 [batch][swa_rows][512], 16-byte aligned; swa_scale fp32
+ *             [batch][swa_rows], not negative and at most 2^50 (a row whose
+ *             scale is below 2^-64 counts as zeros); position p has row p mod swa_rows.  Every row a
+ *             token of the step sees must still be there: min(ctx_len[b], W - 1)
+ *             + cu[b + 1] - cu[b] <= swa_rows (checked on device); swa_rows >= W
+ *   sink      uint8 E4M3 [batch][n_sink][512], 16-byte aligned; sink_scale fp32
+ *             [batch][n_sink]; row s holds position s; NULL when n_sink is 0
+ *   n_sink    0..64
+ *   out       bf16 [n_tokens][64][512] (out), 16-byte aligned; lse fp32
+ *             [n_tokens][64] or NULL (out).  A token that sees nothing gives out =
+ *             0 and lse = -inf; rows from cu[batch] on are left as they were.
+ * Rows no token sees are not read, whatever they hold.  A negative ctx_len (taken
+ * as 0) or a ring too short for the step sets CSA2_DEV_ERR_INDEX.  params.attn_kernel
+ * as csa2_params says.  batch == 0 or n_tokens == 0 is a no-op.
+ */
+csa2_status csa2_window_attn(const csa2_params *params, int32_t batch, int64_t n_tokens, const void *q,
+                             const int32_t *cu, const int32_t *ctx_len, const uint8_t *swa, const float *swa_scale,
+                             int64_t swa_rows, const uint8_t *sink, const float *sink_scale, int32_t n_sink, void *out,
+                             float *lse, csa2_stream_t stream);
+
+/*
+ * csa2_tree_attn -- csa2_sparse_attn for drafted tokens: n_tree query tokens per
+ * sequence, each over its own selected entries, the drafted tokens that its mask
+ * names (itself and those it descends from) and the committed part of its
+ * window, in one softmax.  A token whose mask names c drafted tokens sees of the
+ * committed positions the last max(W - c, 0) before ctx_len[b] (the window of W
+ * ends with the token itself).
+ *   q         bf16 [batch][n_tree][64][512], as csa2_window_attn
+ *   kv        uint8 [batch][cap][288], 16-byte aligned; topk_idx int32
+ *             [batch][n_tree][index_topk], entries in [-1, cap); topk_idx NULL: no
+ *             entries (a window-only layer; kv may be NULL)
+ *   swa       the sequences' rings, as csa2_window_attn, rows of the committed
+ *             positions; swa_rows >= W
+ *   ctx_len   int32 [batch]: committed tokens
+ *   tree      uint8 E4M3 [batch][n_tree][512], 16-byte aligned; tree_scale fp32
+ *             [batch][n_tree]: the drafted tokens' rows (csa2_swa_quant_write)
+ *   tree_mask int64 [batch][n_tree]: bit u of a token's mask names drafted token
+ *             u; bits from n_tree on are ignored
+ *   n_tree    up to 64 (above that CSA2_ERR_UNSUPPORTED)
+ *   out       bf16 [batch][n_tree][64][512] (out), 16-byte aligned; lse fp32
+ *             [batch][n_tree][64] or NULL (out).  A token that sees nothing gives
+ *             out = 0 and lse = -inf.
+ * A negative ctx_len (taken as 0) or an index outside the cache sets
+ * CSA2_DEV_ERR_INDEX.  batch == 0 or n_tree == 0 is a no-op.
+ */
+csa2_status csa2_tree_attn(const csa2_params *params, int32_t batch, int32_t n_tree, const void *q, const uint8_t *kv,
+                           int64_t cap, const int32_t *topk_idx, const uint8_t *swa, const float *swa_scale,
+                           int64_t swa_rows, const int32_t *ctx_len, const uint8_t *tree, const float *tree_scale,
+                           const int64_t *tree_mask, void *out, float *lse, csa2_stream_t stream);
 
 /* Operation selector for csa2_workspace_bytes. */
 typedef enum {

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -88,9 +89,13 @@ def lib():
         L.csa2_indexer_k_read.argtypes = [P, i32, i64, P, i64, P, P]
         L.csa2_cross_attn.argtypes = [i32, i32, P, P, i64, P, i64, P, P, P, sz, P]
         L.csa2_prefix_attn.argtypes = [PP, i32, P, P, i64, P, i64, P, P, P, P, P, P, P, sz, P]
+        L.csa2_slot_map.argtypes = [i32, P, P, i32, i64, i64, i64, i64, P, P, P, P, P, P, P, P, P, P]
+        L.csa2_window_attn.argtypes = [PP, i32, i64, P, P, P, P, P, i64, P, P, i32, P, P, P]
+        L.csa2_tree_attn.argtypes = [PP, i32, i32, P, P, i64, P, P, P, i64, P, P, P, P, P, P, P]
         for f in ("csa2_kv_quant_write", "csa2_kv_quant_write_ik", "csa2_indexer_k_quant", "csa2_indexer_score_topk", "csa2_hier_pool_select",
                   "csa2_sparse_attn", "csa2_sparse_decode", "csa2_swa_quant_write", "csa2_kv_read", "csa2_swa_read",
-                  "csa2_indexer_k_read", "csa2_cross_attn", "csa2_prefix_attn"):
+                  "csa2_indexer_k_read", "csa2_cross_attn", "csa2_prefix_attn", "csa2_slot_map", "csa2_window_attn",
+                  "csa2_tree_attn"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -429,3 +434,87 @@ def prefix_attn(params, q, prefix_kv, kv, topk_idx, swa, swa_scale, swa_len, out
         win(swa_scale, torch.float32, (B, W), "swa_scale", dev), win(swa_len, torch.int32, (B,), "swa_len", dev),
         _dev(out, torch.bfloat16, (B, H, D), "out", dev), _opt(lse, torch.float32, (B, H), "lse", dev),
         _dev(ws, torch.uint8, None, "ws", dev), ws.numel(), _stream(stream)), "csa2_prefix_attn")
+
+
+class SlotMaps(NamedTuple):
+    """Outputs of ``slot_map``: cu int32 [B + 1], tok_seq int32 [n], pos and
+    swa_slot int64 [n], entry_cu int32 [B + 1], entry_pos and slot int64
+    [entries], n_vis and swa_len int32 [B]."""
+    cu: torch.Tensor
+    tok_seq: torch.Tensor
+    pos: torch.Tensor
+    swa_slot: torch.Tensor
+    entry_cu: torch.Tensor
+    entry_pos: torch.Tensor
+    slot: torch.Tensor
+    n_vis: torch.Tensor
+    swa_len: torch.Tensor
+
+
+def slot_maps(batch: int, n_tokens: int, m: int = 1, device=None) -> SlotMaps:
+    """Caller-owned outputs of ``slot_map`` for up to n_tokens packed tokens (and
+    the entries that so many can complete at m = 1 or 2)."""
+    if m not in (1, 2) or batch < 0 or n_tokens < 0:
+        raise Csa2Error("slot_maps: m must be 1 or 2, sizes not negative")
+    entries = n_tokens if m == 1 else (n_tokens + batch) // 2
+
+    def new(n, dtype):
+        return torch.full((n,), -1, dtype=dtype, device=device or "cuda")
+
+    i32, i64 = torch.int32, torch.int64
+    return SlotMaps(new(batch + 1, i32), new(n_tokens, i32), new(n_tokens, i64), new(n_tokens, i64),
+                    new(batch + 1, i32), new(entries, i64), new(entries, i64), new(batch, i32), new(batch, i32))
+
+
+def slot_map(ctx_len, new_len, cap, swa_rows, maps, m=1, stream=None):
+    """A step's positions and cache rows from its lengths: ctx_len, new_len int32
+    [B]; cap entries and swa_rows ring rows per sequence; maps of ``slot_maps``."""
+    B, n, e, dev = ctx_len.numel(), maps.pos.numel(), maps.slot.numel(), _cur(ctx_len)
+    i32, i64 = torch.int32, torch.int64
+    _check(lib().csa2_slot_map(
+        B, _dev(ctx_len, i32, (B,), "ctx_len", dev), _dev(new_len, i32, (B,), "new_len", dev), m, cap, swa_rows, n, e,
+        _dev(maps.cu, i32, (B + 1,), "cu", dev), _dev(maps.tok_seq, i32, (n,), "tok_seq", dev),
+        _dev(maps.pos, i64, (n,), "pos", dev), _dev(maps.swa_slot, i64, (n,), "swa_slot", dev),
+        _dev(maps.entry_cu, i32, (B + 1,), "entry_cu", dev), _dev(maps.entry_pos, i64, (e,), "entry_pos", dev),
+        _dev(maps.slot, i64, (e,), "slot", dev), _dev(maps.n_vis, i32, (B,), "n_vis", dev),
+        _dev(maps.swa_len, i32, (B,), "swa_len", dev), _stream(stream)), "csa2_slot_map")
+
+
+def window_attn(params, q, cu, ctx_len, swa, swa_scale, out, sink=None, sink_scale=None, lse=None, stream=None):
+    """Packed tokens of a window-only layer over their causal window and sinks: q
+    bf16 [n, 64, 512]; cu int32 [B + 1] and ctx_len int32 [B] as ``slot_map``; swa
+    uint8 [B, rows, 512] and swa_scale fp32 [B, rows], rings of position mod rows
+    (None with sliding_window 0); sink uint8 [B, S, 512] and sink_scale fp32 [B, S]
+    (position s in row s) or None; out bf16 [n, 64, 512]; lse fp32 [n, 64] or None."""
+    n, B, dev = q.shape[0], ctx_len.numel(), _cur(out)
+    rows = 0 if swa is None else swa.shape[1]
+    S = 0 if sink is None else sink.shape[1]
+    _check(lib().csa2_window_attn(
+        ctypes.byref(params), B, n, _dev(q, torch.bfloat16, (n, H, D), "q", dev),
+        _dev(cu, torch.int32, (B + 1,), "cu", dev), _dev(ctx_len, torch.int32, (B,), "ctx_len", dev),
+        _opt(swa, torch.uint8, (B, rows, D), "swa", dev), _opt(swa_scale, torch.float32, (B, rows), "swa_scale", dev), rows,
+        _opt(sink, torch.uint8, (B, S, D), "sink", dev), _opt(sink_scale, torch.float32, (B, S), "sink_scale", dev), S,
+        _dev(out, torch.bfloat16, (n, H, D), "out", dev), _opt(lse, torch.float32, (n, H), "lse", dev),
+        _stream(stream)), "csa2_window_attn")
+
+
+def tree_attn(params, q, kv, topk_idx, swa, swa_scale, ctx_len, tree, tree_scale, tree_mask, out, lse=None,
+              stream=None):
+    """Drafted tokens over their entries, the committed window and the drafted
+    tokens their masks name: q bf16 [B, T, 64, 512] (T <= 64); kv uint8 [B, cap, 288]
+    and topk_idx int32 [B, T, K], or None, None (no entries); swa, swa_scale rings as
+    ``window_attn``; ctx_len int32 [B]; tree uint8 [B, T, 512], tree_scale fp32
+    [B, T]; tree_mask int64 [B, T]; out bf16 [B, T, 64, 512]; lse fp32 [B, T, 64] or
+    None."""
+    B, T, dev = q.shape[0], q.shape[1], _cur(out)
+    rows = 0 if swa is None else swa.shape[1]
+    cap = 0 if kv is None else kv.shape[1]
+    _check(lib().csa2_tree_attn(
+        ctypes.byref(params), B, T, _dev(q, torch.bfloat16, (B, T, H, D), "q", dev),
+        _opt(kv, torch.uint8, (B, cap, ENTRY_BYTES), "kv", dev), cap,
+        _opt(topk_idx, torch.int32, (B, T, params.index_topk), "topk_idx", dev),
+        _opt(swa, torch.uint8, (B, rows, D), "swa", dev), _opt(swa_scale, torch.float32, (B, rows), "swa_scale", dev), rows,
+        _dev(ctx_len, torch.int32, (B,), "ctx_len", dev), _dev(tree, torch.uint8, (B, T, D), "tree", dev),
+        _dev(tree_scale, torch.float32, (B, T), "tree_scale", dev), _dev(tree_mask, torch.int64, (B, T), "tree_mask", dev),
+        _dev(out, torch.bfloat16, (B, T, H, D), "out", dev), _opt(lse, torch.float32, (B, T, H), "lse", dev),
+        _stream(stream)), "csa2_tree_attn")

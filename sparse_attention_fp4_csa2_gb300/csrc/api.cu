@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "kernels.cuh"
@@ -35,6 +36,7 @@ cudaError_t record_profile_event(cudaEvent_t ev, cudaStream_t stream) {
 namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -765,4 +767,129 @@ extern "C" csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch
     return CSA2_ERR_CUDA;
   g_last_launches = launches;
   return CSA2_OK;
+}
+
+extern "C" csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *new_len, int32_t m,
+                                     int64_t cap, int64_t swa_rows, int64_t n_tokens, int64_t n_entries, int32_t *cu,
+                                     int32_t *tok_seq, int64_t *pos, int64_t *swa_slot, int32_t *entry_cu,
+                                     int64_t *entry_pos, int64_t *slot, int32_t *n_vis, int32_t *swa_len,
+                                     csa2_stream_t stream) {
+  g_last_launches = 0;
+  if (batch < 0 || (m != 1 && m != 2) || cap < 0 || swa_rows < 1 || n_tokens < 0 || n_entries < 0)
+    return CSA2_ERR_INVALID_ARG;
+  if (batch == 0) return CSA2_OK;
+  if (!ctx_len || !new_len || !cu || !entry_cu || !n_vis || !swa_len || (n_tokens > 0 && (!tok_seq || !pos || !swa_slot)) ||
+      (n_entries > 0 && (!entry_pos || !slot)))
+    return CSA2_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)ctx_len, (const void *)new_len, (const void *)cu, (const void *)tok_seq,
+                        (const void *)entry_cu, (const void *)n_vis, (const void *)swa_len})
+    if (!aligned4(p)) return CSA2_ERR_INVALID_ARG;
+  for (const void *p : {(const void *)pos, (const void *)swa_slot, (const void *)entry_pos, (const void *)slot})
+    if (reinterpret_cast<uintptr_t>(p) & 7u) return CSA2_ERR_INVALID_ARG;
+  if (batch > kMaxMapBatch || n_tokens > INT32_MAX || n_entries > INT32_MAX || cap > kMaxCacheRows / batch ||
+      swa_rows > kMaxCacheRows / batch)
+    return CSA2_ERR_UNSUPPORTED;
+  if (launch_slot_map(ctx_len, new_len, batch, m, cap, swa_rows, n_tokens, n_entries, cu, tok_seq, pos, swa_slot,
+                      entry_cu, entry_pos, slot, n_vis, swa_len, num_sms(),
+                      reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return CSA2_ERR_CUDA;
+  g_last_launches = 1;
+  return CSA2_OK;
+}
+
+namespace {
+
+// The step form of the sparse readout: `tokens` queries over K listed entries
+// each and the 8-bit rows of `s`.
+csa2_status run_step(const csa2_params *p, int64_t tokens, const void *q, const uint8_t *kv, int64_t cap,
+                     const int32_t *topk_idx, const uint8_t *swa, const float *swa_scale, const StepRows &s, float *lse,
+                     cudaStream_t stream) {
+  AttnArgs a;
+  std::memset(&a, 0, sizeof(a));
+  a.q = static_cast<const __nv_bfloat16 *>(q);
+  a.kv = kv;
+  a.idx = topk_idx;
+  a.swa = swa;
+  a.swa_scale = swa_scale;
+  a.lse = lse;
+  a.cap = cap;
+  a.problems = (int32_t)tokens;
+  a.K = topk_idx ? p->index_topk : 0;
+  a.W = s.win + s.extras;
+  a.tokens = 1;
+  a.kernel = p->attn_kernel;
+  a.step = s;
+  int launches = 0;
+  if (launch_sparse_attn(a, nullptr, stream, &launches) != cudaSuccess) return CSA2_ERR_CUDA;
+  g_last_launches = launches;
+  return CSA2_OK;
+}
+
+constexpr int64_t kMaxStepTokens = (int64_t)1 << 24;   // query tokens of a step
+constexpr int32_t kMaxExtraRows = 64;                  // sinks of a sequence, drafted tokens of a tree
+
+}  // namespace
+
+extern "C" csa2_status csa2_window_attn(const csa2_params *params, int32_t batch, int64_t n_tokens, const void *q,
+                                        const int32_t *cu, const int32_t *ctx_len, const uint8_t *swa,
+                                        const float *swa_scale, int64_t swa_rows, const uint8_t *sink,
+                                        const float *sink_scale, int32_t n_sink, void *out, float *lse,
+                                        csa2_stream_t stream) {
+  g_last_launches = 0;
+  if (!params_ok(params)) return CSA2_ERR_UNSUPPORTED;
+  const int32_t W = params->sliding_window;
+  if (batch < 0 || n_tokens < 0 || swa_rows < 0 || n_sink < 0) return CSA2_ERR_INVALID_ARG;
+  if (batch == 0 || n_tokens == 0) return CSA2_OK;
+  if (!q || !cu || !ctx_len || !out || (W > 0 && (!swa || !swa_scale || swa_rows < W)) ||
+      (n_sink > 0 && (!sink || !sink_scale)))
+    return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(swa) || !aligned16(sink) || !aligned4(cu) || !aligned4(ctx_len) ||
+      !aligned4(swa_scale) || !aligned4(sink_scale) || !aligned4(lse))
+    return CSA2_ERR_INVALID_ARG;
+  if (n_tokens > kMaxStepTokens || n_sink > kMaxExtraRows || swa_rows > kMaxCacheRows / batch) return CSA2_ERR_UNSUPPORTED;
+  StepRows s = {};
+  s.cu = cu;
+  s.ctx_len = ctx_len;
+  s.extra = sink;
+  s.extra_scale = sink_scale;
+  s.out = static_cast<__nv_bfloat16 *>(out);
+  s.ring = swa_rows > 0 ? swa_rows : 1;
+  s.batch = batch;
+  s.win = W;
+  s.extras = n_sink;
+  return run_step(params, n_tokens, q, nullptr, 0, nullptr, swa, swa_scale, s, lse, reinterpret_cast<cudaStream_t>(stream));
+}
+
+extern "C" csa2_status csa2_tree_attn(const csa2_params *params, int32_t batch, int32_t n_tree, const void *q,
+                                      const uint8_t *kv, int64_t cap, const int32_t *topk_idx, const uint8_t *swa,
+                                      const float *swa_scale, int64_t swa_rows, const int32_t *ctx_len,
+                                      const uint8_t *tree, const float *tree_scale, const int64_t *tree_mask, void *out,
+                                      float *lse, csa2_stream_t stream) {
+  g_last_launches = 0;
+  if (!params_ok(params)) return CSA2_ERR_UNSUPPORTED;
+  const int32_t W = params->sliding_window;
+  if (batch < 0 || n_tree < 0 || swa_rows < 0 || cap < 0) return CSA2_ERR_INVALID_ARG;
+  if (batch == 0 || n_tree == 0) return CSA2_OK;
+  if (!q || !ctx_len || !tree || !tree_scale || !tree_mask || !out || (topk_idx && (!kv || cap < 1)) ||
+      (W > 0 && (!swa || !swa_scale || swa_rows < W)))
+    return CSA2_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(kv) || !aligned16(swa) || !aligned16(tree) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u) || !aligned4(topk_idx) || !aligned4(swa_scale) ||
+      !aligned4(ctx_len) || !aligned4(tree_scale) || !aligned4(lse))
+    return CSA2_ERR_INVALID_ARG;
+  if (n_tree > kMaxExtraRows || (int64_t)batch * n_tree > kMaxStepTokens || swa_rows > kMaxCacheRows / batch ||
+      cap > kMaxCacheRows / batch)
+    return CSA2_ERR_UNSUPPORTED;
+  StepRows s = {};
+  s.ctx_len = ctx_len;
+  s.mask = reinterpret_cast<const uint64_t *>(tree_mask);
+  s.extra = tree;
+  s.extra_scale = tree_scale;
+  s.out = static_cast<__nv_bfloat16 *>(out);
+  s.ring = swa_rows > 0 ? swa_rows : 1;
+  s.batch = batch;
+  s.win = W;
+  s.extras = n_tree;
+  return run_step(params, (int64_t)batch * n_tree, q, kv, cap, topk_idx, swa, swa_scale, s, lse,
+                  reinterpret_cast<cudaStream_t>(stream));
 }

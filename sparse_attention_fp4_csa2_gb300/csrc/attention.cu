@@ -73,9 +73,10 @@ constexpr int kRedOffMulti = kPOffMulti + 3 * kAtom;
 constexpr int kRedOffSingle = 3 * kAtom;         // single-block items: P^T and reductions in the Q region
 // cluster combine, in the tile region: received [8][2][64] max / sum and
 // [C][D / C rows][128 B] partials, [8][64] weights, staged rows to send
-constexpr uint32_t kCombineParts = 8 * 2 * H * 4;
-constexpr uint32_t kCombineWgt = kCombineParts + D * 128;
-constexpr uint32_t kCombineStage = kCombineWgt + 8 * H * 4;
+// (step form: [8][3][64] max, sum and sum of the scaled weights)
+constexpr uint32_t combine_parts(bool step) { return 8 * (step ? 3 : 2) * H * 4; }
+constexpr uint32_t combine_wgt(bool step) { return combine_parts(step) + D * 128; }
+constexpr uint32_t combine_stage(bool step) { return combine_wgt(step) + 8 * H * 4; }
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;                  // O^T: columns 256 + 64 mt + head, lanes = dims
 constexpr float kLazy = 8.0f;                    // log2 margin before the reference max is raised
@@ -96,10 +97,32 @@ struct __align__(16) Ctl {
   float lfin[H];           // per head at an item's end: row sum
 };
 
+// Step form: per row log2 of its scale (-inf: no key) and 1 / scale, behind
+// what both block forms keep in the tile region (its single blocks are of up to
+// 144 rows).  The reference max is taken over logit + log2(scale), so that what
+// goes to the tensor core, 2^(logit - m) x scale, is at most 1 (2^kLazy) whatever
+// the rows' scales are; the row sum takes it times 1 / scale.  A row whose scale
+// is below 2^-64 counts as zeros (NaN codes stay NaN): codes x 0, with a scale of
+// 2^-64, so that it never sets the reference and, up to scales of 2^50 beside it,
+// 2^(logit - m) x 2^-64 is still an fp32 number that gives back its weight.
+// A chunk's partial is O over the sum of its scaled weights, a convex combination
+// of what the tile holds (at most 2688 and, of 8-bit rows, codes): within fp16
+// whatever the scales; that sum goes along with the row sum.
+struct StepScale {
+  float lg[kMaxBk], inv[kMaxBk];
+  float red2[2][H];
+  float l2fin[H];          // per head at an item's end: sum of the scaled weights
+};
+constexpr int kMaxBkStep = 144;
+constexpr uint32_t kStepScaleOff = kRedOffMulti + 2 * H * 4;
+constexpr float kTinyScale = 5.421010862427522e-20f;   // 2^-64
+static_assert(kStepScaleOff >= kMaxBkStep * D * 2 && kStepScaleOff + sizeof(StepScale) <= kTileRegion &&
+              kStepScaleOff % 16 == 0, "the step form's scales overlap the tile");
+
 constexpr size_t kSmemBytes = 1024 + (size_t)kTileRegion + kQBytes + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "attention exceeds the shared-memory limit");
 static_assert(kRedOffMulti + 2 * H * 4 <= kTileRegion, "multi-block reductions overflow the tile region");
-static_assert(kCombineStage + D * 128 <= kTileRegion, "cluster combine overflows the tile region");
+static_assert(combine_stage(false) + D * 128 <= kTileRegion && combine_stage(true) + D * 128 <= kStepScaleOff, "cluster combine overflows the tile region");
 static_assert(kRedOffSingle >= (kMaxBk / 64 + 1) * kAtom && kRedOffSingle + 4 * H * 4 <= kQBytes,
               "single-block P^T overlaps the reductions");
 
@@ -109,22 +132,71 @@ static_assert(kRedOffSingle >= (kMaxBk / 64 + 1) * kAtom && kRedOffSingle + 4 * 
 struct Item {
   int64_t gp;          // token (global problem index)
   int64_t seq_row0;    // first main-KV row of the token's sequence
-  int64_t swa_row0;    // first SWA row of the token's window
+  int64_t swa_row0;    // first SWA row of the token's window (step form: of its sequence's ring)
   int swa_len;         // valid rows of the window
   int k0, nW, w0, R, nb;
+  // step form (StepRows): row t of the a.W 8-bit rows is window row t, at ring
+  // place ring0 + t (once around), for first <= t < win, and extra row t - win,
+  // a key if its bit of `extra` is set, past that
+  int64_t extra0;      // first extra row of the token's sequence
+  uint64_t extra;
+  int64_t ring0;
+  int first;
 };
 
+// The token's keys in the step form: its sequence, the ring place and the first
+// visible one of its window rows, and its extra rows.  Called by whole warps.
+// Nothing read from the device makes an address: whatever ctx_len, cu and the
+// masks hold, ring0 < ring and seq < batch.
+__device__ __forceinline__ bool step_rows(const AttnArgs &a, int64_t gp, Item &it) {
+  const StepRows &s = a.step;
+  int64_t seq, end;   // the last committed position the window may hold, plus one
+  int left;           // window rows up to there
+  if (s.cu) {         // packed tokens: a causal window and the first tokens as sinks
+    int b;
+    if (!find_sequence(s.cu, s.batch, gp, b)) return false;
+    seq = b;
+    const int64_t r = gp - s.cu[b], ctx = max(s.ctx_len[b], 0);
+    end = ctx + r + 1;
+    left = s.win;
+    const int64_t before = end - s.win;   // positions that the window has left behind
+    const int sinks = (int)(before < s.extras ? (before > 0 ? before : 0) : s.extras);
+    it.extra = sinks >= 64 ? ~0ull : (1ull << sinks) - 1;
+    if (s.ctx_len[b] < 0 || s.win > 0 && min(ctx, (int64_t)s.win - 1) + (s.cu[b + 1] - s.cu[b]) > s.ring) set_error(CSA2_DEV_ERR_INDEX);
+  } else {            // a tree's tokens: the rows their mask names, and the window's rest
+    seq = (int64_t)((uint32_t)gp / (uint32_t)s.extras);
+    const int32_t c = s.ctx_len[seq];
+    if (c < 0) set_error(CSA2_DEV_ERR_INDEX);
+    it.extra = s.mask[gp] & (s.extras >= 64 ? ~0ull : (1ull << s.extras) - 1);
+    end = max(c, 0);
+    left = max(s.win - __popcll(it.extra), 0);
+  }
+  const int64_t start = end - s.win;   // window row 0's position; rows below position 0 hold no key
+  it.first = (int)max((int64_t)(s.win - left), -start);
+  const int64_t m = start % s.ring;
+  it.ring0 = m < 0 ? m + s.ring : m;
+  it.swa_row0 = seq * s.ring;
+  it.extra0 = seq * s.extras;
+  it.seq_row0 = seq * a.cap;
+  return true;
+}
+
+template <bool kStep>
 __device__ __forceinline__ Item item_info(const AttnArgs &a, int item) {
   Item it;
   const int C = a.C;
   const int tok = item / C, c = item - tok * C;
   it.gp = a.p0 + tok;
-  it.seq_row0 = (it.gp / a.tokens) * a.cap;
+  if constexpr (!kStep) it.seq_row0 = (it.gp / a.tokens) * a.cap;
   it.k0 = (c * a.K) / C;
   it.w0 = (c * a.W) / C;
   it.nW = ((c + 1) * a.W) / C - it.w0;
   it.R = it.nW + ((c + 1) * a.K) / C - it.k0;
   it.nb = it.R > a.Bk ? (it.R + a.Bk - 1) / a.Bk : 1;
+  if constexpr (kStep) {
+    if (!step_rows(a, it.gp, it)) it.nW = it.R = 0;   // no sequence's token: no keys, and its rows are not written
+    return it;
+  }
   if (a.causal_swa) {
     const int64_t seq = it.gp / a.tokens;
     const int64_t pos = a.first_pos + it.gp % a.tokens;
@@ -163,7 +235,7 @@ __device__ __forceinline__ int32_t row_slot(const AttnArgs &a, const Item &it, i
   return __ldg(a.idx + it.gp * a.K + it.k0 + (e - it.nW));
 }
 
-template <int N>
+template <bool kStep, int N>
 __device__ __forceinline__ void load_row(const AttnArgs &a, const Item &it, int e, int32_t id, int cp,
                                          RowBufN<N> &b) {
   b.kind = 0;
@@ -188,13 +260,31 @@ __device__ __forceinline__ void load_row(const AttnArgs &a, const Item &it, int 
     b.kind = 1;
   } else if constexpr (N == 16) {
     const int t = it.w0 + e;
-    if (t >= it.swa_len) return;
-    const uint8_t *src = a.swa + (it.swa_row0 + t) * D;
+    const uint8_t *src;
+    if constexpr (kStep) {
+      const float *scale;
+      const int u = t - a.step.win;
+      if (u < 0) {
+        if (t < it.first) return;
+        int64_t row = it.ring0 + t;
+        row = it.swa_row0 + (row >= a.step.ring ? row - a.step.ring : row);
+        src = a.swa + row * D;
+        scale = a.swa_scale + row;
+      } else {
+        if (!((it.extra >> u) & 1)) return;
+        src = a.step.extra + (it.extra0 + u) * D;
+        scale = a.step.extra_scale + it.extra0 + u;
+      }
+      b.scale = __uint_as_float(ld_nc_u32(scale));
+    } else {
+      if (t >= it.swa_len) return;
+      src = a.swa + (it.swa_row0 + t) * D;
+    }
 #pragma unroll
     for (int p = 0; p < 4; ++p)
 #pragma unroll
       for (int u = 0; u < 4; ++u) b.v[4 * p + u] = ld_nc_v4(src + 64 * (cp + 2 * p) + 16 * u);
-    b.scale = __uint_as_float(ld_nc_u32(a.swa_scale + it.swa_row0 + t));
+    if constexpr (!kStep) b.scale = __uint_as_float(ld_nc_u32(a.swa_scale + it.swa_row0 + t));
     b.kind = 2;
   }
 }
@@ -204,7 +294,7 @@ __device__ __forceinline__ void load_row(const AttnArgs &a, const Item &it, int 
 // the buffer's next column then moves to the front.  (One instantiation
 // walked four times: the kernel's code stays small enough for the
 // instruction cache.)
-template <int N>
+template <bool kStep, int N>
 __device__ __forceinline__ void dequant_front(uint8_t *tile, uint32_t col_stride, int r, int c, RowBufN<N> &b) {
   uint8_t *rowp = tile + (uint32_t)c * col_stride + (uint32_t)r * 128;
   const int sw = r & 7;
@@ -228,16 +318,21 @@ __device__ __forceinline__ void dequant_front(uint8_t *tile, uint32_t col_stride
   }
   if constexpr (N == 16) {
     if (b.kind == 2) {
+      const uint32_t keep2 = kStep && b.scale < kTinyScale ? 0u : 0x3C003C00u;   // fp16 1, 1
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint4 raw = b.v[u];
         const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-        const uint4 o0 =
+        uint4 o0 =
             make_uint4(e4m3x2_to_half2((uint16_t)(w[0] & 0xFFFF)), e4m3x2_to_half2((uint16_t)(w[0] >> 16)),
                        e4m3x2_to_half2((uint16_t)(w[1] & 0xFFFF)), e4m3x2_to_half2((uint16_t)(w[1] >> 16)));
-        const uint4 o1 =
+        uint4 o1 =
             make_uint4(e4m3x2_to_half2((uint16_t)(w[2] & 0xFFFF)), e4m3x2_to_half2((uint16_t)(w[2] >> 16)),
                        e4m3x2_to_half2((uint16_t)(w[3] & 0xFFFF)), e4m3x2_to_half2((uint16_t)(w[3] >> 16)));
+        if constexpr (kStep) {
+          o0 = make_uint4(hmul2_u32(o0.x, keep2), hmul2_u32(o0.y, keep2), hmul2_u32(o0.z, keep2), hmul2_u32(o0.w, keep2));
+          o1 = make_uint4(hmul2_u32(o1.x, keep2), hmul2_u32(o1.y, keep2), hmul2_u32(o1.z, keep2), hmul2_u32(o1.w, keep2));
+        }
         *reinterpret_cast<uint4 *>(rowp + (((2 * u) ^ sw) << 4)) = o0;
         *reinterpret_cast<uint4 *>(rowp + (((2 * u + 1) ^ sw) << 4)) = o1;
       }
@@ -248,6 +343,21 @@ __device__ __forceinline__ void dequant_front(uint8_t *tile, uint32_t col_stride
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(rowp + ((i ^ sw) << 4)) = make_uint4(0, 0, 0, 0);
+}
+
+// What the softmax has to know of row r: its scale and whether it holds a key.
+template <bool kStep>
+__device__ __forceinline__ void put_row_info(Ctl &S, uint8_t *tile, int r, const RowBuf &b) {
+  if constexpr (kStep) {
+    StepScale &sc = *reinterpret_cast<StepScale *>(tile + kStepScaleOff);
+    const float f = b.scale < kTinyScale ? kTinyScale : b.scale;
+    S.rs[r] = kLogit * f;   // (of a row of zeros the products are 0, or NaN)
+    sc.lg[r] = b.kind != 0 ? log2f(f) : -INFINITY;
+    sc.inv[r] = 1.0f / f;
+  } else {
+    S.rs[r] = b.scale;
+    S.vld[r] = b.kind != 0 ? 1 : 0;
+  }
 }
 
 __device__ __forceinline__ uint32_t pack_half2(float a, float b) {
@@ -263,6 +373,7 @@ __device__ __forceinline__ void wait_ft(Ctl &S, uint64_t *bar, uint32_t parity) 
 
 // The next block a worker loads: with C = 1 the CTA strides through the
 // items; with C > 1 it holds exactly one.
+template <bool kStep>
 struct Cursor {
   int item, j;
   Item it;
@@ -270,19 +381,32 @@ struct Cursor {
     if (++j >= it.nb) {
       j = 0;
       item += stride;
-      if (item < items) it = item_info(a, item);
+      if (item < items) it = item_info<kStep>(a, item);
     }
   }
 };
 
+// Channel d (a lane's; a warp's 32 are consecutive) of rows `row` and row + 1
+// as bf16: neighbouring lanes exchange, so that the even one stores two channels
+// of the first row and the odd one two of the second.
+__device__ __forceinline__ void put_pair(__nv_bfloat16 *out, int64_t row, int d, float x, float y) {
+  const bool odd = d & 1;
+  const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
+  const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(other, y) : __floats2bfloat162_rn(x, other);
+  *reinterpret_cast<__nv_bfloat162 *>(out + (row + odd) * D + (d & ~1)) = v;
+}
+
 // The finished item's output: out = O^T / l (C = 1), or (C > 1) this chunk's
 // (m, l) and its normalised partial (fp16, [dim][head]) for the dims the other
 // chunks own; the merge follows a cluster barrier.
+template <bool kStep>
 __device__ __forceinline__ void item_epilogue(const AttnArgs &a, Ctl &S, int item, uint32_t s_row, int tid, int q4,
                                               int wh, int lane) {
   const int64_t gp = a.p0 + item;   // C = 1: an item is a token
   bar_named(1, kWorkers);   // inv_l / mfin / lfin of the item are visible
   tc_fence_after();
+  if constexpr (kStep)
+    if (a.step.cu && gp >= a.step.cu[a.step.batch]) return;   // behind the last sequence
   float *outp = a.out + gp * H * D;
 #pragma unroll 1
   for (int mm = 0; mm < 2; ++mm) {
@@ -293,11 +417,19 @@ __device__ __forceinline__ void item_epilogue(const AttnArgs &a, Ctl &S, int ite
     tmem_ld32(s_row + kColO + (uint32_t)(mt * H + 32), v[1]);
     tmem_ld_wait();
     const float keep = S.abort ? 0.0f : 1.0f;
+    if constexpr (kStep) {
 #pragma unroll
-    for (int hh = 0; hh < H; ++hh) outp[hh * D + d] = __uint_as_float(v[hh >> 5][hh & 31]) * (S.inv_l[hh] * keep);
+      for (int hh = 0; hh < H; hh += 2)
+        put_pair(a.step.out, gp * H + hh, d, __uint_as_float(v[hh >> 5][hh & 31]) * (S.inv_l[hh] * keep),
+                 __uint_as_float(v[hh >> 5][(hh & 31) + 1]) * (S.inv_l[hh + 1] * keep));
+    } else {
+#pragma unroll
+      for (int hh = 0; hh < H; ++hh) outp[hh * D + d] = __uint_as_float(v[hh >> 5][hh & 31]) * (S.inv_l[hh] * keep);
+    }
   }
   if (tid < H && a.lse)
-    a.lse[gp * H + tid] = S.lfin[tid] > 0.0f ? (S.mfin[tid] + log2f(S.lfin[tid])) * kLn2 : -INFINITY;
+    a.lse[gp * H + tid] = S.lfin[tid] > 0.0f || (kStep && S.lfin[tid] != 0.0f) ? (S.mfin[tid] + log2f(S.lfin[tid])) * kLn2
+                                                                               : -INFINITY;
 }
 
 // C > 1: the C chunks of a token are the CTAs of one cluster (rank = chunk),
@@ -314,6 +446,7 @@ __device__ __forceinline__ void item_epilogue(const AttnArgs &a, Ctl &S, int ite
 // barrier, arrived once a CTA has received everything and awaited at its
 // end, keeps every CTA resident until the copies out of it are complete
 // (residency only: its arrive orders nothing).
+template <bool kStep>
 __device__ __forceinline__ void cluster_combine(const AttnArgs &a, Ctl &S, uint8_t *tile, uint32_t tmem, int item,
                                                 int tid, int warp, int lane) {
   const int C = a.C;
@@ -322,21 +455,25 @@ __device__ __forceinline__ void cluster_combine(const AttnArgs &a, Ctl &S, uint8
   const int64_t gp = a.p0 + tok;
   const int dc = D / C;                              // dims per owner (>= 64: a warp's 32 dims have one owner)
   const uint32_t slot = (uint32_t)dc * 128;          // one source's rows
-  float(*mlr)[2][H] = reinterpret_cast<float(*)[2][H]>(tile);            // received: [source][max, sum][head]
-  uint8_t *parts = tile + kCombineParts;                                  // received: [source][row][128 B]
-  float(*wgt)[H] = reinterpret_cast<float(*)[H]>(tile + kCombineWgt);     // [source][head]
-  uint8_t *stage = tile + kCombineStage;                                  // sent: [owner][row][128 B]
+  constexpr int kMl = kStep ? 3 : 2;
+  float(*mlr)[kMl][H] = reinterpret_cast<float(*)[kMl][H]>(tile);         // received: [source][max, sum][head]
+  uint8_t *parts = tile + combine_parts(kStep);                           // received: [source][row][128 B]
+  float(*wgt)[H] = reinterpret_cast<float(*)[H]>(tile + combine_wgt(kStep));   // [source][head]
+  uint8_t *stage = tile + combine_stage(kStep);                           // sent: [owner][row][128 B]
   const int q4 = warp & 3, wh = warp >> 2;
   const uint32_t s_row = tmem + ((uint32_t)(32 * q4) << 16);
 
+  bool write = true;
+  if constexpr (kStep) write = !a.step.cu || gp < a.step.cu[a.step.batch];   // not behind the last sequence
   // inv_l / mfin / lfin, which warps 0 .. 3 wrote, are visible (the products'
   // end alone does not say so: a chunk without keys takes the divide's slow
   // path, whose first fetch of instructions can outlast them)
   bar_named(1, kWorkers);
-  if (tid == 0) mbar_arrive_expect_tx(&S.comb, (uint32_t)(C - 1) * (slot + 2 * H * 4));
+  if (tid == 0) mbar_arrive_expect_tx(&S.comb, (uint32_t)(C - 1) * (slot + kMl * H * 4));
   if (tid < H) {
     mlr[rank][0][tid] = S.mfin[tid];   // sent to the peers from here, and this CTA's own
     mlr[rank][1][tid] = S.lfin[tid];
+    if constexpr (kStep) mlr[rank][kMl - 1][tid] = reinterpret_cast<const StepScale *>(tile + kStepScaleOff)->l2fin[tid];
   }
   tc_fence_after();
 #pragma unroll 1
@@ -369,7 +506,7 @@ __device__ __forceinline__ void cluster_combine(const AttnArgs &a, Ctl &S, uint8
   if (tid < C && tid != (int)rank) {
     const uint32_t bar = dsmem_addr(&S.comb, (uint32_t)tid);
     bulk_s2s_cluster(dsmem_addr(parts + rank * slot, (uint32_t)tid), stage + tid * slot, slot, bar);
-    bulk_s2s_cluster(dsmem_addr(&mlr[rank][0][0], (uint32_t)tid), &mlr[rank][0][0], 2 * H * 4, bar);
+    bulk_s2s_cluster(dsmem_addr(&mlr[rank][0][0], (uint32_t)tid), &mlr[rank][0][0], kMl * H * 4, bar);
   }
   wait_ft(S, &S.comb, 0);   // every peer's rows and max / sum have landed
   __syncwarp();
@@ -386,14 +523,20 @@ __device__ __forceinline__ void cluster_combine(const AttnArgs &a, Ctl &S, uint8
     float L = 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
-      lc[c] = mc[c] == -INFINITY ? 0.0f : lc[c] * exp2f(mc[c] - M);
-      L += lc[c];
+      if constexpr (kStep) {
+        const float e = mc[c] == -INFINITY ? 0.0f : exp2f(mc[c] - M);
+        L = fmaf(lc[c], e, L);
+        lc[c] = c < C ? mlr[c][kMl - 1][tid] * e : 0.0f;
+      } else {
+        lc[c] = mc[c] == -INFINITY ? 0.0f : lc[c] * exp2f(mc[c] - M);
+        L += lc[c];
+      }
     }
     const float invL = L > 0.0f ? 1.0f / L : 0.0f;
 #pragma unroll
     for (int c = 0; c < 8; ++c)
       if (c < C) wgt[c][tid] = lc[c] * invL;
-    if (rank == 0 && a.lse) a.lse[gp * H + tid] = L > 0.0f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    if (rank == 0 && a.lse && write) a.lse[gp * H + tid] = L > 0.0f || (kStep && L != 0.0f) ? (M + log2f(L)) * kLn2 : -INFINITY;
   }
   bar_named(1, kWorkers);
   // this CTA's dims d, heads 32 wh .. + 31
@@ -427,8 +570,14 @@ __device__ __forceinline__ void cluster_combine(const AttnArgs &a, Ctl &S, uint8
         }
       }
     }
+    if constexpr (kStep) {
+      if (write)
 #pragma unroll
-    for (int i = 0; i < 32; ++i) outp[(wh * 32 + i) * D + d] = acc[i] * keep;
+        for (int i = 0; i < 32; i += 2) put_pair(a.step.out, gp * H + wh * 32 + i, d, acc[i] * keep, acc[i + 1] * keep);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) outp[(wh * 32 + i) * D + d] = acc[i] * keep;
+    }
   }
   __syncwarp();
   cluster_wait();
@@ -488,7 +637,7 @@ __device__ __forceinline__ void load_q(const AttnArgs &a, Ctl &S, const CUtensor
   }
 }
 
-template <bool kSingle>
+template <bool kSingle, bool kStep>
 __global__ void __launch_bounds__(kThreads, 1)
     sparse_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
@@ -499,6 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // kSingle: every CTA holds one item of one block (up to 160 rows), and P^T
   // and the reductions live in the Q region once S has read Q
   uint8_t *pbuf = kSingle ? qs : tile + kPOffMulti;
+  const StepScale &scales = *reinterpret_cast<const StepScale *>(tile + kStepScaleOff);   // (kStep)
   float(*red)[H] = reinterpret_cast<float(*)[H]>(kSingle ? qs + kRedOffSingle : tile + kRedOffMulti);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -545,8 +695,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool row0 = first_item < items && e0 >= 0 && (warp < kMmaWarp || e0 < a.Bk);
   Item it0;
   int32_t id0 = -1;
-  if (row0) {
-    it0 = item_info(a, first_item);
+  if constexpr (kStep) {   // (by whole warps)
+    if (first_item < items && warp != kMmaWarp) it0 = item_info<true>(a, first_item);
+    if (row0) id0 = row_slot(a, it0, e0);
+  } else if (row0) {
+    it0 = item_info<false>(a, first_item);
     id0 = row_slot(a, it0, e0);
   }
 
@@ -558,7 +711,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   RowBuf b0;
   b0.kind = 0;
   b0.scale = 0.0f;
-  if (row0) load_row(a, it0, e0, id0, tid & 1, b0);
+  if (row0) load_row<kStep>(a, it0, e0, id0, tid & 1, b0);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -588,13 +741,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&S.q_ready[p]);
         }
         if (ht < 64) {
-          if (rows && hcp == 0) {
-            S.rs[r] = b0.scale;
-            S.vld[r] = b0.kind != 0 ? 1 : 0;
-          }
+          if (rows && hcp == 0) put_row_info<kStep>(S, tile, r, b0);
 #pragma unroll 1
           for (int p = 0; p < 4; ++p) {
-            if (rows) dequant_front(tile, col_stride, r, hcp + 2 * p, b0);
+            if (rows) dequant_front<kStep>(tile, col_stride, r, hcp + 2 * p, b0);
             fence_proxy_async_smem();
             mbar_arrive(&S.cols_full[p]);
           }
@@ -627,8 +777,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nks = a.Bk / 16;
       uint32_t g = 0, n_item = 0;
       for (int item = first_item; item < items; item += stride, ++n_item) {
-        const Item it = item_info(a, item);
-        for (int j = 0; j < it.nb; ++j, ++g) {
+        int nb;
+        if constexpr (kStep) nb = item_blocks(a, item);
+        else nb = item_info<false>(a, item).nb;
+        for (int j = 0; j < nb; ++j, ++g) {
           const uint32_t ph = g & 1u;
 
           // (no MMA sits under a per-instruction condition: a conditional
@@ -646,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 4; ++i) mma_f16(tmem, a1 + 2 * i, b1 + 2 * i, id_s, 1u);
           }
           mma_commit(&S.s_full);
-          if (j == it.nb - 1 && item + stride < items) {
+          if (j == nb - 1 && item + stride < items) {
             // Q is read by the last block's S: reload it for the next item
             wait_ft(S, &S.s_full, ph);
             if (!S.abort) load_q(a, S, tm_q, qs, item + stride);
@@ -684,12 +836,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     // next block to load into registers, whose top-K slot `ld_id` was
     // requested one block earlier
     int cur_item = first_item, cur_j = 0, cur_nb = 1;
-    Cursor ld;
+    Cursor<kStep> ld;
     ld.item = first_item;
     ld.j = 0;
     int32_t ld_id = -1;
     if (ld.item < items) {   // (the first block's row is in b0 already)
-      ld.it = item_info(a, ld.item);
+      ld.it = item_info<kStep>(a, ld.item);
       cur_nb = ld.it.nb;
       if constexpr (!kSingle) {
         ld.advance(a, stride, items);
@@ -713,33 +865,30 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t g = 0, n_item = 0;
     bool epi_pending = false;
     int epi_item = 0;
-    float m_ref = -INFINITY, l_part = 0.0f;
+    float m_ref = -INFINITY, l_part = 0.0f, l2_part = 0.0f;   // (l2_part: step form)
 
     for (; cur_item < items; ++g) {
       const uint32_t ph = g & 1u;
       const int j = cur_j;
       // ------------------------------------------------------ Q of a new item
       // --------------------------------------------------------- dequant
-      if (cp == 0 && r0 < a.Bk) {
-        S.rs[r0] = b0.scale;
-        S.vld[r0] = b0.kind != 0 ? 1 : 0;
-      }
+      if (cp == 0 && r0 < a.Bk) put_row_info<kStep>(S, tile, r0, b0);
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
         if (g > 0) wait_ft(S, &S.cols_free[p], (g - 1) & 1u);
-        if (r0 < a.Bk) dequant_front(tile, col_stride, r0, cp + 2 * p, b0);
+        if (r0 < a.Bk) dequant_front<kStep>(tile, col_stride, r0, cp + 2 * p, b0);
         fence_proxy_async_smem();
         mbar_arrive(&S.cols_full[p]);
       }
       // the finished item's epilogue overlaps this block's S = Q K^T
       if (epi_pending) {
-        item_epilogue(a, S, epi_item, s_row, tid, q4, wh, lane);
+        item_epilogue<kStep>(a, S, epi_item, s_row, tid, q4, wh, lane);
         epi_pending = false;
       }
       // ------------------------------------------ next block into registers
       if constexpr (!kSingle) {
         if (ld.item < items) {
-          load_row(a, ld.it, ld.j * a.Bk + r0, ld_id, cp, b0);
+          load_row<kStep>(a, ld.it, ld.j * a.Bk + r0, ld_id, cp, b0);
           ld.advance(a, stride, items);
           if (ld.item < items) ld_id = row_slot(a, ld.it, ld.j * a.Bk + r0);
         }
@@ -760,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bar_named(1, kWorkers);   // rs / vld of every row are visible
       if (j == 0) {
         m_ref = -INFINITY;
-        l_part = 0.0f;
+        l_part = l2_part = 0.0f;
       }
       constexpr int kPairs = kSingle ? 3 : 2;   // slab pairs per warp half (blocks of <= 160 / 128 rows)
       // Logits of slab pair mi for this thread: 16 keys from one 16x32bx2
@@ -773,11 +922,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto row_info = [&](int mi, float (&rsv)[16], uint32_t (&vb)[4]) {
         const int k0 = 16 * (2 * (2 * mi + wh) + th);
         const float4 *r4 = reinterpret_cast<const float4 *>(S.rs + k0);
-        const uint4 v4 = *reinterpret_cast<const uint4 *>(S.vld + k0);
-        vb[0] = v4.x;
-        vb[1] = v4.y;
-        vb[2] = v4.z;
-        vb[3] = v4.w;
+        if constexpr (!kStep) {
+          const uint4 v4 = *reinterpret_cast<const uint4 *>(S.vld + k0);
+          vb[0] = v4.x;
+          vb[1] = v4.y;
+          vb[2] = v4.z;
+          vb[3] = v4.w;
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 f4 = r4[q];
@@ -790,10 +941,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto apply = [&](int mi, const uint32_t (&u)[16], const float (&rsv)[16], const uint32_t (&vb)[4],
                        float (&x)[16]) {
         const int k0 = 16 * (2 * (2 * mi + wh) + th);
+        if constexpr (kStep) {
+          // (k0 is the same for half a warp and a block's rows are a multiple of 16)
+          const float4 *l4 = reinterpret_cast<const float4 *>(scales.lg + k0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const bool ok = (k0 + i < a.Bk) && ((vb[i >> 2] >> (8 * (i & 3))) & 0xFFu);
-          x[i] = ok ? __uint_as_float(u[i]) * (kLogit * rsv[i]) : -INFINITY;
+          for (int q = 0; q < 4; ++q) {
+            const float4 g = l4[q];
+            x[4 * q] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q]), rsv[4 * q], g.x) : -INFINITY;
+            x[4 * q + 1] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q + 1]), rsv[4 * q + 1], g.y) : -INFINITY;
+            x[4 * q + 2] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q + 2]), rsv[4 * q + 2], g.z) : -INFINITY;
+            x[4 * q + 3] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q + 3]), rsv[4 * q + 3], g.w) : -INFINITY;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const bool ok = (k0 + i < a.Bk) && ((vb[i >> 2] >> (8 * (i & 3))) & 0xFFu);
+            x[i] = ok ? __uint_as_float(u[i]) * (kLogit * rsv[i]) : -INFINITY;
+          }
         }
       };
       auto logits = [&](int mi, float (&x)[16]) {
@@ -816,9 +980,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           // masked keys hold -inf: 2^-inf = 0 (no branch); m_ref = -inf only when all are masked
           over |= (x[i] > mref_s + kLazy) | (x[i + 1] > mref_s + kLazy);
           const float p0 = ex2_approx(x[i] - mref_s), p1 = ex2_approx(x[i + 1] - mref_s);
-          l_part += p0 + p1;
-          const float2 r2 = *reinterpret_cast<const float2 *>(S.rs + k0 + i);
-          pk[i >> 1] = pack_half2(p0 * r2.x, p1 * r2.y);
+          if constexpr (kStep) {
+            const float2 r2 = *reinterpret_cast<const float2 *>(scales.inv + (k0 < a.Bk ? k0 + i : 0));
+            l_part = fmaf(p0, r2.x, fmaf(p1, r2.y, l_part));
+            l2_part += p0 + p1;
+            pk[i >> 1] = pack_half2(p0, p1);
+          } else {
+            l_part += p0 + p1;
+            const float2 r2 = *reinterpret_cast<const float2 *>(S.rs + k0 + i);
+            pk[i >> 1] = pack_half2(p0 * r2.x, p1 * r2.y);
+          }
         }
         if (k0 < a.Bk) {
           // P^T K-major: [64-key atom column][64 heads][128 B]
@@ -874,10 +1045,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         done_p = true;
       } else {
         if (m_ref != -INFINITY) {
-          const float l_save = l_part;
+          const float l_save = l_part, l2_save = l2_part;
           const bool over = write_p(m_ref);
           done_p = !bar_named_or(2, kWorkers, over);
-          if (!done_p) l_part = l_save;
+          if (!done_p) {
+            l_part = l_save;
+            l2_part = l2_save;
+          }
         }
       }
       if (!done_p) {
@@ -923,6 +1097,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_st_wait();
         }
         l_part *= f;
+        l2_part *= f;
         (void)write_p(m_ref == -INFINITY ? 0.0f : m_ref);
       }
       fence_proxy_async_smem();
@@ -936,12 +1111,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         float(*red_l)[H] = red + (kSingle ? 2 : 0);
         const float lp = l_part + __shfl_xor_sync(0xffffffffu, l_part, 16);
         if (th == 0) red_l[wh][h] = lp;
+        StepScale *sums = reinterpret_cast<StepScale *>(tile + kStepScaleOff);
+        if constexpr (kStep) {
+          const float l2 = l2_part + __shfl_xor_sync(0xffffffffu, l2_part, 16);
+          if (th == 0) sums->red2[wh][h] = l2;
+        }
         bar_named(1, kWorkers);
         if (th == 0 && wh == 0) {
           const float L = red_l[0][h] + red_l[1][h];
           S.lfin[h] = L;
           S.mfin[h] = m_ref;
-          S.inv_l[h] = L > 0.0f ? 1.0f / L : 0.0f;
+          if constexpr (kStep) {
+            const float L2 = sums->red2[0][h] + sums->red2[1][h], n = a.C > 1 ? L2 : L;
+            sums->l2fin[h] = L2;
+            S.inv_l[h] = n > 0.0f ? 1.0f / n : 0.0f;
+          } else {
+            S.inv_l[h] = L > 0.0f ? 1.0f / L : 0.0f;
+          }
         }
         epi_pending = true;
         epi_item = this_item;
@@ -952,9 +1138,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the last item: wait for its products, then write (C = 1) or combine
       // across the cluster (C > 1: the CTA's one item)
       wait_ft(S, &S.cols_free[3], (g - 1) & 1u);
-      if (a.C == 1) item_epilogue(a, S, epi_item, s_row, tid, q4, wh, lane);
+      if (a.C == 1) item_epilogue<kStep>(a, S, epi_item, s_row, tid, q4, wh, lane);
     }
-    if (a.C > 1) cluster_combine(a, S, tile, tmem, first_item, tid, warp, lane);
+    if (a.C > 1) cluster_combine<kStep>(a, S, tile, tmem, first_item, tid, warp, lane);
   }
 
   tc_fence_before();
@@ -980,7 +1166,7 @@ int max_active_clusters(int c, int sms) {
   if (c < 1 || c > 8) return 0;
   if (cache[c]) return cache[c];
   int n = 0;
-  auto kern = sparse_attn_kernel<true>;
+  auto kern = sparse_attn_kernel<true, false>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)c, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -1049,20 +1235,22 @@ cudaError_t launch_sparse_attn(AttnArgs a, void *scratch, cudaStream_t stream, i
   const bool one_item = grid >= items;
   const int r16 = max_r > 16 ? (max_r + 15) / 16 * 16 : 16;
   // one block per CTA (its rows past 128 must be entries: SWA rows come first)
-  const bool single = one_item && r16 <= kMaxBk && (a.W + a.C - 1) / a.C <= kBlockRows;
+  const bool step = a.step.out != nullptr;
+  const bool single = one_item && r16 <= (step ? kMaxBkStep : kMaxBk) && (a.W + a.C - 1) / a.C <= kBlockRows;
   a.Bk = single ? r16 : kBlockRows;
   (void)scratch;
   CUtensorMap tm_q;
   if (!make_tmap_bf16(&tm_q, a.q, D, (a.p0 + a.problems) * H, H)) return cudaErrorInvalidValue;
-  auto kern = single ? sparse_attn_kernel<true> : sparse_attn_kernel<false>;
+  auto kern = step ? (single ? sparse_attn_kernel<true, true> : sparse_attn_kernel<false, true>)
+                   : (single ? sparse_attn_kernel<true, false> : sparse_attn_kernel<false, false>);
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (err != cudaSuccess) return err;
   const ProfileEvents &pe = profile_events(CSA2_KERNEL_SPARSE_ATTN);
-  if (pe.start && (err = record_profile_event(pe.start, stream)) != cudaSuccess) return err;
+  if (!step && pe.start && (err = record_profile_event(pe.start, stream)) != cudaSuccess) return err;
   err = launch_pdl(kern, dim3((unsigned)grid), dim3(kThreads), kSmemBytes, stream, (unsigned)a.C, tm_q, a);
   if (err != cudaSuccess) return err;
   ++*launches;
-  if (pe.stop && (err = record_profile_event(pe.stop, stream)) != cudaSuccess) return err;
+  if (!step && pe.stop && (err = record_profile_event(pe.stop, stream)) != cudaSuccess) return err;
   return cudaSuccess;
 }
 

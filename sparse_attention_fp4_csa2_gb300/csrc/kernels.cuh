@@ -193,6 +193,22 @@ TopkScratch carve_topk_scratch(void *base, int32_t rows, int64_t row_len, int32_
 cudaError_t launch_pool_topk(const TopkRows &r, void *scratch, int num_sms, cudaStream_t stream, int *launches);
 cudaError_t launch_topk(const TopkRows &r, const TopkScratch &s, int num_sms, cudaStream_t stream, int *launches);
 
+// Where a step's token takes its 8-bit rows from (window_attn and tree_attn):
+// `win` rows of its sequence's ring, in which position p has row p mod ring,
+// and up to 64 extra rows of its sequence (the first tokens, or a tree's).
+// cu != NULL: packed tokens with a causal window, the extra rows its sinks;
+// NULL: `extras` tokens per sequence, each with the extra rows of its mask.
+struct StepRows {
+  const int32_t *cu;          // [batch + 1]
+  const int32_t *ctx_len;     // [batch]
+  const uint64_t *mask;       // [tokens]
+  const uint8_t *extra;       // [batch][extras][512] (E4M3)
+  const float *extra_scale;   // [batch][extras]
+  __nv_bfloat16 *out;         // [tokens][64][512]; NULL: not this form
+  int64_t ring;
+  int32_t batch, win, extras;
+};
+
 struct AttnArgs {
   const __nv_bfloat16 *q;     // [P][64][512]
   const uint8_t *kv;          // [B][cap][288]
@@ -220,7 +236,26 @@ struct AttnArgs {
   int64_t swa_first_pos;
   int64_t swa_seq_rows;
   int32_t kernel;             // 0 automatic, 1 split into chunks, 2 one chunk per token
+  StepRows step;              // step.out: this form instead (W = win + extras)
 };
+
+// The sequence of packed token i: the last b with cu[b] <= i < cu[batch] (false
+// when there is none).  Called by whole warps: 32 probes at a time.
+__device__ __forceinline__ bool find_sequence(const int32_t *cu, int32_t batch, int64_t i, int &b) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = batch;   // the answer is one of lo .. lo + n - 1
+  if (i >= cu[batch]) return false;
+  while (n > 1) {
+    const int step = (n + 31) >> 5;
+    const int at = lo + lane * step;
+    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && cu[at] <= i);
+    const int k = le ? 31 - __clz(le) : 0;
+    lo += k * step;
+    n = min(step, n - k * step);
+  }
+  b = lo;
+  return true;
+}
 
 // Workspace of one readout launch (the chunk partials when tokens are split).
 size_t attn_scratch_bytes(int32_t problems, int32_t K, int32_t W, int32_t kernel);
@@ -241,6 +276,14 @@ cudaError_t launch_swa_read(const uint8_t *swa, const float *swa_scale, int64_t 
                             int64_t k, void *out, cudaStream_t stream);
 cudaError_t launch_indexer_k_read(const uint8_t *k_fp4, int64_t batch, int64_t cap, const int32_t *idx, int64_t k,
                                   void *out, cudaStream_t stream);
+
+// A step's positions and cache rows from its lengths (batch at most
+// kMaxMapBatch: each CTA keeps two prefix sums of them in shared memory).
+constexpr int kMaxMapBatch = 8192;
+cudaError_t launch_slot_map(const int32_t *ctx_len, const int32_t *new_len, int32_t batch, int32_t m, int64_t cap,
+                            int64_t ring, int64_t n_tokens, int64_t n_entries, int32_t *cu, int32_t *tok_seq,
+                            int64_t *pos, int64_t *swa_slot, int32_t *entry_cu, int64_t *entry_pos, int64_t *slot,
+                            int32_t *n_vis, int32_t *swa_len, int num_sms, cudaStream_t stream);
 
 // Dense readout of seqs x n_q tokens over the first n_vis[b] (NULL: n_max)
 // entries of their sequence, merged with own_out / own_lse (fp32 rows and

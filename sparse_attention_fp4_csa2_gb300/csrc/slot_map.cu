@@ -1,0 +1,188 @@
+// From the lengths of a step's requests, the positions and cache rows that the
+// writers take (csa2_slot_map).
+//
+// Token r of sequence b sits at position p = ctx[b] + r and has row p mod ring
+// of the sequence's ring; the entries that the step completes are ctx[b] / m ..
+// (ctx[b] + new[b]) / m - 1, entry e at position m e + m - 1 and row e of the
+// sequence's main cache.  Token i of the packed step belongs to the last
+// sequence whose exclusive prefix sum of the lengths is at most i.
+//
+// What it has to move: 8 bytes a sequence in, 16 out, 20 bytes a token and 16 an
+// entry out; small calls are the launch and the scan's latency.  One launch, no
+// pass between CTAs: each CTA scans all the lengths itself (8,192 at most, which
+// stay in L2), keeps both prefix sums in shared memory and takes every
+// gridDim-th stretch of the tokens and entries, finding a token's sequence by
+// binary search there.
+#include "kernels.cuh"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kMapThreads = 512;
+
+struct SlotArgs {
+  const int32_t *ctx_len, *new_len;
+  int32_t *cu, *tok_seq;
+  int64_t *pos, *swa_slot;
+  int32_t *entry_cu;
+  int64_t *entry_pos, *slot;
+  int32_t *n_vis, *swa_len;
+  int64_t cap, ring, n_tokens, n_entries;
+  int32_t batch, m;
+};
+
+// Exclusive prefix sums of two counts per thread over the CTA; the totals in
+// every thread.
+__device__ __forceinline__ void scan_pair(int64_t &a, int64_t &b, int64_t (*part)[2], int64_t &ta, int64_t &tb) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int64_t a0 = a, b0 = b;
+#pragma unroll
+  for (int o = 1; o < 32; o *= 2) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
+    if (lane >= o) {
+      a += x;
+      b += y;
+    }
+  }
+  if (lane == 31) {
+    part[warp][0] = a;
+    part[warp][1] = b;
+  }
+  __syncthreads();
+  ta = tb = 0;
+  int64_t ba = 0, bb = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w == warp) {
+      ba = ta;
+      bb = tb;
+    }
+    ta += part[w][0];
+    tb += part[w][1];
+  }
+  a += ba - a0;
+  b += bb - b0;
+}
+
+// The last b with cu[b] <= i (cu[0] = 0, i >= 0).
+__device__ __forceinline__ int sequence_of(const int32_t *cu, int batch, int32_t i) {
+  int lo = 0, n = batch;
+  while (n > 1) {
+    const int half = n >> 1;
+    if (cu[lo + half] <= i) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a) {
+  extern __shared__ int32_t sums[];   // [batch + 1] tokens, [batch + 1] entries
+  __shared__ int64_t part[kMapThreads / 32][2];
+  int32_t *tok = sums, *ent = sums + a.batch + 1;
+  pdl_wait();
+  const int per = (a.batch + blockDim.x - 1) / blockDim.x;
+  const int b0 = min((int)threadIdx.x * per, a.batch), b1 = min(b0 + per, a.batch);
+  int64_t t = 0, e = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int64_t c = max(a.ctx_len[b], 0), n = max(a.new_len[b], 0);
+    t += n;
+    e += (c + n) / a.m - c / a.m;
+  }
+  int64_t tokens, entries;
+  scan_pair(t, e, part, tokens, entries);
+  const bool first = blockIdx.x == 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    const int32_t c0 = a.ctx_len[b], n0 = a.new_len[b];
+    const int64_t c = max(c0, 0), n = max(n0, 0);
+    // sums past 32 bits name no token of the outputs: they stay at the largest
+    tok[b] = (int32_t)min(t, (int64_t)INT32_MAX);
+    ent[b] = (int32_t)min(e, (int64_t)INT32_MAX);
+    t += n;
+    e += (c + n) / a.m - c / a.m;
+    if (first) {
+      a.cu[b] = tok[b];
+      a.entry_cu[b] = ent[b];
+      a.n_vis[b] = (int32_t)min(min((c + n) / a.m, a.cap), (int64_t)INT32_MAX);
+      a.swa_len[b] = (int32_t)min(min(c + n, a.ring), (int64_t)INT32_MAX);
+      bad |= c0 < 0 || n0 < 0 || (c + n) / a.m > a.cap;
+    }
+  }
+  if (threadIdx.x == 0) {
+    tok[a.batch] = (int32_t)min(tokens, (int64_t)INT32_MAX);
+    ent[a.batch] = (int32_t)min(entries, (int64_t)INT32_MAX);
+    if (first) {
+      a.cu[a.batch] = tok[a.batch];
+      a.entry_cu[a.batch] = ent[a.batch];
+      bad |= tokens > a.n_tokens || entries > a.n_entries;
+    }
+  }
+  if (bad) set_error(CSA2_DEV_ERR_NVIS);
+  __syncthreads();
+  pdl_release();
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x, i0 = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  for (int64_t i = i0; i < a.n_tokens; i += stride) {
+    int32_t seq = -1;
+    int64_t pos = -1, slot = -1;
+    if (i < tok[a.batch]) {
+      seq = sequence_of(tok, a.batch, (int32_t)i);
+      const int32_t r = (int32_t)i - tok[seq];
+      pos = (int64_t)max(a.ctx_len[seq], 0) + r;
+      // (a row that a later token of the step takes again is written once, by that one)
+      if (a.new_len[seq] - r <= a.ring) slot = (int64_t)seq * a.ring + (uint64_t)pos % (uint64_t)a.ring;
+    }
+    a.tok_seq[i] = seq;
+    a.pos[i] = pos;
+    a.swa_slot[i] = slot;
+  }
+  for (int64_t i = i0; i < a.n_entries; i += stride) {
+    int64_t pos = -1, slot = -1;
+    if (i < ent[a.batch]) {
+      const int seq = sequence_of(ent, a.batch, (int32_t)i);
+      const int64_t e1 = (int64_t)max(a.ctx_len[seq], 0) / a.m + ((int32_t)i - ent[seq]);
+      pos = e1 * a.m + a.m - 1;
+      if (e1 < a.cap) slot = seq * a.cap + e1;
+    }
+    a.entry_pos[i] = pos;
+    a.slot[i] = slot;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_slot_map(const int32_t *ctx_len, const int32_t *new_len, int32_t batch, int32_t m, int64_t cap,
+                            int64_t ring, int64_t n_tokens, int64_t n_entries, int32_t *cu, int32_t *tok_seq,
+                            int64_t *pos, int64_t *swa_slot, int32_t *entry_cu, int64_t *entry_pos, int64_t *slot,
+                            int32_t *n_vis, int32_t *swa_len, int num_sms, cudaStream_t stream) {
+  SlotArgs a;
+  a.ctx_len = ctx_len;
+  a.new_len = new_len;
+  a.cu = cu;
+  a.tok_seq = tok_seq;
+  a.pos = pos;
+  a.swa_slot = swa_slot;
+  a.entry_cu = entry_cu;
+  a.entry_pos = entry_pos;
+  a.slot = slot;
+  a.n_vis = n_vis;
+  a.swa_len = swa_len;
+  a.cap = cap;
+  a.ring = ring;
+  a.n_tokens = n_tokens;
+  a.n_entries = n_entries;
+  a.batch = batch;
+  a.m = m;
+  const int64_t rows = n_tokens > n_entries ? n_tokens : n_entries;
+  int64_t ctas = (rows + kMapThreads - 1) / kMapThreads;
+  ctas = ctas < 1 ? 1 : ctas < 4 * num_sms ? ctas : 4 * num_sms;
+  const size_t smem = (size_t)2 * (batch + 1) * sizeof(int32_t);
+  const cudaError_t e = cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(slot_map_kernel, dim3((unsigned)ctas), dim3(kMapThreads), smem, stream, 0u, a);
+}
+
+}  // namespace csa2
