@@ -63,18 +63,27 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
 
 }  // namespace
 
-// 2-D bf16 tensor map over rows of `inner` elements, box {64, box_rows}, 128B swizzle.
-bool make_tmap_bf16(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows) {
+// 2-D bf16 tensor map over rows of `inner` elements, box {64, box_rows}, 128B
+// swizzle (half: box {32, box_rows}, 64B swizzle).
+static bool make_tmap_bf16_box(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows, bool half) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[2] = {(cuuint64_t)inner, (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)inner * 2};
-  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t box[2] = {half ? 32u : 64u, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+
+bool make_tmap_bf16(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows) {
+  return make_tmap_bf16_box(m, ptr, inner, rows, box_rows, false);
+}
+
+bool make_tmap_bf16_half(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows) {
+  return make_tmap_bf16_box(m, ptr, inner, rows, box_rows, true);
 }
 
 namespace {
@@ -820,7 +829,10 @@ csa2_status run_step(const csa2_params *p, int64_t tokens, const void *q, const 
   a.kernel = p->attn_kernel;
   a.step = s;
   int launches = 0;
-  if (launch_sparse_attn(a, nullptr, stream, &launches) != cudaSuccess) return CSA2_ERR_CUDA;
+  const bool shared = !topk_idx && p->attn_kernel == 0 && window_rows_fit(s);
+  const cudaError_t e = shared ? launch_window_attn(q, swa, swa_scale, s, tokens, lse, num_sms(), stream, &launches)
+                               : launch_sparse_attn(a, nullptr, stream, &launches);
+  if (e != cudaSuccess) return CSA2_ERR_CUDA;
   g_last_launches = launches;
   return CSA2_OK;
 }

@@ -105,6 +105,8 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 
 // 2-D bf16 tensor map over rows of `inner` elements, box {64, box_rows}, 128B swizzle.
 bool make_tmap_bf16(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows);
+// The same with boxes of 32 elements and 64B swizzle.
+bool make_tmap_bf16_half(CUtensorMap *m, const void *ptr, int64_t inner, int64_t rows, uint32_t box_rows);
 
 // w_ik != NULL: also the entry's indexer key k = W_ik e into k_out (bf16 rows,
 // or the MXFP4 planes with fp4), row slot[i] of k_rows.
@@ -265,6 +267,12 @@ cudaError_t attn_take_error(unsigned int *bits);
 // CTAs of a readout of `problems` tokens.
 int attn_ctas(int32_t problems, int32_t K, int32_t W, int32_t kernel);
 cudaError_t launch_sparse_attn(AttnArgs a, void *scratch, cudaStream_t stream, int *launches);
+
+// The step form without entries, in tiles of two tokens that share their rows:
+// for windows and extra rows that fit in a tile.
+bool window_rows_fit(const StepRows &s);
+cudaError_t launch_window_attn(const void *q, const uint8_t *swa, const float *swa_scale, const StepRows &s, int64_t tokens,
+                               float *lse, int num_sms, cudaStream_t stream, int *launches);
 
 // Sliding-window rows as FP8 (pos NULL: no RoPE) and the caches' read-backs
 // (idx NULL: rows 0 .. k - 1 of each sequence).
