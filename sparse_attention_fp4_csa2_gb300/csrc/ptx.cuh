@@ -198,6 +198,12 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void *p) {
   return v;
 }
 
+__device__ __forceinline__ uint2 ld_nc_v2(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
 __device__ __forceinline__ uint32_t ld_nc_u32(const void *p) {
   uint32_t v;
   asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));

@@ -161,10 +161,9 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------- rows
-// 16 codes of a row (a lane's: channels 16 lane ..) as bf16 into slot `slot`: two
-// 16-byte chunks of the 128B-swizzled row in column block lane / 4.  Lanes of odd
-// blocks write their second chunk first (a quarter warp's eight then cover the
-// eight bank groups).
+// A row's codes as bf16 in a slot: a lane takes channels 8 lane .. + 7 and those 256
+// behind them, a 16-byte chunk of the 128B-swizzled row in column blocks lane / 8
+// and lane / 8 + 4 each (eight lanes a whole 128-byte row).
 // Two E4M3 codes (bytes 0 and 1, or 2 and 3, of w: `sel`) as bf16: exponent and
 // fraction moved to bf16's places are the value times 2^-120, subnormals too.
 __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w, uint32_t sel) {
@@ -175,35 +174,22 @@ __device__ __forceinline__ uint32_t e4m3x2_to_bf16x2(uint32_t w, uint32_t sel) {
   return *reinterpret_cast<const uint32_t *>(&v);
 }
 
-// True when the row holds a NaN.  A NaN code becomes a NaN weight (slot_scale: the
-// row's logit is a NaN, so every channel of a token that sees it is) and a zero in
-// the slot, where a token that does not see it multiplies it by a weight of zero.
-__device__ __forceinline__ bool put_row(uint8_t *tile, int slots, int slot, const uint4 &v, bool tiny, int lane) {
+// True when the row holds a NaN, which the slot has as 480: it becomes a NaN weight
+// (slot_scale: the row's logit is a NaN, so every channel of a token that sees it
+// is), and a token that does not see it multiplies the slot by a weight of zero.
+__device__ __forceinline__ bool put_row(uint8_t *at, uint32_t half, int slot, const uint4 &v, bool tiny, int lane) {
   uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t nan = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) nan |= (w[i] & 0x7F7F7F7Fu) + 0x01010101u;
-  nan &= 0x80808080u;
-  const bool bad = __any_sync(0xffffffffu, nan != 0);
-  if (bad || tiny) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = tiny ? 0u : w[i] & ~__vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-  }
-  uint32_t o[2][4];
+  if (tiny) w[0] = w[1] = w[2] = w[3] = 0;
+  uint8_t *dst = at + slot * 128 + (((lane ^ slot) & 7) << 4);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[i][j] = e4m3x2_to_bf16x2(w[2 * i + (j >> 1)], j & 1 ? 0x3424 : 0x1404);
-  uint8_t *row = tile + (size_t)(lane >> 2) * slots * 128 + (size_t)slot * 128;
-  const int c = 2 * (lane & 3), odd = (lane >> 2) & 1, sw = slot & 7;
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const bool second = i ^ odd;
-    *reinterpret_cast<uint4 *>(row + (((c + second) ^ sw) << 4)) =
-        make_uint4(second ? o[1][0] : o[0][0], second ? o[1][1] : o[0][1], second ? o[1][2] : o[0][2],
-                   second ? o[1][3] : o[0][3]);
-  }
-  return bad;
+    *reinterpret_cast<uint4 *>(dst + i * half) =
+        make_uint4(e4m3x2_to_bf16x2(w[2 * i], 0x1404), e4m3x2_to_bf16x2(w[2 * i], 0x3424),
+                   e4m3x2_to_bf16x2(w[2 * i + 1], 0x1404), e4m3x2_to_bf16x2(w[2 * i + 1], 0x3424));
+  return __any_sync(0xffffffffu, nan & 0x80808080u);
 }
 
 // What the softmax has to know of a slot (one thread).
@@ -221,7 +207,11 @@ __device__ __forceinline__ void get_rows(uint4 (&v)[kRows], const uint8_t *row, 
 #pragma unroll
   for (int j = 0; j < kRows; ++j) {
     const uint8_t *p = reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(row), j));
-    v[j] = p ? ld_nc_v4(p + 16 * lane) : make_uint4(0, 0, 0, 0);
+    v[j] = make_uint4(0, 0, 0, 0);
+    if (p) {
+      const uint2 a = ld_nc_v2(p + 8 * lane), b = ld_nc_v2(p + 256 + 8 * lane);
+      v[j] = make_uint4(a.x, a.y, b.x, b.y);
+    }
   }
 }
 
@@ -289,9 +279,11 @@ __device__ void fill_slots(const WindowArgs &a, CtlW &S, uint8_t *tile, const Ti
   const uint32_t tiny = __ballot_sync(0xffffffffu, scale < kTinyScaleW);
   if (i > 0) wait_w(S, &S.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
   uint32_t bad = 0;
+  const uint32_t half = 4 * a.slots * 128;
+  tile += (lane >> 3) * a.slots * 128;
 #pragma unroll
   for (int j = 0; j < kBatch; ++j)
-    if (w + j * warps < a.slots) bad |= (uint32_t)put_row(tile, a.slots, w + j * warps, v[j], tiny >> j & 1, lane) << j;
+    if (w + j * warps < a.slots) bad |= (uint32_t)put_row(tile, half, w + j * warps, v[j], tiny >> j & 1, lane) << j;
   if (lane < kBatch && mine < a.slots) slot_scale(S, mine, scale, bad >> lane & 1);
   fence_proxy_async_smem();
   __syncwarp();
@@ -323,9 +315,10 @@ __device__ void row_warp(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<kTree
         if (s.win > 0) {
           const uint32_t tiny = __ballot_sync(0xffffffffu, scale < kTinyScaleW);
           const int slot = (int)(t.pos % a.ring), second = slot + 1 == a.ring ? 0 : slot + 1;
-          bool bad = put_row(tile, a.slots, slot, ahead[0], tiny & 1, lane);
+          uint8_t *at = tile + (lane >> 3) * a.slots * 128;
+          bool bad = put_row(at, 4 * a.slots * 128, slot, ahead[0], tiny & 1, lane);
           if (t.n > 1) {
-            const bool b = put_row(tile, a.slots, second, ahead[1], tiny >> 1 & 1, lane);
+            const bool b = put_row(at, 4 * a.slots * 128, second, ahead[1], tiny >> 1 & 1, lane);
             if (lane == 1) bad = b;
           }
           if (lane < t.n) slot_scale(S, lane ? second : slot, scale, bad);
