@@ -829,9 +829,16 @@ csa2_status run_step(const csa2_params *p, int64_t tokens, const void *q, const 
   a.kernel = p->attn_kernel;
   a.step = s;
   int launches = 0;
-  const bool shared = !topk_idx && p->attn_kernel == 0 && window_rows_fit(s);
-  const cudaError_t e = shared ? launch_window_attn(q, swa, swa_scale, s, tokens, lse, num_sms(), stream, &launches)
-                               : launch_sparse_attn(a, nullptr, stream, &launches);
+  // Up to a token for two SMs, its keys are split over a cluster (32 window tokens
+  // 14.5 us against 16.2 in tiles, 76 16.3 against 20.0; 80 of four sequences 19.3
+  // against 18.3, 100 21.8 against 21.4); more tokens go in tiles of two that share
+  // their rows where these are all a token has and fit, else a CTA takes one.
+  const int sms = num_sms();
+  const bool split = p->attn_kernel == 1 || (p->attn_kernel == 0 && 2 * tokens <= sms);
+  const bool shared = p->attn_kernel == 0 && !topk_idx && window_rows_fit(s);
+  const cudaError_t e = split    ? launch_sparse_attn(a, nullptr, stream, &launches)
+                        : shared ? launch_window_attn(q, swa, swa_scale, s, tokens, lse, sms, stream, &launches)
+                                 : launch_gather_attn(a, sms, stream, &launches);
   if (e != cudaSuccess) return CSA2_ERR_CUDA;
   g_last_launches = launches;
   return CSA2_OK;

@@ -47,7 +47,7 @@
 // allots each warp role the registers its setmaxnreg asks for (with
 // separate compilation it ignores setmaxnreg); it keeps its own error word.
 #define CSA2_WHOLE_PROGRAM_TU 1
-#include "kernels.cuh"
+#include "step_rows.cuh"
 
 namespace csa2 {
 
@@ -144,40 +144,18 @@ struct Item {
   int first;
 };
 
-// The token's keys in the step form: its sequence, the ring place and the first
-// visible one of its window rows, and its extra rows.  Called by whole warps.
-// Nothing read from the device makes an address: whatever ctx_len, cu and the
-// masks hold, ring0 < ring and seq < batch.
+// The token's keys in the step form.  Called by whole warps.
 __device__ __forceinline__ bool step_rows(const AttnArgs &a, int64_t gp, Item &it) {
-  const StepRows &s = a.step;
-  int64_t seq, end;   // the last committed position the window may hold, plus one
-  int left;           // window rows up to there
-  if (s.cu) {         // packed tokens: a causal window and the first tokens as sinks
-    int b;
-    if (!find_sequence(s.cu, s.batch, gp, b)) return false;
-    seq = b;
-    const int64_t r = gp - s.cu[b], ctx = max(s.ctx_len[b], 0);
-    end = ctx + r + 1;
-    left = s.win;
-    const int64_t before = end - s.win;   // positions that the window has left behind
-    const int sinks = (int)(before < s.extras ? (before > 0 ? before : 0) : s.extras);
-    it.extra = sinks >= 64 ? ~0ull : (1ull << sinks) - 1;
-    if (s.ctx_len[b] < 0 || s.win > 0 && min(ctx, (int64_t)s.win - 1) + (s.cu[b + 1] - s.cu[b]) > s.ring) set_error(CSA2_DEV_ERR_INDEX);
-  } else {            // a tree's tokens: the rows their mask names, and the window's rest
-    seq = (int64_t)((uint32_t)gp / (uint32_t)s.extras);
-    const int32_t c = s.ctx_len[seq];
-    if (c < 0) set_error(CSA2_DEV_ERR_INDEX);
-    it.extra = s.mask[gp] & (s.extras >= 64 ? ~0ull : (1ull << s.extras) - 1);
-    end = max(c, 0);
-    left = max(s.win - __popcll(it.extra), 0);
-  }
-  const int64_t start = end - s.win;   // window row 0's position; rows below position 0 hold no key
-  it.first = (int)max((int64_t)(s.win - left), -start);
-  const int64_t m = start % s.ring;
-  it.ring0 = m < 0 ? m + s.ring : m;
-  it.swa_row0 = seq * s.ring;
-  it.extra0 = seq * s.extras;
-  it.seq_row0 = seq * a.cap;
+  StepToken t;
+  if (!step_token(a.step, gp, t)) return false;
+  const int64_t start = t.end - a.step.win;   // window row 0's position; rows below position 0 hold no key
+  it.extra = t.extra;
+  it.first = (int)max((int64_t)(a.step.win - t.left), -start);
+  const int64_t m = start % a.step.ring;
+  it.ring0 = m < 0 ? m + a.step.ring : m;
+  it.swa_row0 = t.seq * a.step.ring;
+  it.extra0 = t.seq * a.step.extras;
+  it.seq_row0 = t.seq * a.cap;
   return true;
 }
 
@@ -385,16 +363,6 @@ struct Cursor {
     }
   }
 };
-
-// Channel d (a lane's; a warp's 32 are consecutive) of rows `row` and row + 1
-// as bf16: neighbouring lanes exchange, so that the even one stores two channels
-// of the first row and the odd one two of the second.
-__device__ __forceinline__ void put_pair(__nv_bfloat16 *out, int64_t row, int d, float x, float y) {
-  const bool odd = d & 1;
-  const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
-  const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(other, y) : __floats2bfloat162_rn(x, other);
-  *reinterpret_cast<__nv_bfloat162 *>(out + (row + odd) * D + (d & ~1)) = v;
-}
 
 // The finished item's output: out = O^T / l (C = 1), or (C > 1) this chunk's
 // (m, l) and its normalised partial (fp16, [dim][head]) for the dims the other

@@ -1,0 +1,569 @@
+// The step form of the readout, one CTA per token: a token's listed main-KV
+// entries, its window rows and its extra rows (csa2_tree_attn; csa2_window_attn
+// when its rows do not fit in the tiles of window_attn.cu), in one softmax:
+//   o_h = sum_k softmax_k(q_h . v_k s_k / sqrt(512)) v_k s_k,
+// v_k an entry's 512 values (E2M1 x E4M3, s_k = 1) or a row's E4M3 codes, s_k its
+// scale, all exact in fp16.
+//
+// No two tokens list the same entries, so a token's 64 heads are all that share a
+// key: 4 x 64 x 512 flop for 288 bytes, which the tensor cores take as products of
+// 64 rows at a quarter of their rate.  What bounds it is the SM's shared-memory
+// pipe: a step of 64 keys passes 512 wavefronts of fp16 stores, some 580 of
+// arriving entry sectors, 1,024 of operands of S and 768 of the second product.
+// So the keys go through in steps of 64 in two slots of 64 KB, every part of the
+// work on warps of its own, a step's rows being converted while the step before is
+// in its softmax and products:
+//   rows     8 warps: eight lanes on 128 contiguous bytes of an entry, loaded a
+//            step ahead into registers, written as fp16 into the slot [8 x 64
+//            channels][64 keys][128 B], 128B-swizzled;
+//   S        M = 64 heads, N = 64 keys, K = 512, in two accumulators in turn
+//            (products into one wait for each other), two S buffers;
+//   softmax  4 warps, a head's 64 logits on two lanes; the reference maximum (over
+//            logit + log2(s_k)) is raised only past 2^8, O^T then rescaled; P to
+//            shared memory as fp16;
+//   O^T += V^T P^T  M = 128 channels (four blocks), N = 64 heads, K = 64 keys, V^T
+//            from the same slot; its end frees the slot;
+//   rows out O^T read per channel, pairs of channels stored as bf16, while the next
+//            token's first steps are converted and multiplied.
+// Keys that the token does not see take no place: the window's visible rows, the
+// named extra rows, then the list (whose -1 are masked).
+//
+// Warps: 0-3 softmax, 4-11 rows, 12 S, 13 second product.  Every wait is bounded;
+// after one runs out every role falls through its waits and the output is
+// undefined (CSA2_DEV_ERR_TIMEOUT).
+#include "step_rows.cuh"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kSoftG = 4, kRowG = 8;
+constexpr int kScoreWarpG = kSoftG + kRowG, kValueWarpG = kScoreWarpG + 1;
+constexpr int kThreadsG = (kValueWarpG + 1) * 32;   // 144 registers a thread
+constexpr int kStep = 64;                    // keys of a step
+constexpr int kSlotG = kStep * D * 2;
+constexpr int kBlockG = kStep * 128;         // a column block of 64 channels: of a slot, of Q, a buffer of P
+constexpr uint32_t kColOG = 256;             // tensor memory: S at 128 slot + 64 accumulator, O^T at 256
+constexpr float kLogitG = 0.06375871295460785f;   // log2(e) / sqrt(512)
+constexpr float kLn2G = 0.69314718055994531f;
+constexpr float kLazyG = 8.0f;               // log2 margin before the reference is raised
+constexpr float kTinyScaleG = 5.421010862427522e-20f;   // 2^-64: rows of a smaller scale count as zeros
+constexpr uint32_t kIdescSG = idesc_f16(0, 0, 0, kStep, H);
+constexpr uint32_t kIdescOG = idesc_f16(0, /*A MN-major*/ 1, 0, H, 128);
+
+struct __align__(16) CtlG {
+  uint64_t rows_full[2], slot_free[2], s_full[2], p_full[2], q_raw, q_ready, q_free, o_free, done;
+  uint32_t tmem_base;
+  volatile uint32_t abort;
+  float fac[H], inv_l[H];
+  // per key of a slot: log2(e) / sqrt(512) x scale, log2(scale) (-inf: no key), 1 / scale
+  __align__(16) float rs[2][kStep];
+  __align__(16) float lg[2][kStep];
+  __align__(16) float inv[2][kStep];
+};
+
+constexpr size_t kSmemG = 1024 + (size_t)2 * kSlotG + H * D * 2 + 2 * kBlockG + sizeof(CtlG);
+static_assert(kSmemG <= 232448, "gathered attention exceeds the shared-memory limit");
+
+__device__ __forceinline__ void wait_g(CtlG &S, uint64_t *bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity) || S.abort) return;
+  if (!mbar_wait(bar, parity)) S.abort = 1;
+}
+
+// A token's keys: window rows at ring places place, place + 1, .. (around the
+// ring's end), named extra rows, list.  By whole warps.
+struct Keys {
+  int64_t gp;
+  int64_t ring_row0, extra_row0, entry_row0;   // first rows of the token's sequence
+  int64_t place;
+  uint64_t extra;
+  int rows, named, steps;   // window rows, extra rows; steps of 64 keys (0: no token)
+};
+
+__device__ __forceinline__ Keys keys_of(const AttnArgs &a, int64_t gp) {
+  Keys k;
+  k.gp = gp;
+  k.steps = 0;
+  StepToken t;
+  if (!step_token(a.step, gp, t)) return k;
+  const int64_t first = max(t.end - t.left, (int64_t)0);
+  k.rows = (int)(t.end - first);
+  k.place = first % a.step.ring;
+  k.extra = t.extra;
+  k.named = __popcll(t.extra);
+  k.ring_row0 = t.seq * a.step.ring;
+  k.extra_row0 = t.seq * a.step.extras;
+  k.entry_row0 = t.seq * a.cap;
+  const int n = k.rows + k.named + a.K;
+  k.steps = n > kStep ? (n + kStep - 1) / kStep : 1;
+  return k;
+}
+
+// The place of set bit n of m.
+__device__ __forceinline__ int nth_bit(uint64_t m, int n) {
+  int at = 0;
+#pragma unroll
+  for (int w = 32; w > 0; w >>= 1) {
+    const int c = __popcll(m & low_bits(w));
+    if (n >= c) {
+      n -= c;
+      at += w;
+      m >>= w;
+    }
+  }
+  return at;
+}
+
+// ------------------------------------------------------------------- rows
+// Eight lanes of a key take 32 channels each of its lower and of its upper half.
+struct KeyData {
+  uint4 v[2][2];      // [half][16 bytes]: an entry's codes in [half][0]
+  uint32_t sc[2];     // [half]: an entry's two scales
+  float scale;
+  int kind;           // 0 none, 1 entry, 2 row of codes
+};
+
+__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) { return hmul2_u32(a, b); }
+
+// Chunks i = 0 .. 3 of 8 channels at `at` ^ 16 i; a lane's order starts at chunk o
+// (the eight lanes of a key then cover the eight bank groups).
+__device__ __forceinline__ void put_entry(uint32_t at, const uint4 &v, uint32_t sc, bool o1, bool o2) {
+  const uint32_t e = e4m3x2_to_half2((uint16_t)sc);
+  const uint32_t s0 = __byte_perm(e, 0, o2 ? 0x3232 : 0x1010), s1 = __byte_perm(e, 0, o2 ? 0x1010 : 0x3232);
+  const uint32_t x = o1 ? v.y : v.x, y = o1 ? v.x : v.y, z = o1 ? v.w : v.z, u = o1 ? v.z : v.w;
+  const uint32_t w[4] = {o2 ? z : x, o2 ? u : y, o2 ? x : z, o2 ? y : u};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[4];
+    e2m1x8_to_half2x4(w[i], h);
+    const uint32_t s = i < 2 ? s0 : s1;
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (uint32_t)(i << 4)), "r"(half2_mul(h[0], s)),
+                 "r"(half2_mul(h[1], s)), "r"(half2_mul(h[2], s)), "r"(half2_mul(h[3], s))
+                 : "memory");
+  }
+}
+
+__device__ __forceinline__ void put_codes(uint32_t at, const uint4 &lo, const uint4 &hi, uint32_t keep, bool o1, bool o2) {
+  const uint2 c[4] = {{lo.x, lo.y}, {lo.z, lo.w}, {hi.x, hi.y}, {hi.z, hi.w}};
+  const uint2 d[4] = {o1 ? c[1] : c[0], o1 ? c[0] : c[1], o1 ? c[3] : c[2], o1 ? c[2] : c[3]};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint2 w = o2 ? d[i ^ 2] : d[i];
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (uint32_t)(i << 4)),
+                 "r"(half2_mul(e4m3x2_to_half2((uint16_t)w.x), keep)), "r"(half2_mul(e4m3x2_to_half2((uint16_t)(w.x >> 16)), keep)),
+                 "r"(half2_mul(e4m3x2_to_half2((uint16_t)w.y), keep)), "r"(half2_mul(e4m3x2_to_half2((uint16_t)(w.y >> 16)), keep))
+                 : "memory");
+  }
+}
+
+__device__ __forceinline__ void put_zeros(uint32_t at) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at ^ (uint32_t)(i << 4)), "r"(0) : "memory");
+}
+
+// List place of key e, or -1 (past the list, a window or extra row).
+__device__ __forceinline__ int32_t list_id(const AttnArgs &a, const Keys &k, int e) {
+  const int j = e - k.rows - k.named;
+  return k.steps && j >= 0 && j < a.K ? __ldg(a.idx + k.gp * a.K + j) : -1;
+}
+
+__device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e, int32_t id, int c8, KeyData &d) {
+  d.kind = 0;
+  d.scale = 1.0f;
+  if (e >= k.rows + k.named) {
+    if (id < 0) return;
+    if (id >= a.cap) {
+      set_error(CSA2_DEV_ERR_INDEX);
+      return;
+    }
+    const uint8_t *p = a.kv + (k.entry_row0 + id) * ENTRY_BYTES;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      d.v[h][0] = ld_nc_v4(p + 128 * h + 16 * c8);
+      d.sc[h] = ld_nc_u16(p + 256 + 16 * h + 2 * c8);
+    }
+    d.kind = 1;
+    return;
+  }
+  const uint8_t *p;
+  const float *s;
+  if (e < k.rows) {
+    const int64_t at = k.place + e, row = k.ring_row0 + (at >= a.step.ring ? at - a.step.ring : at);
+    p = a.swa + row * D;
+    s = a.swa_scale + row;
+  } else {
+    const int64_t row = k.extra_row0 + nth_bit(k.extra, e - k.rows);
+    p = a.step.extra + row * D;
+    s = a.step.extra_scale + row;
+  }
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int u = 0; u < 2; ++u) d.v[h][u] = ld_nc_v4(p + 256 * h + 32 * c8 + 16 * u);
+  d.scale = __uint_as_float(ld_nc_u32(s));
+  d.kind = 2;
+}
+
+// Q in place from bf16 to fp16.
+__device__ __forceinline__ void convert_q(uint8_t *qs, int t) {
+  uint4 *q = reinterpret_cast<uint4 *>(qs);
+#pragma unroll 4
+  for (int i = t; i < H * D * 2 / 16; i += kRowG * 32) {
+    const uint4 v = q[i];
+    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __half2 f = __floats2half2_rn(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
+      h[j] = *reinterpret_cast<const uint32_t *>(&f);
+    }
+    q[i] = make_uint4(h[0], h[1], h[2], h[3]);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Warp w holds keys 8 w + 4 j + lane / 8 of a step (j = 0, 1).
+__device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t *qs, int w, int lane) {
+  const int c8 = lane & 7, key0 = 8 * w + (lane >> 3), o = c8 >> 1;
+  const bool o1 = o & 1, o2 = o & 2;
+  int64_t token = blockIdx.x;
+  // the step in registers (its token's keys k), the one after it (kn, list places idn)
+  Keys k, kn;
+  int s = 0, sn = 0;
+  int64_t tn = token;
+  KeyData d[2];
+  int32_t idn[2];
+  // the next token with steps from `tn` on
+  auto seek = [&]() {
+    kn.steps = 0;
+    for (; tn < a.problems; tn += gridDim.x) {
+      kn = keys_of(a, tn);
+      if (kn.steps) break;
+    }
+  };
+  auto ids = [&]() {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) idn[j] = list_id(a, kn, sn * kStep + key0 + 4 * j);
+  };
+  auto load = [&]() {   // the next step becomes the one in registers
+    k = kn;
+    s = sn;
+    if (!k.steps) return;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) load_key(a, k, s * kStep + key0 + 4 * j, idn[j], c8, d[j]);
+    if (++sn == kn.steps) {
+      sn = 0;
+      tn += gridDim.x;
+      seek();
+    }
+    ids();
+  };
+  seek();
+  ids();
+  load();
+  uint32_t n = 0;
+  for (uint32_t g = 0; k.steps; ++g) {
+    const uint32_t b = g & 1;
+    const bool first = s == 0;
+    if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int key = key0 + 4 * j;
+      const float f = d[j].scale < kTinyScaleG ? kTinyScaleG : d[j].scale;
+      if (c8 == 0) {
+        S.rs[b][key] = kLogitG * f;
+        S.lg[b][key] = d[j].kind ? log2f(f) : -INFINITY;
+        S.inv[b][key] = d[j].kind ? 1.0f / f : 1.0f;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = smem_u32(slots) + b * kSlotG + (4 * h + o) * kBlockG + key * 128 +
+                            (((4 * (c8 & 1)) ^ o ^ (key & 7)) << 4);
+        if (d[j].kind == 1)
+          put_entry(at, d[j].v[h][0], d[j].sc[h], o1, o2);
+        else if (d[j].kind == 2)
+          put_codes(at, d[j].v[h][0], d[j].v[h][1], d[j].scale < kTinyScaleG ? 0u : 0x3C003C00u, o1, o2);
+        else
+          put_zeros(at);
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&S.rows_full[b]);
+    load();
+    if (first) {   // the token's Q, which lands about now
+      wait_g(S, &S.q_raw, n & 1);
+      ++n;
+      convert_q(qs, w * 32 + lane);
+      if (lane == 0) mbar_arrive(&S.q_ready);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- softmax
+__device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_t tmem, int w, int lane) {
+  const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
+  const int th = lane >> 4, h = 16 * w + (lane & 15), tid = w * 32 + lane;
+  uint32_t g = 0;
+  for (int64_t token = blockIdx.x; token < a.problems; token += gridDim.x) {
+    const Keys k = keys_of(a, token);
+    float m = -INFINITY, l = 0.0f;
+#pragma unroll 1
+    for (int s = 0; s < k.steps; ++s, ++g) {
+      const uint32_t b = g & 1, ph = (g >> 1) & 1;
+      wait_g(S, &S.rows_full[b], ph);   // the keys' scales
+      wait_g(S, &S.s_full[b], ph);
+      tc_fence_after();
+      float x[2][16];
+      float mx = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint32_t u0[16], u1[16];
+        tmem_ld16x2(lanes + b * 128 + 32 * i, u0);
+        tmem_ld16x2(lanes + b * 128 + 64 + 32 * i, u1);
+        tmem_ld_wait();
+        const float4 *r4 = reinterpret_cast<const float4 *>(&S.rs[b][32 * i + 16 * th]);
+        const float4 *g4 = reinterpret_cast<const float4 *>(&S.lg[b][32 * i + 16 * th]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 r = r4[q], e = g4[q];
+          x[i][4 * q] = fmaf(__uint_as_float(u0[4 * q]) + __uint_as_float(u1[4 * q]), r.x, e.x);
+          x[i][4 * q + 1] = fmaf(__uint_as_float(u0[4 * q + 1]) + __uint_as_float(u1[4 * q + 1]), r.y, e.y);
+          x[i][4 * q + 2] = fmaf(__uint_as_float(u0[4 * q + 2]) + __uint_as_float(u1[4 * q + 2]), r.z, e.z);
+          x[i][4 * q + 3] = fmaf(__uint_as_float(u0[4 * q + 3]) + __uint_as_float(u1[4 * q + 3]), r.w, e.w);
+        }
+#pragma unroll
+        for (int q = 0; q < 16; ++q) mx = fmaxf(mx, x[i][q]);
+      }
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+      // a head that saw no key so far has nothing in O^T: its reference is set, not raised
+      const bool raise = mx > m + kLazyG, over = raise && m != -INFINITY;
+      if (bar_named_or(1, kSoftG * 32, over)) {
+        const float f = over ? ex2_approx(m - mx) : 1.0f;
+        if (th == 0) S.fac[h] = f;
+        l *= f;
+        bar_named(1, kSoftG * 32);
+        wait_g(S, &S.slot_free[(g - 1) & 1], ((g - 1) >> 1) & 1);   // the products so far
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < 256; c += 32) {
+          uint32_t v[32];
+          tmem_ld32(lanes + kColOG + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = __float_as_uint(__uint_as_float(v[q]) * S.fac[(c & 63) + q]);
+          tmem_st32(lanes + kColOG + c, v);
+        }
+        tmem_st_wait();
+        bar_named(1, kSoftG * 32);   // fac may be written again
+      }
+      if (raise) m = mx;
+      const float ms = m == -INFINITY ? 0.0f : m;
+      // P of two steps ago has been read
+      if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
+      uint8_t *prow = ps + b * kBlockG + h * 128;
+      float l2 = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float4 *v4 = reinterpret_cast<const float4 *>(&S.inv[b][32 * i + 16 * th]);
+        uint32_t pk[8];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const float4 v = v4[q];
+          const float p0 = ex2_approx(x[i][4 * q] - ms), p1 = ex2_approx(x[i][4 * q + 1] - ms),
+                      p2 = ex2_approx(x[i][4 * q + 2] - ms), p3 = ex2_approx(x[i][4 * q + 3] - ms);
+          l = fmaf(p0, v.x, fmaf(p1, v.y, l));
+          l2 = fmaf(p2, v.z, fmaf(p3, v.w, l2));
+          const __half2 a2 = __floats2half2_rn(p0, p1), b2 = __floats2half2_rn(p2, p3);
+          pk[2 * q] = *reinterpret_cast<const uint32_t *>(&a2);
+          pk[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&b2);
+        }
+        const int c0 = 4 * i + 2 * th;
+        *reinterpret_cast<uint4 *>(prow + ((c0 ^ (h & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        *reinterpret_cast<uint4 *>(prow + (((c0 + 1) ^ (h & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+      }
+      l += l2;
+      fence_proxy_async_smem();
+      tc_fence_before();
+      mbar_arrive(&S.p_full[b]);
+    }
+    if (!k.steps) continue;
+    // ---------------------------------------------------------- token's end
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    if (th == 0) {
+      S.inv_l[h] = l > 0.0f && !S.abort ? 1.0f / l : l;   // (0 stays 0, a NaN a NaN)
+      if (a.lse) a.lse[token * H + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2G;
+    }
+    bar_named(1, kSoftG * 32);
+    wait_g(S, &S.slot_free[(g - 1) & 1], ((g - 1) >> 1) & 1);
+    tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < 256; c += 32) {
+      uint32_t v[32];
+      tmem_ld32(lanes + kColOG + c, v);
+      tmem_ld_wait();
+      if (c == 224) {   // O^T is read: the next token's products may start
+        tc_fence_before();
+        mbar_arrive(&S.o_free);
+      }
+      const int d = (c >> 6) * 128 + tid, h0 = c & 63;
+#pragma unroll
+      for (int q = 0; q < 32; q += 2)
+        put_pair(a.step.out, token * H + h0 + q, d, __uint_as_float(v[q]) * S.inv_l[h0 + q],
+                 __uint_as_float(v[q + 1]) * S.inv_l[h0 + q + 1]);
+    }
+    bar_named(1, kSoftG * 32);   // inv_l may be written again
+  }
+}
+
+// --------------------------------------------------------------- products
+__device__ __forceinline__ void load_q_g(CtlG &S, const CUtensorMap &tm_q, uint8_t *qs, int64_t token) {
+  mbar_arrive_expect_tx(&S.q_raw, (uint32_t)(H * D * 2));
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) tma_load_2d(qs + c * kBlockG, &tm_q, 64 * c, (int32_t)(token * H), &S.q_raw);
+}
+
+// (both by whole warps, an elected thread issuing)
+__device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q, uint8_t *slots, uint8_t *qs, uint32_t tmem) {
+  const uint64_t qd = smem_desc(smem_u32(qs), 16, 1024), kd = smem_desc(smem_u32(slots), 16, 1024);
+  uint32_t g = 0, n = 0, copies = 0;
+  for (int64_t token = blockIdx.x; token < a.problems; token += gridDim.x) {
+    const Keys k = keys_of(a, token);
+    if (!k.steps) continue;
+    // Q's last reader was the token before's last S
+    if (n) wait_g(S, &S.q_free, (n - 1) & 1);
+    if (!S.abort) {
+      if (elect_one()) load_q_g(S, tm_q, qs, token);
+      ++copies;
+    }
+    __syncwarp();
+    wait_g(S, &S.q_ready, n & 1);
+    ++n;
+#pragma unroll 1
+    for (int s = 0; s < k.steps; ++s, ++g) {
+      const uint32_t b = g & 1, d = tmem + b * 128;
+      wait_g(S, &S.rows_full[b], (g >> 1) & 1);
+      if (g > 1) wait_g(S, &S.p_full[b], ((g >> 1) - 1) & 1);   // S of two steps ago has been read
+      tc_fence_after();
+      if (elect_one()) {
+        uint64_t qa = qd, kb = kd + (uint64_t)(b * kSlotG >> 4);
+#pragma unroll 1
+        for (int c = 0; c < 8; c += 2) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            mma_f16(d, qa + 2 * i, kb + 2 * i, kIdescSG, (c | i) ? 1u : 0u);
+            mma_f16(d + 64, qa + (kBlockG >> 4) + 2 * i, kb + (kBlockG >> 4) + 2 * i, kIdescSG, (c | i) ? 1u : 0u);
+          }
+          qa += 2 * (kBlockG >> 4);
+          kb += 2 * (kBlockG >> 4);
+        }
+        mma_commit(&S.s_full[b]);
+        if (s == k.steps - 1) mma_commit(&S.q_free);
+      }
+      __syncwarp();
+    }
+  }
+  if (n) wait_g(S, &S.q_free, (n - 1) & 1);
+  // a copy still in flight lands before the CTA's memory goes, also after a wait ran out
+  if (copies) mbar_wait(&S.q_raw, (copies - 1) & 1);
+}
+
+__device__ void value_warp_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t *ps, uint32_t tmem) {
+  const uint64_t vd = smem_desc(smem_u32(slots), kBlockG, 1024), pd = smem_desc(smem_u32(ps), 16, 1024);
+  uint32_t g = 0, n = 0;
+  for (int64_t token = blockIdx.x; token < a.problems; token += gridDim.x) {
+    const Keys k = keys_of(a, token);
+    if (!k.steps) continue;
+    if (n) wait_g(S, &S.o_free, (n - 1) & 1);
+    ++n;
+#pragma unroll 1
+    for (int s = 0; s < k.steps; ++s, ++g) {
+      const uint32_t b = g & 1;
+      wait_g(S, &S.p_full[b], (g >> 1) & 1);
+      tc_fence_after();
+      if (elect_one()) {
+        uint64_t va = vd + (uint64_t)(b * kSlotG >> 4), pb = pd + (uint64_t)(b * kBlockG >> 4);
+#pragma unroll 1
+        for (int i = 0; i < kStep / 16; ++i) {   // 16 keys; the accumulators in turn
+          const uint32_t acc = (s | i) ? 1u : 0u;
+#pragma unroll
+          for (int t = 0; t < 4; ++t) mma_f16(tmem + kColOG + 64 * t, va + (uint64_t)(2 * t * kBlockG >> 4), pb, kIdescOG, acc);
+          va += 128;
+          pb += 2;
+        }
+        mma_commit(&S.slot_free[b]);
+      }
+      __syncwarp();
+    }
+  }
+  // every product has completed before the teardown, also after a wait ran out
+  if (elect_one()) mma_commit(&S.done);
+  __syncwarp();
+  mbar_wait(&S.done, 0);
+}
+
+__global__ void __launch_bounds__(kThreadsG, 1)
+    gather_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttnArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *slots = base, *qs = slots + 2 * kSlotG, *ps = qs + H * D * 2;
+  CtlG &S = *reinterpret_cast<CtlG *>(ps + 2 * kBlockG);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&S.rows_full[i], kRowG);
+      mbar_init(&S.slot_free[i], 1);
+      mbar_init(&S.s_full[i], 1);
+      mbar_init(&S.p_full[i], kSoftG * 32);
+    }
+    mbar_init(&S.q_raw, 1);
+    mbar_init(&S.q_ready, kRowG);
+    mbar_init(&S.q_free, 1);
+    mbar_init(&S.o_free, kSoftG * 32);
+    mbar_init(&S.done, 1);
+    S.abort = 0;
+    fence_barrier_init();
+    prefetch_tmap(&tm_q);
+  }
+  pdl_enter();
+  if (warp == kValueWarpG) {
+    tmem_alloc(&S.tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem_base;
+  if (warp < kSoftG)
+    softmax_warps_g(a, S, ps, tmem, warp, lane);
+  else if (warp < kScoreWarpG)
+    row_warps_g(a, S, slots, qs, warp - kSoftG, lane);
+  else if (warp == kScoreWarpG)
+    score_warp_g(a, S, tm_q, slots, qs, tmem);
+  else
+    value_warp_g(a, S, slots, ps, tmem);
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kValueWarpG) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_gather_attn(const AttnArgs &a, int num_sms, cudaStream_t stream, int *launches) {
+  CUtensorMap tm_q;
+  if (!make_tmap_bf16(&tm_q, a.q, D, (int64_t)a.problems * H, H)) return cudaErrorInvalidValue;
+  cudaError_t e = cudaFuncSetAttribute(gather_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemG);
+  if (e != cudaSuccess) return e;
+  const int grid = a.problems < num_sms ? a.problems : num_sms;
+  e = launch_pdl(gather_attn_kernel, dim3((unsigned)grid), dim3(kThreadsG), kSmemG, stream, 0u, tm_q, a);
+  if (e == cudaSuccess) ++*launches;
+  return e;
+}
+
+}  // namespace csa2

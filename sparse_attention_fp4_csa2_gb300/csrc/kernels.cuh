@@ -274,6 +274,9 @@ bool window_rows_fit(const StepRows &s);
 cudaError_t launch_window_attn(const void *q, const uint8_t *swa, const float *swa_scale, const StepRows &s, int64_t tokens,
                                float *lse, int num_sms, cudaStream_t stream, int *launches);
 
+// The step form, one CTA per token: many tokens, or rows that fit in no tile.
+cudaError_t launch_gather_attn(const AttnArgs &a, int num_sms, cudaStream_t stream, int *launches);
+
 // Sliding-window rows as FP8 (pos NULL: no RoPE) and the caches' read-backs
 // (idx NULL: rows 0 .. k - 1 of each sequence).
 cudaError_t launch_swa_quant_write(const void *latent, int64_t n, const int64_t *pos, const int64_t *slot, uint8_t *swa,

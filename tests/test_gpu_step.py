@@ -250,6 +250,9 @@ WINDOWS = [
     dict(ctx=[0, 0, 0], new=[0, 0, 3], W=128, S=4), dict(ctx=[2 ** 31 - 200], new=[150], W=128, S=4),
     dict(ctx=[20 * i for i in range(150)], new=[3 if i % 7 else 0 for i in range(150)], W=128, S=4, spare=1),
     dict(ctx=[17, 400, 0, 88, 1000], new=[401, 1, 256, 2, 33], W=128, S=15), dict(ctx=[17, 400], new=[33, 260], W=128, S=16),
+    dict(ctx=[9, 0], new=[60, 40], W=0, S=6), dict(ctx=[9], new=[100], W=0, S=0), dict(ctx=[0, 700], new=[80, 81], W=128, S=13),
+    dict(ctx=[31 * i for i in range(320)], new=[1] * 320, W=128, S=4), dict(ctx=[31 * i for i in range(200)], new=[2 - i % 2 for i in range(200)], W=16, S=1),
+    dict(ctx=[100, 5], new=[90, 77], W=1024, S=3),
 ]
 
 
@@ -396,6 +399,9 @@ TREES = [
     dict(B=2, T=64, K=0, W=128, ctx=[500, 64]), dict(B=2, T=9, K=0, W=0, ctx=[500, 64]), dict(B=2, T=9, K=1, W=0, cap=1, ctx=[0, 64]),
     dict(B=2, T=31, K=0, W=3, ctx=[500, 1]), dict(B=1, T=6, K=2048, W=1024, cap=2100, ctx=[5000]),
     dict(B=40, T=8, K=64, W=128, cap=100, ctx=[31 * i for i in range(40)]), dict(B=64, T=5, K=0, W=128, ctx=[31 * i for i in range(64)]),
+    dict(B=20, T=9, K=0, W=0, ctx=[7 * i for i in range(20)]), dict(B=10, T=16, K=0, W=128, ctx=[40 * i for i in range(10)]),
+    dict(B=30, T=8, K=0, W=3, ctx=[i for i in range(30)]), dict(B=90, T=1, K=0, W=128, ctx=[3 * i for i in range(90)]),
+    dict(B=170, T=2, K=1, W=7, cap=3, ctx=[i for i in range(170)]), dict(B=3, T=64, K=130, W=128, cap=200, ctx=[0, 1, 5000]),
     dict(B=5, T=33, K=200, W=37, cap=201, ctx=[2 ** 31 - 1, 0, 36, 37, 38]), dict(B=20, T=16, K=512, W=128, cap=700, ctx=[900] * 20),
 ]
 
