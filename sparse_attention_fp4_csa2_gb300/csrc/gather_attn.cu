@@ -23,10 +23,11 @@
 //            shared memory as fp16;
 //   O^T += V^T P^T  M = 128 channels (four blocks), N = 64 heads, K = 64 keys, V^T
 //            from the same slot; its end frees the slot;
-//   rows out O^T read per channel, pairs of channels stored as bf16, while the next
+//   rows out O^T through shared memory and tensor copies, as bf16, while the next
 //            token's first steps are converted and multiplied.
-// Keys that the token does not see take no place: the window's visible rows, the
-// named extra rows, then the list (whose -1 are masked).
+// Keys that the token does not see take no place: the list (whose -1 are masked),
+// the window's visible rows, then the named extra rows.  (The list first: entries
+// have scale 1, so the first step sets a reference that rows rarely raise.)
 //
 // Warps: 0-3 softmax, 4-11 rows, 12 S, 13 second product.  Every wait is bounded;
 // after one runs out every role falls through its waits and the output is
@@ -37,9 +38,9 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kSoftG = 4, kRowG = 8;
+constexpr int kSoftG = 4, kRowG = 8, kRowKeys = 64 / kRowG / 4;   // keys of a lane
 constexpr int kScoreWarpG = kSoftG + kRowG, kValueWarpG = kScoreWarpG + 1;
-constexpr int kThreadsG = (kValueWarpG + 1) * 32;   // 144 registers a thread
+constexpr int kThreadsG = (kValueWarpG + 1) * 32;   // 128 registers a thread
 constexpr int kStep = 64;                    // keys of a step
 constexpr int kSlotG = kStep * D * 2;
 constexpr int kBlockG = kStep * 128;         // a column block of 64 channels: of a slot, of Q, a buffer of P
@@ -55,7 +56,8 @@ struct __align__(16) CtlG {
   uint64_t rows_full[2], slot_free[2], s_full[2], p_full[2], q_raw, q_ready, q_free, o_free, done;
   uint32_t tmem_base;
   volatile uint32_t abort;
-  float fac[H], inv_l[H];
+  float fac[H];
+  __align__(16) float inv_l[H];
   // per key of a slot: log2(e) / sqrt(512) x scale, log2(scale) (-inf: no key), 1 / scale
   __align__(16) float rs[2][kStep];
   __align__(16) float lg[2][kStep];
@@ -70,8 +72,8 @@ __device__ __forceinline__ void wait_g(CtlG &S, uint64_t *bar, uint32_t parity) 
   if (!mbar_wait(bar, parity)) S.abort = 1;
 }
 
-// A token's keys: window rows at ring places place, place + 1, .. (around the
-// ring's end), named extra rows, list.  By whole warps.
+// A token's keys: its list, window rows at ring places place, place + 1, .. (around
+// the ring's end), named extra rows.  By whole warps.
 struct Keys {
   int64_t gp;
   int64_t ring_row0, extra_row0, entry_row0;   // first rows of the token's sequence
@@ -162,16 +164,15 @@ __device__ __forceinline__ void put_zeros(uint32_t at) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at ^ (uint32_t)(i << 4)), "r"(0) : "memory");
 }
 
-// List place of key e, or -1 (past the list, a window or extra row).
+// List place of key e, or -1 (past the list).
 __device__ __forceinline__ int32_t list_id(const AttnArgs &a, const Keys &k, int e) {
-  const int j = e - k.rows - k.named;
-  return k.steps && j >= 0 && j < a.K ? __ldg(a.idx + k.gp * a.K + j) : -1;
+  return k.steps && e < a.K ? __ldg(a.idx + k.gp * a.K + e) : -1;
 }
 
 __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e, int32_t id, int c8, KeyData &d) {
   d.kind = 0;
   d.scale = 1.0f;
-  if (e >= k.rows + k.named) {
+  if (e < a.K) {
     if (id < 0) return;
     if (id >= a.cap) {
       set_error(CSA2_DEV_ERR_INDEX);
@@ -188,6 +189,8 @@ __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e
   }
   const uint8_t *p;
   const float *s;
+  e -= a.K;
+  if (e >= k.rows + k.named) return;
   if (e < k.rows) {
     const int64_t at = k.place + e, row = k.ring_row0 + (at >= a.step.ring ? at - a.step.ring : at);
     p = a.swa + row * D;
@@ -224,17 +227,17 @@ __device__ __forceinline__ void convert_q(uint8_t *qs, int t) {
   __syncwarp();
 }
 
-// Warp w holds keys 8 w + 4 j + lane / 8 of a step (j = 0, 1).
+// Eight lanes a key, kRowKeys keys of a step for each lane.
 __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t *qs, int w, int lane) {
-  const int c8 = lane & 7, key0 = 8 * w + (lane >> 3), o = c8 >> 1;
+  const int c8 = lane & 7, key0 = 4 * kRowKeys * w + (lane >> 3), o = c8 >> 1;
   const bool o1 = o & 1, o2 = o & 2;
   int64_t token = blockIdx.x;
   // the step in registers (its token's keys k), the one after it (kn, list places idn)
   Keys k, kn;
   int s = 0, sn = 0;
   int64_t tn = token;
-  KeyData d[2];
-  int32_t idn[2];
+  KeyData d[kRowKeys];
+  int32_t idn[kRowKeys];
   // the next token with steps from `tn` on
   auto seek = [&]() {
     kn.steps = 0;
@@ -245,14 +248,14 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
   };
   auto ids = [&]() {
 #pragma unroll
-    for (int j = 0; j < 2; ++j) idn[j] = list_id(a, kn, sn * kStep + key0 + 4 * j);
+    for (int j = 0; j < kRowKeys; ++j) idn[j] = list_id(a, kn, sn * kStep + key0 + 4 * j);
   };
   auto load = [&]() {   // the next step becomes the one in registers
     k = kn;
     s = sn;
     if (!k.steps) return;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) load_key(a, k, s * kStep + key0 + 4 * j, idn[j], c8, d[j]);
+    for (int j = 0; j < kRowKeys; ++j) load_key(a, k, s * kStep + key0 + 4 * j, idn[j], c8, d[j]);
     if (++sn == kn.steps) {
       sn = 0;
       tn += gridDim.x;
@@ -269,7 +272,7 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
     const bool first = s == 0;
     if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    for (int j = 0; j < kRowKeys; ++j) {
       const int key = key0 + 4 * j;
       const float f = d[j].scale < kTinyScaleG ? kTinyScaleG : d[j].scale;
       if (c8 == 0) {
@@ -303,9 +306,9 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
 }
 
 // ---------------------------------------------------------------- softmax
-__device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_t tmem, int w, int lane) {
+__device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_out, uint8_t *ps, uint32_t tmem, int w, int lane) {
   const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-  const int th = lane >> 4, h = 16 * w + (lane & 15), tid = w * 32 + lane;
+  const int th = lane >> 4, h = 16 * w + (lane & 15);
   uint32_t g = 0;
   for (int64_t token = blockIdx.x; token < a.problems; token += gridDim.x) {
     const Keys k = keys_of(a, token);
@@ -338,10 +341,12 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_
         for (int q = 0; q < 16; ++q) mx = fmaxf(mx, x[i][q]);
       }
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-      // a head that saw no key so far has nothing in O^T: its reference is set, not raised
-      const bool raise = mx > m + kLazyG, over = raise && m != -INFINITY;
-      if (bar_named_or(1, kSoftG * 32, over)) {
-        const float f = over ? ex2_approx(m - mx) : 1.0f;
+      // a head that saw no key so far has nothing in O^T: its reference is set, not
+      // raised; once one is raised, all are that can be
+      if (m == -INFINITY) m = mx;
+      if (bar_named_or(1, kSoftG * 32, mx > m + kLazyG)) {
+        const float f = mx > m ? ex2_approx(m - mx) : 1.0f;
+        m = fmaxf(m, mx);
         if (th == 0) S.fac[h] = f;
         l *= f;
         bar_named(1, kSoftG * 32);
@@ -359,7 +364,6 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_
         tmem_st_wait();
         bar_named(1, kSoftG * 32);   // fac may be written again
       }
-      if (raise) m = mx;
       const float ms = m == -INFINITY ? 0.0f : m;
       // P of two steps ago has been read
       if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
@@ -399,6 +403,9 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_
     bar_named(1, kSoftG * 32);
     wait_g(S, &S.slot_free[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
+    // 32 heads x 32 channels at a time (a lane's channel, pairs of heads exchanged
+    // between neighbouring lanes) through the P buffers, which the last products
+    // have read, and tensor copies: stores from the registers took 11,000 clocks
 #pragma unroll 1
     for (int c = 0; c < 256; c += 32) {
       uint32_t v[32];
@@ -408,14 +415,31 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_
         tc_fence_before();
         mbar_arrive(&S.o_free);
       }
-      const int d = (c >> 6) * 128 + tid, h0 = c & 63;
+      uint8_t *stage = ps + w * 4096 + (c & 32) * 64;
+      if (lane == 0) bulk_wait_read<1>();   // the copy out of it two chunks ago
+      __syncwarp();
+      const float4 *il = reinterpret_cast<const float4 *>(S.inv_l + (c & 32));
+      uint8_t *dst = stage + (lane & 1) * 64 + (lane & 6) * 2;
 #pragma unroll
-      for (int q = 0; q < 32; q += 2)
-        put_pair(a.step.out, token * H + h0 + q, d, __uint_as_float(v[q]) * S.inv_l[h0 + q],
-                 __uint_as_float(v[q + 1]) * S.inv_l[h0 + q + 1]);
+      for (int q = 0; q < 32; q += 4) {
+        const float4 f = il[q >> 2];
+        *reinterpret_cast<uint32_t *>(dst + q * 64 + (((lane >> 3) ^ ((q >> 1) & 3)) << 4)) =
+            lane_pair(lane & 1, __uint_as_float(v[q]) * f.x, __uint_as_float(v[q + 1]) * f.y);
+        *reinterpret_cast<uint32_t *>(dst + (q + 2) * 64 + (((lane >> 3) ^ (((q + 2) >> 1) & 3)) << 4)) =
+            lane_pair(lane & 1, __uint_as_float(v[q + 2]) * f.z, __uint_as_float(v[q + 3]) * f.w);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(&tm_out, (c >> 6) * 128 + 32 * w, (int32_t)(token * H + (c & 32)), stage);
+        bulk_commit();
+      }
     }
-    bar_named(1, kSoftG * 32);   // inv_l may be written again
+    if (lane == 0) bulk_wait_read<0>();   // P may be written again
+    __syncwarp();
+    bar_named(1, kSoftG * 32);   // inv_l and the other warps' stages may be written again
   }
+  if (lane == 0) bulk_wait<0>();
 }
 
 // --------------------------------------------------------------- products
@@ -505,7 +529,8 @@ __device__ void value_warp_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t
 }
 
 __global__ void __launch_bounds__(kThreadsG, 1)
-    gather_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttnArgs a) {
+    gather_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_out,
+                       const __grid_constant__ AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *slots = base, *qs = slots + 2 * kSlotG, *ps = qs + H * D * 2;
@@ -526,6 +551,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     S.abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_out);
   }
   pdl_enter();
   if (warp == kValueWarpG) {
@@ -537,7 +563,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   if (warp < kSoftG)
-    softmax_warps_g(a, S, ps, tmem, warp, lane);
+    softmax_warps_g(a, S, tm_out, ps, tmem, warp, lane);
   else if (warp < kScoreWarpG)
     row_warps_g(a, S, slots, qs, warp - kSoftG, lane);
   else if (warp == kScoreWarpG)
@@ -556,12 +582,14 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 }  // namespace
 
 cudaError_t launch_gather_attn(const AttnArgs &a, int num_sms, cudaStream_t stream, int *launches) {
-  CUtensorMap tm_q;
-  if (!make_tmap_bf16(&tm_q, a.q, D, (int64_t)a.problems * H, H)) return cudaErrorInvalidValue;
+  CUtensorMap tm_q, tm_out;
+  if (!make_tmap_bf16(&tm_q, a.q, D, (int64_t)a.problems * H, H) ||
+      !make_tmap_bf16_half(&tm_out, a.step.out, D, (int64_t)a.problems * H, 32))
+    return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(gather_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemG);
   if (e != cudaSuccess) return e;
   const int grid = a.problems < num_sms ? a.problems : num_sms;
-  e = launch_pdl(gather_attn_kernel, dim3((unsigned)grid), dim3(kThreadsG), kSmemG, stream, 0u, tm_q, a);
+  e = launch_pdl(gather_attn_kernel, dim3((unsigned)grid), dim3(kThreadsG), kSmemG, stream, 0u, tm_q, tm_out, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }

@@ -40,14 +40,19 @@ __device__ __forceinline__ bool step_token(const StepRows &s, int64_t gp, StepTo
   return true;
 }
 
-// Channel d (a lane's; a warp's 32 are consecutive) of rows `row` and row + 1 as
-// bf16: neighbouring lanes exchange, so that the even one stores two channels of
-// the first row and the odd one two of the second.
-__device__ __forceinline__ void put_pair(__nv_bfloat16 *out, int64_t row, int d, float x, float y) {
-  const bool odd = d & 1;
+// A lane holds x and y of two rows at its own column; neighbouring lanes exchange,
+// so that the even one has two columns of the first row (bf16) and the odd one two
+// of the second.
+__device__ __forceinline__ uint32_t lane_pair(bool odd, float x, float y) {
   const float other = __shfl_xor_sync(0xffffffffu, odd ? x : y, 1);
   const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(other, y) : __floats2bfloat162_rn(x, other);
-  *reinterpret_cast<__nv_bfloat162 *>(out + (row + odd) * D + (d & ~1)) = v;
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// Channel d (a lane's; a warp's 32 are consecutive) of rows `row` and row + 1.
+__device__ __forceinline__ void put_pair(__nv_bfloat16 *out, int64_t row, int d, float x, float y) {
+  const bool odd = d & 1;
+  *reinterpret_cast<uint32_t *>(out + (row + odd) * D + (d & ~1)) = lane_pair(odd, x, y);
 }
 
 }  // namespace csa2
