@@ -23,7 +23,7 @@
 //            shared memory as fp16;
 //   O^T += V^T P^T  M = 128 channels (four blocks), N = 64 heads, K = 64 keys, V^T
 //            from the same slot; its end frees the slot;
-//   rows out O^T through shared memory and tensor copies, as bf16, while the next
+//   rows out O^T through shared memory, as bf16, while the next
 //            token's first steps are converted and multiplied.
 // Keys that the token does not see take no place: the list (whose -1 are masked),
 // the window's visible rows, then the named extra rows.  (The list first: entries
@@ -306,7 +306,7 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
 }
 
 // ---------------------------------------------------------------- softmax
-__device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_out, uint8_t *ps, uint32_t tmem, int w, int lane) {
+__device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_t tmem, int w, int lane) {
   const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
   const int th = lane >> 4, h = 16 * w + (lane & 15);
   uint32_t g = 0;
@@ -369,10 +369,10 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, const CUtensorMap &t
       if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
       uint8_t *prow = ps + b * kBlockG + h * 128;
       float l2 = 0.0f;
+      uint32_t pk[2][8];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const float4 *v4 = reinterpret_cast<const float4 *>(&S.inv[b][32 * i + 16 * th]);
-        uint32_t pk[8];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const float4 v = v4[q];
@@ -381,12 +381,15 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, const CUtensorMap &t
           l = fmaf(p0, v.x, fmaf(p1, v.y, l));
           l2 = fmaf(p2, v.z, fmaf(p3, v.w, l2));
           const __half2 a2 = __floats2half2_rn(p0, p1), b2 = __floats2half2_rn(p2, p3);
-          pk[2 * q] = *reinterpret_cast<const uint32_t *>(&a2);
-          pk[2 * q + 1] = *reinterpret_cast<const uint32_t *>(&b2);
+          pk[i][2 * q] = *reinterpret_cast<const uint32_t *>(&a2);
+          pk[i][2 * q + 1] = *reinterpret_cast<const uint32_t *>(&b2);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         const int c0 = 4 * i + 2 * th;
-        *reinterpret_cast<uint4 *>(prow + ((c0 ^ (h & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-        *reinterpret_cast<uint4 *>(prow + (((c0 + 1) ^ (h & 7)) << 4)) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+        *reinterpret_cast<uint4 *>(prow + ((c0 ^ (h & 7)) << 4)) = make_uint4(pk[i][0], pk[i][1], pk[i][2], pk[i][3]);
+        *reinterpret_cast<uint4 *>(prow + (((c0 + 1) ^ (h & 7)) << 4)) = make_uint4(pk[i][4], pk[i][5], pk[i][6], pk[i][7]);
       }
       l += l2;
       fence_proxy_async_smem();
@@ -405,7 +408,8 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, const CUtensorMap &t
     tc_fence_after();
     // 32 heads x 32 channels at a time (a lane's channel, pairs of heads exchanged
     // between neighbouring lanes) through the P buffers, which the last products
-    // have read, and tensor copies: stores from the registers took 11,000 clocks
+    // have read, for stores of 64 bytes a row (tensor copies wait behind the copies
+    // of the next Q: 11,000 clocks, as many as 4-byte stores from the registers)
 #pragma unroll 1
     for (int c = 0; c < 256; c += 32) {
       uint32_t v[32];
@@ -415,31 +419,32 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, const CUtensorMap &t
         tc_fence_before();
         mbar_arrive(&S.o_free);
       }
-      uint8_t *stage = ps + w * 4096 + (c & 32) * 64;
-      if (lane == 0) bulk_wait_read<1>();   // the copy out of it two chunks ago
-      __syncwarp();
+      uint8_t *stage = ps + w * 4096 + (c & 32) * 64;   // (two in turn: one barrier a chunk)
       const float4 *il = reinterpret_cast<const float4 *>(S.inv_l + (c & 32));
       uint8_t *dst = stage + (lane & 1) * 64 + (lane & 6) * 2;
+      uint32_t o[16];   // (all of them before the first store, which may not pass the loads of inv_l)
 #pragma unroll
-      for (int q = 0; q < 32; q += 4) {
-        const float4 f = il[q >> 2];
-        *reinterpret_cast<uint32_t *>(dst + q * 64 + (((lane >> 3) ^ ((q >> 1) & 3)) << 4)) =
-            lane_pair(lane & 1, __uint_as_float(v[q]) * f.x, __uint_as_float(v[q + 1]) * f.y);
-        *reinterpret_cast<uint32_t *>(dst + (q + 2) * 64 + (((lane >> 3) ^ (((q + 2) >> 1) & 3)) << 4)) =
-            lane_pair(lane & 1, __uint_as_float(v[q + 2]) * f.z, __uint_as_float(v[q + 3]) * f.w);
+      for (int q = 0; q < 8; ++q) {
+        const float4 f = il[q];
+        o[2 * q] = lane_pair(lane & 1, __uint_as_float(v[4 * q]) * f.x, __uint_as_float(v[4 * q + 1]) * f.y);
+        o[2 * q + 1] = lane_pair(lane & 1, __uint_as_float(v[4 * q + 2]) * f.z, __uint_as_float(v[4 * q + 3]) * f.w);
       }
-      fence_proxy_async_smem();
+#pragma unroll
+      for (int q = 0; q < 16; ++q)
+        *reinterpret_cast<uint32_t *>(dst + 2 * q * 64 + (((lane >> 3) ^ (q & 3)) << 4)) = o[q];
       __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(&tm_out, (c >> 6) * 128 + 32 * w, (int32_t)(token * H + (c & 32)), stage);
-        bulk_commit();
+      __nv_bfloat16 *out = a.step.out + (token * H + (c & 32)) * D + (c >> 6) * 128 + 32 * w + 8 * (lane & 3);
+      uint4 u[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 8 * q + (lane >> 2);
+        u[q] = *reinterpret_cast<const uint4 *>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
       }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(out + (8 * q + (lane >> 2)) * D) = u[q];
     }
-    if (lane == 0) bulk_wait_read<0>();   // P may be written again
-    __syncwarp();
     bar_named(1, kSoftG * 32);   // inv_l and the other warps' stages may be written again
   }
-  if (lane == 0) bulk_wait<0>();
 }
 
 // --------------------------------------------------------------- products
@@ -529,8 +534,7 @@ __device__ void value_warp_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t
 }
 
 __global__ void __launch_bounds__(kThreadsG, 1)
-    gather_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_out,
-                       const __grid_constant__ AttnArgs a) {
+    gather_attn_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ AttnArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t *slots = base, *qs = slots + 2 * kSlotG, *ps = qs + H * D * 2;
@@ -551,7 +555,6 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     S.abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_q);
-    prefetch_tmap(&tm_out);
   }
   pdl_enter();
   if (warp == kValueWarpG) {
@@ -563,7 +566,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   if (warp < kSoftG)
-    softmax_warps_g(a, S, tm_out, ps, tmem, warp, lane);
+    softmax_warps_g(a, S, ps, tmem, warp, lane);
   else if (warp < kScoreWarpG)
     row_warps_g(a, S, slots, qs, warp - kSoftG, lane);
   else if (warp == kScoreWarpG)
@@ -582,14 +585,12 @@ __global__ void __launch_bounds__(kThreadsG, 1)
 }  // namespace
 
 cudaError_t launch_gather_attn(const AttnArgs &a, int num_sms, cudaStream_t stream, int *launches) {
-  CUtensorMap tm_q, tm_out;
-  if (!make_tmap_bf16(&tm_q, a.q, D, (int64_t)a.problems * H, H) ||
-      !make_tmap_bf16_half(&tm_out, a.step.out, D, (int64_t)a.problems * H, 32))
-    return cudaErrorInvalidValue;
+  CUtensorMap tm_q;
+  if (!make_tmap_bf16(&tm_q, a.q, D, (int64_t)a.problems * H, H)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(gather_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemG);
   if (e != cudaSuccess) return e;
   const int grid = a.problems < num_sms ? a.problems : num_sms;
-  e = launch_pdl(gather_attn_kernel, dim3((unsigned)grid), dim3(kThreadsG), kSmemG, stream, 0u, tm_q, tm_out, a);
+  e = launch_pdl(gather_attn_kernel, dim3((unsigned)grid), dim3(kThreadsG), kSmemG, stream, 0u, tm_q, a);
   if (e == cudaSuccess) ++*launches;
   return e;
 }
