@@ -13,7 +13,7 @@
 // So the keys go through in steps of 64 in two slots of 64 KB, every part of the
 // work on warps of its own, a step's rows being converted while the step before is
 // in its softmax and products:
-//   rows     8 warps: eight lanes on 128 contiguous bytes of an entry, loaded a
+//   rows     8 warps: four lanes on 128 contiguous bytes of an entry, loaded a
 //            step ahead into registers, written as fp16 into the slot [8 x 64
 //            channels][64 keys][128 B], 128B-swizzled;
 //   S        M = 64 heads, N = 64 keys, K = 512, in two accumulators in turn
@@ -38,7 +38,7 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kSoftG = 4, kRowG = 8, kRowKeys = 64 / kRowG / 4;   // keys of a lane
+constexpr int kSoftG = 4, kRowG = 8;
 constexpr int kScoreWarpG = kSoftG + kRowG, kValueWarpG = kScoreWarpG + 1;
 constexpr int kThreadsG = (kValueWarpG + 1) * 32;   // 128 registers a thread
 constexpr int kStep = 64;                    // keys of a step
@@ -117,51 +117,46 @@ __device__ __forceinline__ int nth_bit(uint64_t m, int n) {
 }
 
 // ------------------------------------------------------------------- rows
-// Eight lanes of a key take 32 channels each of its lower and of its upper half.
+// A warp has 8 keys of a step: lane l key l % 8, of which it takes 64 channels (a
+// column block of the slot) twice, blocks l / 8 and l / 8 + 4.  Four lanes of a key
+// read 128 contiguous bytes of an entry, and the eight lanes that a store serves at
+// once are eight keys, whose swizzled chunks cover the eight bank groups.
 struct KeyData {
-  uint4 v[2][2];      // [half][16 bytes]: an entry's codes in [half][0]
-  uint32_t sc[2];     // [half]: an entry's two scales
+  uint4 v[2][4];      // [block]: an entry's codes in the first two, or a row's 64
+  uint32_t sc[2];     // [block]: an entry's four scales
   float scale;
   int kind;           // 0 none, 1 entry, 2 row of codes
 };
 
-__device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) { return hmul2_u32(a, b); }
+__device__ __forceinline__ void st_chunk(uint32_t at, int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (uint32_t)(chunk << 4)), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
 
-// Chunks i = 0 .. 3 of 8 channels at `at` ^ 16 i; a lane's order starts at chunk o
-// (the eight lanes of a key then cover the eight bank groups).
-__device__ __forceinline__ void put_entry(uint32_t at, const uint4 &v, uint32_t sc, bool o1, bool o2) {
-  const uint32_t e = e4m3x2_to_half2((uint16_t)sc);
-  const uint32_t s0 = __byte_perm(e, 0, o2 ? 0x3232 : 0x1010), s1 = __byte_perm(e, 0, o2 ? 0x1010 : 0x3232);
-  const uint32_t x = o1 ? v.y : v.x, y = o1 ? v.x : v.y, z = o1 ? v.w : v.z, u = o1 ? v.z : v.w;
-  const uint32_t w[4] = {o2 ? z : x, o2 ? u : y, o2 ? x : z, o2 ? y : u};
+// 64 channels into the 128-byte row whose chunk 0 is at `at` (chunk i at ^ 16 i).
+__device__ __forceinline__ void put_entry(uint32_t at, const uint4 (&v)[4], uint32_t sc) {
+  const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+  const uint32_t e[2] = {e4m3x2_to_half2((uint16_t)sc), e4m3x2_to_half2((uint16_t)(sc >> 16))};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < 8; ++i) {   // 8 channels, of scale i / 2
     uint32_t h[4];
     e2m1x8_to_half2x4(w[i], h);
-    const uint32_t s = i < 2 ? s0 : s1;
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (uint32_t)(i << 4)), "r"(half2_mul(h[0], s)),
-                 "r"(half2_mul(h[1], s)), "r"(half2_mul(h[2], s)), "r"(half2_mul(h[3], s))
-                 : "memory");
+    const uint32_t s = __byte_perm(e[i >> 2], 0, i & 2 ? 0x3232 : 0x1010);
+    st_chunk(at, i, hmul2_u32(h[0], s), hmul2_u32(h[1], s), hmul2_u32(h[2], s), hmul2_u32(h[3], s));
   }
 }
 
-__device__ __forceinline__ void put_codes(uint32_t at, const uint4 &lo, const uint4 &hi, uint32_t keep, bool o1, bool o2) {
-  const uint2 c[4] = {{lo.x, lo.y}, {lo.z, lo.w}, {hi.x, hi.y}, {hi.z, hi.w}};
-  const uint2 d[4] = {o1 ? c[1] : c[0], o1 ? c[0] : c[1], o1 ? c[3] : c[2], o1 ? c[2] : c[3]};
+__device__ __forceinline__ void put_codes(uint32_t at, const uint4 (&v)[4], uint32_t keep) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint2 w = o2 ? d[i ^ 2] : d[i];
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (uint32_t)(i << 4)),
-                 "r"(half2_mul(e4m3x2_to_half2((uint16_t)w.x), keep)), "r"(half2_mul(e4m3x2_to_half2((uint16_t)(w.x >> 16)), keep)),
-                 "r"(half2_mul(e4m3x2_to_half2((uint16_t)w.y), keep)), "r"(half2_mul(e4m3x2_to_half2((uint16_t)(w.y >> 16)), keep))
-                 : "memory");
-  }
-}
-
-__device__ __forceinline__ void put_zeros(uint32_t at) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at ^ (uint32_t)(i << 4)), "r"(0) : "memory");
+    for (int j = 0; j < 2; ++j)
+      st_chunk(at, 2 * i + j, hmul2_u32(e4m3x2_to_half2((uint16_t)w[2 * j]), keep),
+               hmul2_u32(e4m3x2_to_half2((uint16_t)(w[2 * j] >> 16)), keep),
+               hmul2_u32(e4m3x2_to_half2((uint16_t)w[2 * j + 1]), keep),
+               hmul2_u32(e4m3x2_to_half2((uint16_t)(w[2 * j + 1] >> 16)), keep));
+  }
 }
 
 // List place of key e, or -1 (past the list).
@@ -169,7 +164,7 @@ __device__ __forceinline__ int32_t list_id(const AttnArgs &a, const Keys &k, int
   return k.steps && e < a.K ? __ldg(a.idx + k.gp * a.K + e) : -1;
 }
 
-__device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e, int32_t id, int c8, KeyData &d) {
+__device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e, int32_t id, int block, KeyData &d) {
   d.kind = 0;
   d.scale = 1.0f;
   if (e < a.K) {
@@ -181,8 +176,9 @@ __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e
     const uint8_t *p = a.kv + (k.entry_row0 + id) * ENTRY_BYTES;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      d.v[h][0] = ld_nc_v4(p + 128 * h + 16 * c8);
-      d.sc[h] = ld_nc_u16(p + 256 + 16 * h + 2 * c8);
+      d.v[h][0] = ld_nc_v4(p + 128 * h + 32 * block);
+      d.v[h][1] = ld_nc_v4(p + 128 * h + 32 * block + 16);
+      d.sc[h] = ld_nc_u32(p + 256 + 16 * h + 4 * block);
     }
     d.kind = 1;
     return;
@@ -203,7 +199,7 @@ __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int u = 0; u < 2; ++u) d.v[h][u] = ld_nc_v4(p + 256 * h + 32 * c8 + 16 * u);
+    for (int u = 0; u < 4; ++u) d.v[h][u] = ld_nc_v4(p + 256 * h + 64 * block + 16 * u);
   d.scale = __uint_as_float(ld_nc_u32(s));
   d.kind = 2;
 }
@@ -227,17 +223,15 @@ __device__ __forceinline__ void convert_q(uint8_t *qs, int t) {
   __syncwarp();
 }
 
-// Eight lanes a key, kRowKeys keys of a step for each lane.
 __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t *qs, int w, int lane) {
-  const int c8 = lane & 7, key0 = 4 * kRowKeys * w + (lane >> 3), o = c8 >> 1;
-  const bool o1 = o & 1, o2 = o & 2;
+  const int key = 8 * w + (lane & 7), block = lane >> 3;
   int64_t token = blockIdx.x;
   // the step in registers (its token's keys k), the one after it (kn, list places idn)
   Keys k, kn;
   int s = 0, sn = 0;
   int64_t tn = token;
-  KeyData d[kRowKeys];
-  int32_t idn[kRowKeys];
+  KeyData d;
+  int32_t idn;
   // the next token with steps from `tn` on
   auto seek = [&]() {
     kn.steps = 0;
@@ -246,16 +240,12 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
       if (kn.steps) break;
     }
   };
-  auto ids = [&]() {
-#pragma unroll
-    for (int j = 0; j < kRowKeys; ++j) idn[j] = list_id(a, kn, sn * kStep + key0 + 4 * j);
-  };
+  auto ids = [&]() { idn = list_id(a, kn, sn * kStep + key); };
   auto load = [&]() {   // the next step becomes the one in registers
     k = kn;
     s = sn;
     if (!k.steps) return;
-#pragma unroll
-    for (int j = 0; j < kRowKeys; ++j) load_key(a, k, s * kStep + key0 + 4 * j, idn[j], c8, d[j]);
+    load_key(a, k, s * kStep + key, idn, block, d);
     if (++sn == kn.steps) {
       sn = 0;
       tn += gridDim.x;
@@ -271,25 +261,22 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
     const uint32_t b = g & 1;
     const bool first = s == 0;
     if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
+    if (block == 0) {
+      const float f = d.scale < kTinyScaleG ? kTinyScaleG : d.scale;
+      S.rs[b][key] = kLogitG * f;
+      S.lg[b][key] = d.kind ? log2f(f) : -INFINITY;
+      S.inv[b][key] = d.kind ? 1.0f / f : 1.0f;
+    }
 #pragma unroll
-    for (int j = 0; j < kRowKeys; ++j) {
-      const int key = key0 + 4 * j;
-      const float f = d[j].scale < kTinyScaleG ? kTinyScaleG : d[j].scale;
-      if (c8 == 0) {
-        S.rs[b][key] = kLogitG * f;
-        S.lg[b][key] = d[j].kind ? log2f(f) : -INFINITY;
-        S.inv[b][key] = d[j].kind ? 1.0f / f : 1.0f;
-      }
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t at = smem_u32(slots) + b * kSlotG + (4 * h + block) * kBlockG + key * 128 + ((key & 7) << 4);
+      if (d.kind == 1) {
+        put_entry(at, d.v[h], d.sc[h]);
+      } else if (d.kind == 2) {
+        put_codes(at, d.v[h], d.scale < kTinyScaleG ? 0u : 0x3C003C00u);
+      } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t at = smem_u32(slots) + b * kSlotG + (4 * h + o) * kBlockG + key * 128 +
-                            (((4 * (c8 & 1)) ^ o ^ (key & 7)) << 4);
-        if (d[j].kind == 1)
-          put_entry(at, d[j].v[h][0], d[j].sc[h], o1, o2);
-        else if (d[j].kind == 2)
-          put_codes(at, d[j].v[h][0], d[j].v[h][1], d[j].scale < kTinyScaleG ? 0u : 0x3C003C00u, o1, o2);
-        else
-          put_zeros(at);
+        for (int i = 0; i < 8; ++i) st_chunk(at, i, 0, 0, 0, 0);
       }
     }
     fence_proxy_async_smem();
@@ -406,42 +393,52 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_
     bar_named(1, kSoftG * 32);
     wait_g(S, &S.slot_free[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
-    // 32 heads x 32 channels at a time (a lane's channel, pairs of heads exchanged
-    // between neighbouring lanes) through the P buffers, which the last products
-    // have read, for stores of 64 bytes a row (tensor copies wait behind the copies
-    // of the next Q: 11,000 clocks, as many as 4-byte stores from the registers)
+    // 32 heads x 32 channels at a time: a lane's channel, heads in pairs, through the
+    // P buffers (which the last products have read) as rows [channel][32 heads], and
+    // back transposed, 8 channels of a head a lane, for 64 contiguous bytes a head.
+    // (Few shared-memory instructions: pairs of channels by shuffles and 4-byte
+    // stores took 9,000 clocks a token beside the row warps' stores.)
+    const int mr = lane & 7, md = 8 * (mr >> 1) + 2 * (lane >> 3) + (mr & 1);   // the lane's matrix row: a channel
+    const uint32_t sw = (lane >> 3 ^ lane >> 1) & 3, mw = (md >> 3 ^ md >> 1) & 3;
 #pragma unroll 1
-    for (int c = 0; c < 256; c += 32) {
-      uint32_t v[32];
-      tmem_ld32(lanes + kColOG + c, v);
-      tmem_ld_wait();
-      if (c == 224) {   // O^T is read: the next token's products may start
-        tc_fence_before();
-        mbar_arrive(&S.o_free);
+    for (int h0 = 0; h0 < H; h0 += 32) {
+      float il[32];
+#pragma unroll
+      for (int q = 0; q < 32; q += 4) {
+        const float4 f = *reinterpret_cast<const float4 *>(S.inv_l + h0 + q);
+        il[q] = f.x;
+        il[q + 1] = f.y;
+        il[q + 2] = f.z;
+        il[q + 3] = f.w;
       }
-      uint8_t *stage = ps + w * 4096 + (c & 32) * 64;   // (two in turn: one barrier a chunk)
-      const float4 *il = reinterpret_cast<const float4 *>(S.inv_l + (c & 32));
-      uint8_t *dst = stage + (lane & 1) * 64 + (lane & 6) * 2;
-      uint32_t o[16];   // (all of them before the first store, which may not pass the loads of inv_l)
+#pragma unroll 1
+      for (int t = 0; t < 4; ++t) {
+        uint32_t v[32];
+        tmem_ld32(lanes + kColOG + 64 * t + h0, v);
+        tmem_ld_wait();
+        if (h0 && t == 3) {   // O^T is read: the next token's products may start
+          tc_fence_before();
+          mbar_arrive(&S.o_free);
+        }
+        const uint32_t stage = smem_u32(ps + w * 4096 + (t & 1) * 2048);   // (two in turn: one barrier a time)
+        uint32_t o[16];
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const float4 f = il[q];
-        o[2 * q] = lane_pair(lane & 1, __uint_as_float(v[4 * q]) * f.x, __uint_as_float(v[4 * q + 1]) * f.y);
-        o[2 * q + 1] = lane_pair(lane & 1, __uint_as_float(v[4 * q + 2]) * f.z, __uint_as_float(v[4 * q + 3]) * f.w);
+        for (int q = 0; q < 16; ++q) {
+          const __nv_bfloat162 f =
+              __floats2bfloat162_rn(__uint_as_float(v[2 * q]) * il[2 * q], __uint_as_float(v[2 * q + 1]) * il[2 * q + 1]);
+          o[q] = *reinterpret_cast<const uint32_t *>(&f);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st_chunk(stage + lane * 64 + (sw << 4), q, o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+        __syncwarp();
+        __nv_bfloat16 *out = a.step.out + (token * H + h0 + (lane >> 2)) * D + t * 128 + 32 * w + 8 * (lane & 3);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint4 u;
+          ldmatrix_x4_trans((stage + md * 64 + (mw << 4)) ^ (uint32_t)(q << 4), u);
+          *reinterpret_cast<uint4 *>(out + 8 * q * D) = u;
+        }
       }
-#pragma unroll
-      for (int q = 0; q < 16; ++q)
-        *reinterpret_cast<uint32_t *>(dst + 2 * q * 64 + (((lane >> 3) ^ (q & 3)) << 4)) = o[q];
-      __syncwarp();
-      __nv_bfloat16 *out = a.step.out + (token * H + (c & 32)) * D + (c >> 6) * 128 + 32 * w + 8 * (lane & 3);
-      uint4 u[4];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = 8 * q + (lane >> 2);
-        u[q] = *reinterpret_cast<const uint4 *>(stage + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4));
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4 *>(out + (8 * q + (lane >> 2)) * D) = u[q];
     }
     bar_named(1, kSoftG * 32);   // inv_l and the other warps' stages may be written again
   }

@@ -648,6 +648,16 @@ __device__ __forceinline__ uint32_t dsmem_atom_add(uint32_t addr, uint32_t v) {
   return old;
 }
 
+// Four 8 x 8 matrices of 16-bit elements, transposed: lane l names row l % 8 of
+// matrix l / 8 (16 bytes, shared memory) and gets, of matrix j in word j, column l /
+// 4 of rows 2 (l % 4) and 2 (l % 4) + 1.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t row, uint4 &v) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(row)
+               : "memory");
+}
+
 // ------------------------------------------------------- FP4 / FP8 helpers
 // Two fp32 -> packed E2M1 pair (hi -> bits 4..7, lo -> bits 0..3), RNE, satfinite.
 __device__ __forceinline__ uint32_t cvt_e2m1x2(float hi, float lo) {
