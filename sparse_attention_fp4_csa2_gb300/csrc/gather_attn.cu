@@ -164,7 +164,17 @@ __device__ __forceinline__ int32_t list_id(const AttnArgs &a, const Keys &k, int
   return k.steps && e < a.K ? __ldg(a.idx + k.gp * a.K + e) : -1;
 }
 
-__device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e, int32_t id, int block, KeyData &d) {
+// 32 bytes of a key; `wide`: the caches are 32-byte aligned (entries are 9 x 32 bytes).
+__device__ __forceinline__ void load32(const uint8_t *p, bool wide, uint4 &x, uint4 &y) {
+  if (wide) {
+    ld_nc_v8(p, x, y);
+  } else {
+    x = ld_nc_v4(p);
+    y = ld_nc_v4(p + 16);
+  }
+}
+
+__device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e, int32_t id, int block, bool wide, KeyData &d) {
   d.kind = 0;
   d.scale = 1.0f;
   if (e < a.K) {
@@ -176,8 +186,7 @@ __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e
     const uint8_t *p = a.kv + (k.entry_row0 + id) * ENTRY_BYTES;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      d.v[h][0] = ld_nc_v4(p + 128 * h + 32 * block);
-      d.v[h][1] = ld_nc_v4(p + 128 * h + 32 * block + 16);
+      load32(p + 128 * h + 32 * block, wide, d.v[h][0], d.v[h][1]);
       d.sc[h] = ld_nc_u32(p + 256 + 16 * h + 4 * block);
     }
     d.kind = 1;
@@ -199,7 +208,7 @@ __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
-    for (int u = 0; u < 4; ++u) d.v[h][u] = ld_nc_v4(p + 256 * h + 64 * block + 16 * u);
+    for (int u = 0; u < 4; u += 2) load32(p + 256 * h + 64 * block + 16 * u, wide, d.v[h][u], d.v[h][u + 1]);
   d.scale = __uint_as_float(ld_nc_u32(s));
   d.kind = 2;
 }
@@ -225,6 +234,8 @@ __device__ __forceinline__ void convert_q(uint8_t *qs, int t) {
 
 __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t *qs, int w, int lane) {
   const int key = 8 * w + (lane & 7), block = lane >> 3;
+  const bool wide = ((reinterpret_cast<uintptr_t>(a.kv) | reinterpret_cast<uintptr_t>(a.swa) |
+                      reinterpret_cast<uintptr_t>(a.step.extra)) & 31) == 0;
   int64_t token = blockIdx.x;
   // the step in registers (its token's keys k), the one after it (kn, list places idn)
   Keys k, kn;
@@ -245,7 +256,7 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
     k = kn;
     s = sn;
     if (!k.steps) return;
-    load_key(a, k, s * kStep + key, idn, block, d);
+    load_key(a, k, s * kStep + key, idn, block, wide, d);
     if (++sn == kn.steps) {
       sn = 0;
       tn += gridDim.x;

@@ -198,6 +198,13 @@ __device__ __forceinline__ uint4 ld_nc_v4(const void *p) {
   return v;
 }
 
+// 32 bytes at once (p 32-byte aligned).
+__device__ __forceinline__ void ld_nc_v8(const void *p, uint4 &a, uint4 &b) {
+  asm volatile("ld.global.nc.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(a.x), "=r"(a.y), "=r"(a.z), "=r"(a.w), "=r"(b.x), "=r"(b.y), "=r"(b.z), "=r"(b.w)
+               : "l"(p));
+}
+
 __device__ __forceinline__ uint2 ld_nc_v2(const void *p) {
   uint2 v;
   asm volatile("ld.global.nc.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
