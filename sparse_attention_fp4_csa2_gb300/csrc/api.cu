@@ -829,13 +829,21 @@ csa2_status run_step(const csa2_params *p, int64_t tokens, const void *q, const 
   a.kernel = p->attn_kernel;
   a.step = s;
   int launches = 0;
-  // Up to a token for two SMs, its keys are split over a cluster (32 window tokens
-  // 14.5 us against 16.2 in tiles, 76 16.3 against 20.0; 80 of four sequences 19.3
-  // against 18.3, 100 21.8 against 21.4); more tokens go in tiles of two that share
-  // their rows where these are all a token has and fit, else a CTA takes one.
+  // A token's keys over a cluster while four CTAs or more a token fit and it has more
+  // keys than four steps of a CTA (5 tokens, 512 + 128 keys: 15.3 us against 23.9 in
+  // one CTA each, 20 tokens 21.8 against 24.2, 40 in pairs 28.5 against 25.5; 5 tokens
+  // with 256 + 128 14.4 against 16.8, with 37 + 128 14.4 against 11.7).
+  // Tiles of two tokens that share their rows, where these are all a token has, fit,
+  // and there are tokens enough to share them (packed tokens, windows of 128: 152 of
+  // one sequence 20.3 us against 14.6 in a CTA each, 300 22.4 against 23.1, 1,200 44
+  // against 72; one each of 608 sequences 69 against 45, two each of 304 40 against
+  // 43.  Trees: 64 x 5 27.7 against 27.2, 128 x 5 35 against 42, 300 x 2 40 against 36).
+  // Else a CTA for each token.
   const int sms = num_sms();
-  const bool split = p->attn_kernel == 1 || (p->attn_kernel == 0 && 2 * tokens <= sms);
-  const bool shared = p->attn_kernel == 0 && !topk_idx && window_rows_fit(s);
+  const int64_t keys = (int64_t)a.K + (s.cu ? s.win + s.extras : s.win > s.extras ? s.win : s.extras);
+  const bool split = p->attn_kernel == 1 || (p->attn_kernel == 0 && 4 * tokens <= sms && keys > 256);
+  const bool shared = p->attn_kernel == 0 && !topk_idx && window_rows_fit(s) &&
+                      (s.cu ? tokens > sms && tokens >= 2 * (int64_t)s.batch : tokens > 2 * sms && s.extras >= 3);
   const cudaError_t e = split    ? launch_sparse_attn(a, nullptr, stream, &launches)
                         : shared ? launch_window_attn(q, swa, swa_scale, s, tokens, lse, sms, stream, &launches)
                                  : launch_gather_attn(a, sms, stream, &launches);

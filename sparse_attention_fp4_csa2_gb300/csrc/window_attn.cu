@@ -307,11 +307,12 @@ __device__ void row_warp(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<kTree
       filling = true;
       ++fresh;
     } else {
+      // (tree form too, which adds no rows: no role may be two phases behind)
+      if (i > 1) wait_w(S, &S.pv_done[i & 1], ((i >> 1) - 1) & 1);
       if constexpr (!kTree) {
         // (a slot written below may be another warp's in the fill before)
         if (filling) wait_w(S, &S.fresh_full, (fresh - 1) & 1);
         filling = false;
-        if (i > 1) wait_w(S, &S.pv_done[i & 1], ((i >> 1) - 1) & 1);
         if (s.win > 0) {
           const uint32_t tiny = __ballot_sync(0xffffffffu, scale < kTinyScaleW);
           const int slot = (int)(t.pos % a.ring), second = slot + 1 == a.ring ? 0 : slot + 1;

@@ -252,7 +252,9 @@ WINDOWS = [
     dict(ctx=[17, 400, 0, 88, 1000], new=[401, 1, 256, 2, 33], W=128, S=15), dict(ctx=[17, 400], new=[33, 260], W=128, S=16),
     dict(ctx=[9, 0], new=[60, 40], W=0, S=6), dict(ctx=[9], new=[100], W=0, S=0), dict(ctx=[0, 700], new=[80, 81], W=128, S=13),
     dict(ctx=[31 * i for i in range(320)], new=[1] * 320, W=128, S=4), dict(ctx=[31 * i for i in range(200)], new=[2 - i % 2 for i in range(200)], W=16, S=1),
-    dict(ctx=[100, 5], new=[90, 77], W=1024, S=3),
+    dict(ctx=[100, 5], new=[90, 77], W=1024, S=3), dict(ctx=[31 * i for i in range(100)], new=[4] * 100, W=128, S=2),
+    dict(ctx=[2, 0], new=[100, 140], W=0, S=6), dict(ctx=[900], new=[400], W=128, S=13), dict(ctx=[3, 0], new=[121, 90], W=1, S=2),
+    dict(ctx=[60 + i for i in range(40)], new=[i % 11 for i in range(40)], W=37, S=3),
 ]
 
 
@@ -399,6 +401,9 @@ TREES = [
     dict(B=2, T=64, K=0, W=128, ctx=[500, 64]), dict(B=2, T=9, K=0, W=0, ctx=[500, 64]), dict(B=2, T=9, K=1, W=0, cap=1, ctx=[0, 64]),
     dict(B=2, T=31, K=0, W=3, ctx=[500, 1]), dict(B=1, T=6, K=2048, W=1024, cap=2100, ctx=[5000]),
     dict(B=40, T=8, K=64, W=128, cap=100, ctx=[31 * i for i in range(40)]), dict(B=64, T=5, K=0, W=128, ctx=[31 * i for i in range(64)]),
+    dict(B=64, T=16, K=0, W=128, ctx=[9 * i for i in range(64)]), dict(B=160, T=10, K=0, W=128, ctx=[5 * i for i in range(160)]),
+    dict(B=20, T=40, K=0, W=100, ctx=[30 * i for i in range(20)]), dict(B=110, T=3, K=0, W=4, ctx=[i for i in range(110)]),
+    dict(B=70, T=9, K=0, W=0, ctx=[7 * i for i in range(70)]),
     dict(B=20, T=9, K=0, W=0, ctx=[7 * i for i in range(20)]), dict(B=10, T=16, K=0, W=128, ctx=[40 * i for i in range(10)]),
     dict(B=30, T=8, K=0, W=3, ctx=[i for i in range(30)]), dict(B=90, T=1, K=0, W=128, ctx=[3 * i for i in range(90)]),
     dict(B=170, T=2, K=1, W=7, cap=3, ctx=[i for i in range(170)]), dict(B=3, T=64, K=130, W=128, cap=200, ctx=[0, 1, 5000]),
@@ -438,6 +443,30 @@ def test_tree_rows_of_any_size(c2, std):
             t.call(c2, kernel)
             assert c2.get_device_status() == 0
             t.check()
+
+
+def test_rows_aligned_to_16_bytes_only(c2):
+    """Caches whose first byte is 16 past a multiple of 32."""
+    def shift(t):
+        buf = torch.zeros(t.numel() + 48, dtype=torch.uint8, device="cuda")
+        off = 16 + (-buf.data_ptr()) % 32
+        new = buf[off:off + t.numel()].view(t.shape)
+        new.copy_(t)
+        return new
+
+    t = Tree(c2, 20, 8, 50, 128, [20 * i for i in range(20)], cap=64, seed=37)
+    for name in ("kv", "swa", "tree"):
+        setattr(t, name, shift(getattr(t, name)))
+        for kernel in (0, 1, 2):
+            t.call(c2, kernel)
+            assert c2.get_device_status() == 0
+            t.check()
+    w = Window([300, 20], [100, 90], 128, 4, seed=38)
+    w.swa, w.sink = shift(w.swa), shift(w.sink)
+    for kernel in (0, 1, 2):
+        w.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        w.check()
 
 
 def test_tree_bad_indices(c2):
