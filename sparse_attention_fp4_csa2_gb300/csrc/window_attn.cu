@@ -18,8 +18,8 @@
 //   S = Q K^T      tcgen05, Q streamed through a ring of four 16 KB pieces of 64
 //                  channels as it arrives (used once: no room and no need for all
 //                  of it), two S buffers in tensor memory;
-//   softmax        a thread per row of S: exact maximum, then the weights, written
-//                  back in place of S as the A operand of the second product;
+//   softmax        two threads per row of S; the weights are written back in place
+//                  of S as the A operand of the second product;
 //   O = P V        P from tensor memory, V^T from the same slots (MN-major), in
 //                  pieces of 128, 64, 128, 64, 128 channels through two buffers;
 //   rows out       bf16 through shared memory and tensor copies.
@@ -29,7 +29,7 @@
 // P = 2^(logit - m) s_k is at most 1 whatever the rows' scales are; the row sum
 // takes it times 1 / s_k.
 //
-// Warps: 0-3 softmax, 4-11 output, 12 rows, 13 copies of Q, 14 first product, 15
+// Warps: 0-7 softmax, 8-15 output, 16 rows, 17 copies of Q, 18 first product, 19
 // second product.  Every wait is bounded; after one runs out every role falls
 // through its waits and the output is undefined (CSA2_DEV_ERR_TIMEOUT).
 #include "kernels.cuh"
@@ -38,10 +38,10 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kOutWarp = 4, kOutWarps = 8;
+constexpr int kOutWarp = 8, kOutWarps = 8;   // softmax warps 0 .. 7
 constexpr int kRowWarp = kOutWarp + kOutWarps;   // one warp
 constexpr int kCopyWarp = kRowWarp + 1, kScoreWarp = kCopyWarp + 1, kValueWarp = kCopyWarp + 2;
-constexpr int kThreadsW = (kValueWarp + 1) * 32;   // 128 registers a thread
+constexpr int kThreadsW = (kValueWarp + 1) * 32;   // 96 registers a thread
 constexpr int kMaxSlots = 144;
 constexpr int kQPiece = 128 * 128;               // [128 rows][64 channels]
 constexpr int kQRing = 4;
@@ -49,6 +49,7 @@ constexpr int kStage = 32 * 64;                  // [32 rows][32 channels] bf16,
 constexpr uint32_t kColS = 0, kColsS = 144;      // two S / P buffers
 constexpr uint32_t kColO = 288;                  // pieces of 128 channels; of 64 channels behind it
 constexpr uint32_t kColL = 480;                  // 1 / row sum, a column per S buffer
+constexpr uint32_t kColX = 482;                  // what a row's two softmax threads tell each other: [half] maximum, reference, sum
 constexpr float kLogitW = 0.06375871295460785f;  // log2(e) / sqrt(512)
 constexpr float kLn2W = 0.69314718055994531f;
 constexpr float kTinyScaleW = 5.421010862427522e-20f;   // 2^-64: rows of a smaller scale count as zeros
@@ -60,7 +61,7 @@ struct __align__(16) CtlW {
   volatile uint32_t abort;
   __align__(16) float rs[kMaxSlots];         // per slot: log2(e) / sqrt(512) x scale
   __align__(16) float lg[kMaxSlots];         // log2(scale)
-  __align__(16) float inv[kMaxSlots + 16];   // 1 / scale (past the last slot 0)
+  __align__(16) float inv[kMaxSlots];        // 1 / scale
 };
 
 constexpr size_t kSmemW = 1024 + (size_t)kMaxSlots * D * 2 + kQRing * kQPiece + kOutWarps * kStage + sizeof(CtlW);
@@ -364,20 +365,21 @@ struct Seen {
       extra = (1ull << (before < s.extras ? (before > 0 ? before : 0) : s.extras)) - 1;   // (fewer than 64 fit behind the window)
     }
   }
-  // slots 32 c .. + 31, a bit each, by whole warps
+  // slots 16 c .. + 15, a bit each, by whole warps
   __device__ __forceinline__ uint32_t word(int c, int lane) const {
-    const int slot = 32 * c + lane, e = slot - held;
+    const int slot = 16 * c + (lane & 15), e = slot - held;
     const int d = slot - at;
     const bool ok = e < 0 ? (kTree || d >= 0 ? d : d + held) < len && (!kTree || d >= 0) : e < 64 && ((extra >> e) & 1);
-    return __ballot_sync(0xffffffffu, ok);
+    return __ballot_sync(0xffffffffu, ok) & 0xFFFFu;
   }
 };
 
-// Weights already written (chunks 0 .. n - 1 of 32 slots) times f: the words of a
-// chunk are 16 of rounded weights and 16 of the rest.
-__device__ __noinline__ void scale_weights(uint32_t st, int n, float f) {
+// Weights already written (chunks c0 .. c1 - 1 of 16 slots) times f: the words of a
+// chunk are 8 of upper halves and 8 of the rest.
+__device__ __noinline__ void scale_weights(uint32_t st, int c0, int c1, float f) {
+  tmem_st_wait();
 #pragma unroll 1
-  for (int c = 0; c < 2 * n; ++c) {
+  for (int c = c0; c < c1; ++c) {
     uint32_t u[16];
     tmem_ld16(st + 16 * c, u);
     tmem_ld_wait();
@@ -391,16 +393,31 @@ __device__ __noinline__ void scale_weights(uint32_t st, int n, float f) {
   tmem_st_wait();
 }
 
-// One pass over a row: its reference is raised only when a logit exceeds it by
-// 2^kLazyW (bf16 has fp32's exponents, so weights above 1 cost nothing), which
-// after the first chunk of 32 slots hardly ever happens; the weights written
-// until then are then scaled in place.
+// Two threads a row, each on half of its chunks of 16 slots, in one pass: the
+// reference is the maximum over both threads' first chunks, raised only when a
+// logit exceeds it by 2^kLazyW (bf16 has fp32's exponents, so weights above 1 cost
+// nothing), which hardly ever happens; the weights written until then are then
+// scaled in place, and the other thread's at the end.
 constexpr float kLazyW = 40.0f;
+
+// v of this thread's row to the other one of the row (the other half's warp of the
+// same 32 rows), and its back.
+__device__ __forceinline__ float swap_row(uint32_t lanes, int what, int half, int quarter, float v) {
+  tmem_st1(lanes + kColX + 2 * what + half, __float_as_uint(v));
+  tmem_st_wait();
+  tc_fence_before();
+  bar_named(1 + quarter, 64);
+  tc_fence_after();
+  return __uint_as_float(tmem_ld1(lanes + kColX + 2 * what + (half ^ 1)));
+}
 
 template <bool kTree>
 __device__ void softmax_warps(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<kTree> walk, uint32_t tmem, int w, int lane) {
-  const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
-  const int j = w >> 1, h = 32 * (w & 1) + lane;   // token of the tile, head
+  const int quarter = w & 3, half = w >> 2;
+  const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+  const int j = quarter >> 1, h = 32 * (quarter & 1) + lane;   // token of the tile, head
+  const int chunks = a.slots >> 4, mid = (chunks + 1) >> 1;
+  const int c0 = half ? mid : 0, c1 = half ? chunks : mid;
   Tile t;
   RowsReady rows;
   for (uint32_t i = 0; walk.next(a, t); ++i) {
@@ -416,49 +433,53 @@ __device__ void softmax_warps(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<
     rows.wait(S, t);   // the slots' scales
     wait_w(S, &S.s_full[b], (i >> 1) & 1);
     tc_fence_after();
-    float m = -INFINITY, ms = 0.0f, l = 0.0f;
+    float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
-    for (int c = 0; 32 * c < a.slots; ++c) {
+    for (int c = c0; c < c1; ++c) {
+      uint32_t u[16];
+      tmem_ld16(st + 16 * c, u);
       const uint32_t seen = see.word(c, lane);
-      float x[32];
-      {
-        uint32_t u[32];
-        tmem_ld32(st + 32 * c, u);   // (a last half chunk reads past the slots: not seen)
-        tmem_ld_wait();
+      float4 r[4], g[4];
 #pragma unroll
-        for (int q = 0; q < 32; q += 4) {
-          const float4 r = *reinterpret_cast<const float4 *>(S.rs + 32 * c + q);
-          const float4 g = *reinterpret_cast<const float4 *>(S.lg + 32 * c + q);
-          x[q] = fmaf(__uint_as_float(u[q]), r.x, g.x);
-          x[q + 1] = fmaf(__uint_as_float(u[q + 1]), r.y, g.y);
-          x[q + 2] = fmaf(__uint_as_float(u[q + 2]), r.z, g.z);
-          x[q + 3] = fmaf(__uint_as_float(u[q + 3]), r.w, g.w);
-        }
+      for (int q = 0; q < 4; ++q) {
+        r[q] = *reinterpret_cast<const float4 *>(S.rs + 16 * c + 4 * q);
+        g[q] = *reinterpret_cast<const float4 *>(S.lg + 16 * c + 4 * q);
       }
-      if (seen != 0xFFFFFFFFu) {
+      tmem_ld_wait();
+      float x[16];
 #pragma unroll
-        for (int q = 0; q < 32; ++q)
+      for (int q = 0; q < 4; ++q) {
+        x[4 * q] = fmaf(__uint_as_float(u[4 * q]), r[q].x, g[q].x);
+        x[4 * q + 1] = fmaf(__uint_as_float(u[4 * q + 1]), r[q].y, g[q].y);
+        x[4 * q + 2] = fmaf(__uint_as_float(u[4 * q + 2]), r[q].z, g[q].z);
+        x[4 * q + 3] = fmaf(__uint_as_float(u[4 * q + 3]), r[q].w, g[q].w);
+      }
+      if (seen != 0xFFFFu) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q)
           if (!(seen >> q & 1)) x[q] = -INFINITY;
       }
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int q = 0; q < 32; ++q) mx[q & 3] = fmaxf(mx[q & 3], x[q]);
-      const float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const bool up = cm > m + kLazyW;
-      if (__any_sync(0xffffffffu, up)) {
-        const float f = !up ? 1.0f : m == -INFINITY ? 0.0f : ex2_approx(m - cm);
-        if (__any_sync(0xffffffffu, up && m != -INFINITY)) {
-          tmem_st_wait();
-          scale_weights(st, c, f);
+      for (int q = 0; q < 16; ++q) mx[q & 3] = fmaxf(mx[q & 3], x[q]);
+      float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if (c == c0) {
+        m = fmaxf(cm, swap_row(lanes, 0, half, quarter, cm));
+      } else {
+        const bool up = cm > m + kLazyW;
+        if (__any_sync(0xffffffffu, up)) {
+          const float f = !up ? 1.0f : m == -INFINITY ? 0.0f : ex2_approx(m - cm);
+          if (__any_sync(0xffffffffu, up && m != -INFINITY)) scale_weights(st, c0, c, f);
+          l *= f;
+          if (up) m = cm;
         }
-        l *= f;
-        if (up) m = ms = cm;
       }
-      uint32_t o[32];
+      const float ms = m == -INFINITY ? 0.0f : m;
+      uint32_t o[16];
       float l2 = 0.0f;
 #pragma unroll
-      for (int q = 0; q < 32; q += 4) {
-        const float4 v = *reinterpret_cast<const float4 *>(S.inv + 32 * c + q);
+      for (int q = 0; q < 16; q += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(S.inv + 16 * c + q);
         const float p0 = ex2_approx(x[q] - ms), p1 = ex2_approx(x[q + 1] - ms), p2 = ex2_approx(x[q + 2] - ms),
                     p3 = ex2_approx(x[q + 3] - ms);
         l = fmaf(p0, v.x, fmaf(p1, v.y, l));
@@ -469,27 +490,28 @@ __device__ void softmax_warps(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<
         o[(q >> 1) + 1] = __byte_perm(b2, b3, 0x7632);
         const __nv_bfloat162 r0 = __floats2bfloat162_rn(p0 - __uint_as_float(b0 & 0xFFFF0000u), p1 - __uint_as_float(b1 & 0xFFFF0000u));
         const __nv_bfloat162 r1 = __floats2bfloat162_rn(p2 - __uint_as_float(b2 & 0xFFFF0000u), p3 - __uint_as_float(b3 & 0xFFFF0000u));
-        o[16 + (q >> 1)] = *reinterpret_cast<const uint32_t *>(&r0);
-        o[16 + (q >> 1) + 1] = *reinterpret_cast<const uint32_t *>(&r1);
+        o[8 + (q >> 1)] = *reinterpret_cast<const uint32_t *>(&r0);
+        o[8 + (q >> 1) + 1] = *reinterpret_cast<const uint32_t *>(&r1);
       }
       l += l2;
-      if (32 * c + 32 <= a.slots) {
-        tmem_st32(st + 32 * c, o);
-      } else {
-        uint32_t half[16];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          half[k] = o[k];
-          half[8 + k] = o[16 + k];
-        }
-        tmem_st16(st + 32 * c, half);
-      }
+      tmem_st16(st + 16 * c, o);
     }
-    tmem_st1(lanes + kColL + b, __float_as_uint(l > 0.0f && !S.abort ? 1.0f / l : l));   // (0 stays 0, a NaN a NaN)
+    if (c0 == c1) m = swap_row(lanes, 0, half, quarter, m);   // (16 slots in all: none of them this thread's)
+    // one reference and one sum for the row
+    tmem_st1(lanes + kColX + 4 + half, __float_as_uint(l));
+    const float mo = swap_row(lanes, 1, half, quarter, m), mm = fmaxf(m, mo);
+    const float lo = __uint_as_float(tmem_ld1(lanes + kColX + 4 + (half ^ 1)));
+    if (__any_sync(0xffffffffu, m < mm)) {
+      const float f = m < mm ? (m == -INFINITY ? 0.0f : ex2_approx(m - mm)) : 1.0f;
+      scale_weights(st, c0, c1, f);
+      l *= f;
+    }
+    l += mo < mm ? (mo == -INFINITY ? 0.0f : lo * ex2_approx(mo - mm)) : lo;
+    if (half == 0) tmem_st1(lanes + kColL + b, __float_as_uint(l > 0.0f && !S.abort ? 1.0f / l : l));   // (0 stays 0, a NaN a NaN)
     tmem_st_wait();
     tc_fence_before();
     mbar_arrive(&S.p_full[b]);
-    if (a.lse && j < t.n) a.lse[(t.tok + j) * H + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2W;
+    if (half == 0 && a.lse && j < t.n) a.lse[(t.tok + j) * H + h] = l == 0.0f ? -INFINITY : (mm + log2f(l)) * kLn2W;
   }
 }
 
@@ -621,12 +643,9 @@ __device__ void value_warp(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<kTr
       uint64_t vb = vd + (uint64_t)(3 * (piece >> 1) + 2 * buf) * col;
 #pragma unroll 1
       for (int k = 0; k < steps; ++k, vb += 128) {
-        // 16 slots: 8 columns of rounded weights, and of the rest 16 columns
-        // (in a last half chunk of 16 slots: 8) behind them
-        const uint32_t pa = p + 32 * (k >> 1) + 8 * (k & 1);
-        const uint32_t rest = (k == steps - 1 && !(k & 1)) ? 8 : 16;
-        mma_f16_ts(d, pa, vb, idesc, k ? 1u : 0u);
-        mma_f16_ts(d, pa + rest, vb, idesc, 1u);
+        // 16 slots: 8 columns of upper halves, 8 of the rest
+        mma_f16_ts(d, p + 16 * k, vb, idesc, k ? 1u : 0u);
+        mma_f16_ts(d, p + 16 * k + 8, vb, idesc, 1u);
       }
       mma_commit(&S.o_full[buf]);
     }
@@ -654,7 +673,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.rows_full[i], 1);
       mbar_init(&S.s_full[i], 1);
-      mbar_init(&S.p_full[i], 128);
+      mbar_init(&S.p_full[i], kOutWarp * 32);
       mbar_init(&S.pv_done[i], 1);
       mbar_init(&S.o_full[i], 1);
       mbar_init(&S.o_free[i], kOutWarps);
@@ -662,7 +681,6 @@ __global__ void __launch_bounds__(kThreadsW, 1)
     mbar_init(&S.fresh_full, kFillWarps);
     mbar_init(&S.done, 1);
     S.abort = 0;
-    for (int i = 0; i < 16; ++i) S.inv[a.slots + i] = 0.0f;   // a half chunk at the end multiplies them by 0
     fence_barrier_init();
   }
   if (warp == kCopyWarp && lane == 0) {
