@@ -101,6 +101,31 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs &a, int64_t gp) {
   return k;
 }
 
+// The CTA's tokens that have steps, by whole warps; the next one is looked up while
+// the one before is worked on.
+struct Tokens {
+  int64_t next;
+  int steps;   // of the token `next`
+  __device__ __forceinline__ void seek(const AttnArgs &a) {
+    for (steps = 0; next < a.problems; next += gridDim.x) {
+      steps = keys_of(a, next).steps;
+      if (steps) break;
+    }
+  }
+  __device__ __forceinline__ void start(const AttnArgs &a) {
+    next = blockIdx.x;
+    seek(a);
+  }
+  __device__ __forceinline__ bool take(const AttnArgs &a, int64_t &token, int &n) {
+    token = next;
+    n = steps;
+    if (!n) return false;
+    next += gridDim.x;
+    seek(a);
+    return true;
+  }
+};
+
 // The place of set bit n of m.
 __device__ __forceinline__ int nth_bit(uint64_t m, int n) {
   int at = 0;
@@ -215,18 +240,24 @@ __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e
 
 // Q in place from bf16 to fp16.
 __device__ __forceinline__ void convert_q(uint8_t *qs, int t) {
-  uint4 *q = reinterpret_cast<uint4 *>(qs);
-#pragma unroll 4
-  for (int i = t; i < H * D * 2 / 16; i += kRowG * 32) {
-    const uint4 v = q[i];
-    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-    uint32_t h[4];
+  uint4 *q = reinterpret_cast<uint4 *>(qs) + t;
+  constexpr int kAtOnce = 8;   // loads before the first store
+#pragma unroll 1
+  for (int i = 0; i < H * D * 2 / 16; i += kAtOnce * kRowG * 32) {
+    uint4 v[kAtOnce];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __half2 f = __floats2half2_rn(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
-      h[j] = *reinterpret_cast<const uint32_t *>(&f);
+    for (int u = 0; u < kAtOnce; ++u) v[u] = q[i + u * kRowG * 32];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
+      uint32_t h[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2 f = __floats2half2_rn(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
+        h[j] = *reinterpret_cast<const uint32_t *>(&f);
+      }
+      q[i + u * kRowG * 32] = make_uint4(h[0], h[1], h[2], h[3]);
     }
-    q[i] = make_uint4(h[0], h[1], h[2], h[3]);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -308,11 +339,13 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_
   const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
   const int th = lane >> 4, h = 16 * w + (lane & 15);
   uint32_t g = 0;
-  for (int64_t token = blockIdx.x; token < a.problems; token += gridDim.x) {
-    const Keys k = keys_of(a, token);
+  Tokens tokens;
+  tokens.start(a);
+  int64_t token;
+  for (int steps; tokens.take(a, token, steps);) {
     float m = -INFINITY, l = 0.0f;
 #pragma unroll 1
-    for (int s = 0; s < k.steps; ++s, ++g) {
+    for (int s = 0; s < steps; ++s, ++g) {
       const uint32_t b = g & 1, ph = (g >> 1) & 1;
       wait_g(S, &S.rows_full[b], ph);   // the keys' scales
       wait_g(S, &S.s_full[b], ph);
@@ -394,7 +427,6 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_
       tc_fence_before();
       mbar_arrive(&S.p_full[b]);
     }
-    if (!k.steps) continue;
     // ---------------------------------------------------------- token's end
     l += __shfl_xor_sync(0xffffffffu, l, 16);
     if (th == 0) {
@@ -466,9 +498,10 @@ __device__ __forceinline__ void load_q_g(CtlG &S, const CUtensorMap &tm_q, uint8
 __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q, uint8_t *slots, uint8_t *qs, uint32_t tmem) {
   const uint64_t qd = smem_desc(smem_u32(qs), 16, 1024), kd = smem_desc(smem_u32(slots), 16, 1024);
   uint32_t g = 0, n = 0, copies = 0;
-  for (int64_t token = blockIdx.x; token < a.problems; token += gridDim.x) {
-    const Keys k = keys_of(a, token);
-    if (!k.steps) continue;
+  Tokens tokens;
+  tokens.start(a);
+  int64_t token;
+  for (int steps; tokens.take(a, token, steps);) {
     // Q's last reader was the token before's last S
     if (n) wait_g(S, &S.q_free, (n - 1) & 1);
     if (!S.abort) {
@@ -479,7 +512,7 @@ __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q
     wait_g(S, &S.q_ready, n & 1);
     ++n;
 #pragma unroll 1
-    for (int s = 0; s < k.steps; ++s, ++g) {
+    for (int s = 0; s < steps; ++s, ++g) {
       const uint32_t b = g & 1, d = tmem + b * 128;
       wait_g(S, &S.rows_full[b], (g >> 1) & 1);
       if (g > 1) wait_g(S, &S.p_full[b], ((g >> 1) - 1) & 1);   // S of two steps ago has been read
@@ -497,7 +530,7 @@ __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q
           kb += 2 * (kBlockG >> 4);
         }
         mma_commit(&S.s_full[b]);
-        if (s == k.steps - 1) mma_commit(&S.q_free);
+        if (s == steps - 1) mma_commit(&S.q_free);
       }
       __syncwarp();
     }
@@ -510,13 +543,14 @@ __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q
 __device__ void value_warp_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t *ps, uint32_t tmem) {
   const uint64_t vd = smem_desc(smem_u32(slots), kBlockG, 1024), pd = smem_desc(smem_u32(ps), 16, 1024);
   uint32_t g = 0, n = 0;
-  for (int64_t token = blockIdx.x; token < a.problems; token += gridDim.x) {
-    const Keys k = keys_of(a, token);
-    if (!k.steps) continue;
+  Tokens tokens;
+  tokens.start(a);
+  int64_t token;
+  for (int steps; tokens.take(a, token, steps);) {
     if (n) wait_g(S, &S.o_free, (n - 1) & 1);
     ++n;
 #pragma unroll 1
-    for (int s = 0; s < k.steps; ++s, ++g) {
+    for (int s = 0; s < steps; ++s, ++g) {
       const uint32_t b = g & 1;
       wait_g(S, &S.p_full[b], (g >> 1) & 1);
       tc_fence_after();
