@@ -436,10 +436,7 @@ def prefix_attn(params, q, prefix_kv, kv, topk_idx, swa, swa_scale, swa_len, out
         _dev(ws, torch.uint8, None, "ws", dev), ws.numel(), _stream(stream)), "csa2_prefix_attn")
 
 
-class SlotMaps(NamedTuple):
-    """Outputs of ``slot_map``: cu int32 [B + 1], tok_seq int32 [n], pos and
-    swa_slot int64 [n], entry_cu int32 [B + 1], entry_pos and slot int64
-    [entries], n_vis and swa_len int32 [B]."""
+class _SlotMaps(NamedTuple):
     cu: torch.Tensor
     tok_seq: torch.Tensor
     pos: torch.Tensor
@@ -449,6 +446,25 @@ class SlotMaps(NamedTuple):
     slot: torch.Tensor
     n_vis: torch.Tensor
     swa_len: torch.Tensor
+
+
+class SlotMaps(_SlotMaps):
+    """Outputs of ``slot_map``: cu int32 [B + 1], tok_seq int32 [n], pos and
+    swa_slot int64 [n], entry_cu int32 [B + 1], entry_pos and slot int64
+    [entries], n_vis and swa_len int32 [B]."""
+
+    def pointers(self, batch, dev):
+        """Device pointers of the nine (checked: the checks' result is kept with the
+        pointers it holds for, and redone when one of them has changed)."""
+        p = tuple([t.data_ptr() for t in self])
+        if self.__dict__.get("_checked") != (p, batch, dev):
+            n, e, i32, i64 = self.pos.numel(), self.slot.numel(), torch.int32, torch.int64
+            for t, dtype, size, name in zip(self, (i32, i32, i64, i64, i32, i64, i64, i32, i32),
+                                            (batch + 1, n, n, n, batch + 1, e, e, batch, batch), self._fields):
+                _dev(t, dtype, (size,), name, dev)
+            self._sizes = n, e
+            self._checked = p, batch, dev
+        return p, self._sizes
 
 
 def slot_maps(batch: int, n_tokens: int, m: int = 1, device=None) -> SlotMaps:
@@ -469,15 +485,11 @@ def slot_maps(batch: int, n_tokens: int, m: int = 1, device=None) -> SlotMaps:
 def slot_map(ctx_len, new_len, cap, swa_rows, maps, m=1, stream=None):
     """A step's positions and cache rows from its lengths: ctx_len, new_len int32
     [B]; cap entries and swa_rows ring rows per sequence; maps of ``slot_maps``."""
-    B, n, e, dev = ctx_len.numel(), maps.pos.numel(), maps.slot.numel(), _cur(ctx_len)
-    i32, i64 = torch.int32, torch.int64
+    B, dev = ctx_len.numel(), _cur(ctx_len)
+    p, (n, e) = maps.pointers(B, dev)
     _check(lib().csa2_slot_map(
-        B, _dev(ctx_len, i32, (B,), "ctx_len", dev), _dev(new_len, i32, (B,), "new_len", dev), m, cap, swa_rows, n, e,
-        _dev(maps.cu, i32, (B + 1,), "cu", dev), _dev(maps.tok_seq, i32, (n,), "tok_seq", dev),
-        _dev(maps.pos, i64, (n,), "pos", dev), _dev(maps.swa_slot, i64, (n,), "swa_slot", dev),
-        _dev(maps.entry_cu, i32, (B + 1,), "entry_cu", dev), _dev(maps.entry_pos, i64, (e,), "entry_pos", dev),
-        _dev(maps.slot, i64, (e,), "slot", dev), _dev(maps.n_vis, i32, (B,), "n_vis", dev),
-        _dev(maps.swa_len, i32, (B,), "swa_len", dev), _stream(stream)), "csa2_slot_map")
+        B, _dev(ctx_len, torch.int32, (B,), "ctx_len", dev), _dev(new_len, torch.int32, (B,), "new_len", dev), m, cap,
+        swa_rows, n, e, *p, _stream(stream)), "csa2_slot_map")
 
 
 def window_attn(params, q, cu, ctx_len, swa, swa_scale, out, sink=None, sink_scale=None, lse=None, stream=None):

@@ -10,9 +10,9 @@
 // What it has to move: 8 bytes a sequence in, 16 out, 20 bytes a token and 16 an
 // entry out; small calls are the launch and the scan's latency.  One launch, no
 // pass between CTAs: each CTA scans all the lengths itself (8,192 at most, which
-// stay in L2), keeps both prefix sums in shared memory and takes every
-// gridDim-th stretch of the tokens and entries, finding a token's sequence by
-// binary search there.
+// stay in L2), keeps both prefix sums and the lengths before the step in shared
+// memory and takes every gridDim-th stretch of the tokens and entries, finding a
+// token's sequence by binary search there.
 #include "kernels.cuh"
 
 namespace csa2 {
@@ -80,9 +80,9 @@ __device__ __forceinline__ int sequence_of(const int32_t *cu, int batch, int32_t
 }
 
 __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a) {
-  extern __shared__ int32_t sums[];   // [batch + 1] tokens, [batch + 1] entries
+  extern __shared__ int32_t sums[];   // [batch + 1] tokens, [batch + 1] entries, [batch] tokens before the step
   __shared__ int64_t part[kMapThreads / 32][2];
-  int32_t *tok = sums, *ent = sums + a.batch + 1;
+  int32_t *tok = sums, *ent = sums + a.batch + 1, *ctx = ent + a.batch + 1;
   pdl_wait();
   const int per = (a.batch + blockDim.x - 1) / blockDim.x;
   const int b0 = min((int)threadIdx.x * per, a.batch), b1 = min(b0 + per, a.batch);
@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
     // sums past 32 bits name no token of the outputs: they stay at the largest
     tok[b] = (int32_t)min(t, (int64_t)INT32_MAX);
     ent[b] = (int32_t)min(e, (int64_t)INT32_MAX);
+    ctx[b] = (int32_t)c;
     t += n;
     e += (c + n) / a.m - c / a.m;
     if (first) {
@@ -131,9 +132,10 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
     if (i < tok[a.batch]) {
       seq = sequence_of(tok, a.batch, (int32_t)i);
       const int32_t r = (int32_t)i - tok[seq];
-      pos = (int64_t)max(a.ctx_len[seq], 0) + r;
+      pos = (int64_t)ctx[seq] + r;
       // (a row that a later token of the step takes again is written once, by that one)
-      if (a.new_len[seq] - r <= a.ring) slot = (int64_t)seq * a.ring + (uint64_t)pos % (uint64_t)a.ring;
+      if (tok[seq + 1] - tok[seq] - r <= a.ring)
+        slot = (int64_t)seq * a.ring + (((uint64_t)pos | (uint64_t)a.ring) >> 32 ? pos % a.ring : (uint32_t)pos % (uint32_t)a.ring);
     }
     a.tok_seq[i] = seq;
     a.pos[i] = pos;
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
     int64_t pos = -1, slot = -1;
     if (i < ent[a.batch]) {
       const int seq = sequence_of(ent, a.batch, (int32_t)i);
-      const int64_t e1 = (int64_t)max(a.ctx_len[seq], 0) / a.m + ((int32_t)i - ent[seq]);
+      const int64_t e1 = (int64_t)(ctx[seq] >> (a.m - 1)) + ((int32_t)i - ent[seq]);
       pos = e1 * a.m + a.m - 1;
       if (e1 < a.cap) slot = seq * a.cap + e1;
     }
@@ -179,9 +181,11 @@ cudaError_t launch_slot_map(const int32_t *ctx_len, const int32_t *new_len, int3
   const int64_t rows = n_tokens > n_entries ? n_tokens : n_entries;
   int64_t ctas = (rows + kMapThreads - 1) / kMapThreads;
   ctas = ctas < 1 ? 1 : ctas < 4 * num_sms ? ctas : 4 * num_sms;
-  const size_t smem = (size_t)2 * (batch + 1) * sizeof(int32_t);
-  const cudaError_t e = cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
+  const size_t smem = ((size_t)3 * batch + 2) * sizeof(int32_t);
+  if (smem > 48 * 1024) {   // (less needs no attribute)
+    const cudaError_t e = cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_pdl(slot_map_kernel, dim3((unsigned)ctas), dim3(kMapThreads), smem, stream, 0u, a);
 }
 

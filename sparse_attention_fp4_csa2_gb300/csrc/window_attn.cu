@@ -145,7 +145,20 @@ struct Walk {
     } else {
       if (tok >= end) return false;
       if (tok == seq_end) {
-        while (seq + 1 < a.s.batch && a.s.cu[seq + 1] <= tok) ++seq;
+        // the next one with tokens: the neighbour, or by binary search (a run of empty ones)
+        ++seq;
+        if (seq + 1 < a.s.batch && a.s.cu[seq + 1] <= tok) {
+          int n = a.s.batch - seq;   // the answer is one of seq .. seq + n - 1
+          while (n > 1) {
+            const int half = n >> 1;
+            if (a.s.cu[seq + half] <= tok) {
+              seq += half;
+              n -= half;
+            } else {
+              n = half;
+            }
+          }
+        }
         enter(a);
       }
       t.n = seq_end - tok > 1 ? 2 : 1;

@@ -314,6 +314,29 @@ def test_window_ring_too_short(c2):
     assert c2.get_device_status() == 2
 
 
+def test_window_many_empty_sequences(c2):
+    """Tokens of the first and the last of a million sequences, and of one among them."""
+    B, n, at = 1_000_000, 130, 654_321
+    w = Window([300, 200, 5], [n, n, n], 128, 4, seed=9)
+    ctx, cu = torch.zeros(B, dtype=torch.int32, device="cuda"), torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    place = torch.tensor([0, at, B - 1], device="cuda")
+    ctx[place] = w.ctx_t
+    cu[1:at + 1], cu[at + 1:B], cu[B] = n, 2 * n, 3 * n
+    # (rings of a million sequences would be 65 GB and more: W = 0, two first tokens each)
+    sink, scale = torch.zeros(B, 2, D, dtype=torch.uint8, device="cuda"), torch.ones(B, 2, device="cuda")
+    codes, s = rows8((3, 2), 10)
+    sink[place], scale[place] = codes, s
+    for kernel in (0, 2):
+        c2.window_attn(c2.Params.make(sliding_window=0, attn_kernel=kernel), w.q, cu, ctx, None, None, w.out, sink=sink,
+                       sink_scale=scale, lse=w.lse)
+        assert c2.get_device_status() == 0
+        for i in (0, 1, n - 1, n, 2 * n - 1, 2 * n, 3 * n - 1):
+            b = i // n
+            seen = min(2, w.ctx[b] + i - b * n + 1)
+            ref, lse = attend64(w.q[i].double(), rows64(codes[b, :seen], s[b, :seen]))
+            check_out(w.out[i], w.lse[i], ref, lse)
+
+
 @pytest.mark.parametrize("new", [1, 40])
 def test_window_graph_stream_and_repeat(c2, new):
     """A captured call replayed on other inputs, beside calls on another stream; the same call twice gives the same bits."""
