@@ -426,38 +426,43 @@ csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch, const voi
                              const uint8_t *swa, const float *swa_scale, const int32_t *swa_len, void *out, float *lse,
                              void *ws, size_t ws_bytes, csa2_stream_t stream);
 
+/* What csa2_slot_map writes (device pointers). */
+typedef struct {
+  int32_t *cu;        /* [batch + 1]: exclusive prefix sums of new_len; tokens cu[b] ..
+                         cu[b + 1] - 1 are sequence b's                               */
+  int32_t *tok_seq;   /* [n_tokens]: the token's sequence                             */
+  int64_t *pos;       /* [n_tokens]: its position, ctx_len[b] + (i - cu[b])           */
+  int64_t *swa_slot;  /* [n_tokens]: its row of the window rings, b * swa_rows + pos
+                         mod swa_rows (for csa2_swa_quant_write); -1 when a later
+                         token of the same step takes that row                        */
+  int32_t *entry_cu;  /* [batch + 1]: the same sums of the main-KV entries that the
+                         step completes (at m = 2 one per odd position it reaches)    */
+  int64_t *entry_pos; /* [n_entries]: the entry's position, m e + m - 1               */
+  int64_t *slot;      /* [n_entries]: its row, b * cap + e (for csa2_kv_quant_write,
+                         csa2_kv_quant_write_ik, csa2_indexer_k_quant); -1 when e >=
+                         cap                                                          */
+  int32_t *n_vis;     /* [batch]: entries after the step, at most cap                 */
+  int32_t *swa_len;   /* [batch]: ring rows that hold a token, at most swa_rows       */
+} csa2_slot_maps;
+
 /*
  * csa2_slot_map -- from the lengths of a step's requests, the positions and
  * cache rows that the writers take and the counts that the readouts take.
  * Sequence b holds ctx_len[b] tokens and gets new_len[b] more in this step; the
  * step's tokens are packed, sequence after sequence.
- *   cu        int32 [batch + 1] (out): exclusive prefix sums of new_len; tokens
- *             cu[b] .. cu[b + 1] - 1 are sequence b's
- *   tok_seq   int32 [n_tokens] (out): the token's sequence
- *   pos       int64 [n_tokens] (out): its position, ctx_len[b] + (i - cu[b])
- *   swa_slot  int64 [n_tokens] (out): its row of the window rings, b * swa_rows +
- *             pos mod swa_rows (for csa2_swa_quant_write); -1 when a later token
- *             of the same step takes that row
- *   entry_cu  int32 [batch + 1] (out): the same sums of the main-KV entries that
- *             the step completes (at m = 2 one per odd position it reaches)
- *   entry_pos int64 [n_entries] (out): the entry's position, m e + m - 1
- *   slot      int64 [n_entries] (out): its row, b * cap + e (for
- *             csa2_kv_quant_write, csa2_kv_quant_write_ik, csa2_indexer_k_quant);
- *             -1 when e >= cap
- *   n_vis     int32 [batch] (out): entries after the step, at most cap
- *   swa_len   int32 [batch] (out): ring rows that hold a token, at most swa_rows
+ *   ctx_len, new_len int32 [batch]
  *   m         1 or 2; cap entries and swa_rows >= 1 ring rows per sequence
  *   n_tokens, n_entries: lengths of the outputs.  Places past the last token or
  *             entry get -1 (which the writers skip, and report); tokens and
  *             entries past the outputs' lengths are dropped.
+ *   maps      the outputs (out; the struct itself is read by the call)
  * A negative length (taken as 0), dropped tokens or entries, and a sequence past
  * its cap set CSA2_DEV_ERR_NVIS.  batch above 8192 is CSA2_ERR_UNSUPPORTED.
  * batch == 0 is a no-op.
  */
 csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *new_len, int32_t m, int64_t cap,
-                          int64_t swa_rows, int64_t n_tokens, int64_t n_entries, int32_t *cu, int32_t *tok_seq,
-                          int64_t *pos, int64_t *swa_slot, int32_t *entry_cu, int64_t *entry_pos, int64_t *slot,
-                          int32_t *n_vis, int32_t *swa_len, csa2_stream_t stream);
+                          int64_t swa_rows, int64_t n_tokens, int64_t n_entries, const csa2_slot_maps *maps,
+                          csa2_stream_t stream);
 
 /*
  * csa2_window_attn -- the attention of a window-only layer ([N] section 2: the
@@ -555,7 +560,8 @@ int32_t csa2_last_launch_count(void);
  * right before every launch of the chosen kernel and `stop` right after it
  * (kernel 0 = the indexer sweep, 1 = the sparse-attention kernel, 2 = the
  * chunked-prefill indexer, 3 = the top-K selection).  NULL
- * handles switch the hook off.  Events recorded during stream capture become
+ * handles switch the hook off.  csa2_window_attn and csa2_tree_attn record
+ * nothing.  Events recorded during stream capture become
  * part of the captured graph. */
 typedef enum {
   CSA2_KERNEL_INDEXER_SWEEP = 0,

@@ -89,7 +89,7 @@ def lib():
         L.csa2_indexer_k_read.argtypes = [P, i32, i64, P, i64, P, P]
         L.csa2_cross_attn.argtypes = [i32, i32, P, P, i64, P, i64, P, P, P, sz, P]
         L.csa2_prefix_attn.argtypes = [PP, i32, P, P, i64, P, i64, P, P, P, P, P, P, P, sz, P]
-        L.csa2_slot_map.argtypes = [i32, P, P, i32, i64, i64, i64, i64, P, P, P, P, P, P, P, P, P, P]
+        L.csa2_slot_map.argtypes = [i32, P, P, i32, i64, i64, i64, i64, P, P]
         L.csa2_window_attn.argtypes = [PP, i32, i64, P, P, P, P, P, i64, P, P, i32, P, P, P]
         L.csa2_tree_attn.argtypes = [PP, i32, i32, P, P, i64, P, P, P, i64, P, P, P, P, P, P, P]
         for f in ("csa2_kv_quant_write", "csa2_kv_quant_write_ik", "csa2_indexer_k_quant", "csa2_indexer_score_topk", "csa2_hier_pool_select",
@@ -355,6 +355,11 @@ def _opt(t, dtype, shape, name, dev):
     return None if t is None else _dev(t, dtype, shape, name, dev)
 
 
+def _stream_on(dev, stream):
+    """``_stream`` where the current device is known to be `dev`."""
+    return _raw_stream(dev) if stream is None and _raw_stream is not None else _stream(stream)
+
+
 def swa_quant_write(latent, slot, swa, swa_scale, pos=None, rope_theta=10000.0, stream=None):
     """Write sliding-window rows as FP8: latent bf16 [n, 512]; slot int64 [n]
     (distinct); pos int64 [n] or None (no RoPE); swa uint8 [rows, 512] and
@@ -454,17 +459,20 @@ class SlotMaps(_SlotMaps):
     [entries], n_vis and swa_len int32 [B]."""
 
     def pointers(self, batch, dev):
-        """Device pointers of the nine (checked: the checks' result is kept with the
-        pointers it holds for, and redone when one of them has changed)."""
-        p = tuple([t.data_ptr() for t in self])
-        if self.__dict__.get("_checked") != (p, batch, dev):
+        """Address of the C struct of the nine device pointers, and the lengths
+        (checked: the checks' result is kept with the pointers it holds for, and
+        redone when one of them has changed)."""
+        p = [t.data_ptr() for t in self]
+        d = self.__dict__
+        if d.get("_checked") != (p, batch, dev):
             n, e, i32, i64 = self.pos.numel(), self.slot.numel(), torch.int32, torch.int64
             for t, dtype, size, name in zip(self, (i32, i32, i64, i64, i32, i64, i64, i32, i32),
                                             (batch + 1, n, n, n, batch + 1, e, e, batch, batch), self._fields):
                 _dev(t, dtype, (size,), name, dev)
-            self._sizes = n, e
-            self._checked = p, batch, dev
-        return p, self._sizes
+            d["_struct"] = (ctypes.c_void_p * 9)(*p)
+            d["_args"] = n, e, ctypes.addressof(d["_struct"])
+            d["_checked"] = p, batch, dev
+        return d["_args"]
 
 
 def slot_maps(batch: int, n_tokens: int, m: int = 1, device=None) -> SlotMaps:
@@ -473,23 +481,21 @@ def slot_maps(batch: int, n_tokens: int, m: int = 1, device=None) -> SlotMaps:
     if m not in (1, 2) or batch < 0 or n_tokens < 0:
         raise Csa2Error("slot_maps: m must be 1 or 2, sizes not negative")
     entries = n_tokens if m == 1 else (n_tokens + batch) // 2
-
-    def new(n, dtype):
-        return torch.full((n,), -1, dtype=dtype, device=device or "cuda")
-
-    i32, i64 = torch.int32, torch.int64
-    return SlotMaps(new(batch + 1, i32), new(n_tokens, i32), new(n_tokens, i64), new(n_tokens, i64),
-                    new(batch + 1, i32), new(entries, i64), new(entries, i64), new(batch, i32), new(batch, i32))
+    i64 = torch.full((2 * n_tokens + 2 * entries,), -1, dtype=torch.int64, device=device or "cuda")
+    i32 = torch.full((n_tokens + 4 * batch + 2,), -1, dtype=torch.int32, device=device or "cuda")
+    pos, swa_slot, entry_pos, slot = i64.split([n_tokens, n_tokens, entries, entries])
+    cu, entry_cu, n_vis, swa_len, tok_seq = i32.split([batch + 1, batch + 1, batch, batch, n_tokens])
+    return SlotMaps(cu, tok_seq, pos, swa_slot, entry_cu, entry_pos, slot, n_vis, swa_len)
 
 
 def slot_map(ctx_len, new_len, cap, swa_rows, maps, m=1, stream=None):
     """A step's positions and cache rows from its lengths: ctx_len, new_len int32
     [B]; cap entries and swa_rows ring rows per sequence; maps of ``slot_maps``."""
     B, dev = ctx_len.numel(), _cur(ctx_len)
-    p, (n, e) = maps.pointers(B, dev)
+    n, e, out = maps.pointers(B, dev)
     _check(lib().csa2_slot_map(
         B, _dev(ctx_len, torch.int32, (B,), "ctx_len", dev), _dev(new_len, torch.int32, (B,), "new_len", dev), m, cap,
-        swa_rows, n, e, *p, _stream(stream)), "csa2_slot_map")
+        swa_rows, n, e, out, _stream_on(dev, stream)), "csa2_slot_map")
 
 
 def window_attn(params, q, cu, ctx_len, swa, swa_scale, out, sink=None, sink_scale=None, lse=None, stream=None):
@@ -507,7 +513,7 @@ def window_attn(params, q, cu, ctx_len, swa, swa_scale, out, sink=None, sink_sca
         _opt(swa, torch.uint8, (B, rows, D), "swa", dev), _opt(swa_scale, torch.float32, (B, rows), "swa_scale", dev), rows,
         _opt(sink, torch.uint8, (B, S, D), "sink", dev), _opt(sink_scale, torch.float32, (B, S), "sink_scale", dev), S,
         _dev(out, torch.bfloat16, (n, H, D), "out", dev), _opt(lse, torch.float32, (n, H), "lse", dev),
-        _stream(stream)), "csa2_window_attn")
+        _stream_on(dev, stream)), "csa2_window_attn")
 
 
 def tree_attn(params, q, kv, topk_idx, swa, swa_scale, ctx_len, tree, tree_scale, tree_mask, out, lse=None,
@@ -529,4 +535,4 @@ def tree_attn(params, q, kv, topk_idx, swa, swa_scale, ctx_len, tree, tree_scale
         _dev(ctx_len, torch.int32, (B,), "ctx_len", dev), _dev(tree, torch.uint8, (B, T, D), "tree", dev),
         _dev(tree_scale, torch.float32, (B, T), "tree_scale", dev), _dev(tree_mask, torch.int64, (B, T), "tree_mask", dev),
         _dev(out, torch.bfloat16, (B, T, H, D), "out", dev), _opt(lse, torch.float32, (B, T, H), "lse", dev),
-        _stream(stream)), "csa2_tree_attn")
+        _stream_on(dev, stream)), "csa2_tree_attn")

@@ -4,7 +4,6 @@
 
 #include <cmath>
 #include <cstring>
-#include <initializer_list>
 #include <mutex>
 
 #include "kernels.cuh"
@@ -37,6 +36,7 @@ namespace {
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -779,27 +779,25 @@ extern "C" csa2_status csa2_prefix_attn(const csa2_params *params, int32_t batch
 }
 
 extern "C" csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *new_len, int32_t m,
-                                     int64_t cap, int64_t swa_rows, int64_t n_tokens, int64_t n_entries, int32_t *cu,
-                                     int32_t *tok_seq, int64_t *pos, int64_t *swa_slot, int32_t *entry_cu,
-                                     int64_t *entry_pos, int64_t *slot, int32_t *n_vis, int32_t *swa_len,
-                                     csa2_stream_t stream) {
+                                     int64_t cap, int64_t swa_rows, int64_t n_tokens, int64_t n_entries,
+                                     const csa2_slot_maps *maps, csa2_stream_t stream) {
   g_last_launches = 0;
   if (batch < 0 || (m != 1 && m != 2) || cap < 0 || swa_rows < 1 || n_tokens < 0 || n_entries < 0)
     return CSA2_ERR_INVALID_ARG;
   if (batch == 0) return CSA2_OK;
-  if (!ctx_len || !new_len || !cu || !entry_cu || !n_vis || !swa_len || (n_tokens > 0 && (!tok_seq || !pos || !swa_slot)) ||
-      (n_entries > 0 && (!entry_pos || !slot)))
+  if (!ctx_len || !new_len || !maps) return CSA2_ERR_INVALID_ARG;
+  const csa2_slot_maps &o = *maps;
+  if (!o.cu || !o.entry_cu || !o.n_vis || !o.swa_len || (n_tokens > 0 && (!o.tok_seq || !o.pos || !o.swa_slot)) ||
+      (n_entries > 0 && (!o.entry_pos || !o.slot)))
     return CSA2_ERR_INVALID_ARG;
-  for (const void *p : {(const void *)ctx_len, (const void *)new_len, (const void *)cu, (const void *)tok_seq,
-                        (const void *)entry_cu, (const void *)n_vis, (const void *)swa_len})
-    if (!aligned4(p)) return CSA2_ERR_INVALID_ARG;
-  for (const void *p : {(const void *)pos, (const void *)swa_slot, (const void *)entry_pos, (const void *)slot})
-    if (reinterpret_cast<uintptr_t>(p) & 7u) return CSA2_ERR_INVALID_ARG;
+  if (!aligned4(ctx_len) || !aligned4(new_len) || !aligned4(o.cu) || !aligned4(o.tok_seq) || !aligned4(o.entry_cu) ||
+      !aligned4(o.n_vis) || !aligned4(o.swa_len) || !aligned8(o.pos) || !aligned8(o.swa_slot) || !aligned8(o.entry_pos) ||
+      !aligned8(o.slot))
+    return CSA2_ERR_INVALID_ARG;
   if (batch > kMaxMapBatch || n_tokens > INT32_MAX || n_entries > INT32_MAX || cap > kMaxCacheRows / batch ||
       swa_rows > kMaxCacheRows / batch)
     return CSA2_ERR_UNSUPPORTED;
-  if (launch_slot_map(ctx_len, new_len, batch, m, cap, swa_rows, n_tokens, n_entries, cu, tok_seq, pos, swa_slot,
-                      entry_cu, entry_pos, slot, n_vis, swa_len, num_sms(),
+  if (launch_slot_map(ctx_len, new_len, batch, m, cap, swa_rows, n_tokens, n_entries, o, num_sms(),
                       reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return CSA2_ERR_CUDA;
   g_last_launches = 1;
@@ -901,7 +899,7 @@ extern "C" csa2_status csa2_tree_attn(const csa2_params *params, int32_t batch, 
       (W > 0 && (!swa || !swa_scale || swa_rows < W)))
     return CSA2_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(kv) || !aligned16(swa) || !aligned16(tree) ||
-      (reinterpret_cast<uintptr_t>(tree_mask) & 7u) || !aligned4(topk_idx) || !aligned4(swa_scale) ||
+      !aligned8(tree_mask) || !aligned4(topk_idx) || !aligned4(swa_scale) ||
       !aligned4(ctx_len) || !aligned4(tree_scale) || !aligned4(lse))
     return CSA2_ERR_INVALID_ARG;
   if (n_tree > kMaxExtraRows || (int64_t)batch * n_tree > kMaxStepTokens || swa_rows > kMaxCacheRows / batch ||

@@ -292,9 +292,8 @@ cudaError_t launch_indexer_k_read(const uint8_t *k_fp4, int64_t batch, int64_t c
 // kMaxMapBatch: each CTA keeps two prefix sums of them in shared memory).
 constexpr int kMaxMapBatch = 8192;
 cudaError_t launch_slot_map(const int32_t *ctx_len, const int32_t *new_len, int32_t batch, int32_t m, int64_t cap,
-                            int64_t ring, int64_t n_tokens, int64_t n_entries, int32_t *cu, int32_t *tok_seq,
-                            int64_t *pos, int64_t *swa_slot, int32_t *entry_cu, int64_t *entry_pos, int64_t *slot,
-                            int32_t *n_vis, int32_t *swa_len, int num_sms, cudaStream_t stream);
+                            int64_t ring, int64_t n_tokens, int64_t n_entries, const csa2_slot_maps &out, int num_sms,
+                            cudaStream_t stream);
 
 // Dense readout of seqs x n_q tokens over the first n_vis[b] (NULL: n_max)
 // entries of their sequence, merged with own_out / own_lse (fp32 rows and

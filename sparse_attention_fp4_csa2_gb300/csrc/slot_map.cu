@@ -23,11 +23,7 @@ constexpr int kMapThreads = 512;
 
 struct SlotArgs {
   const int32_t *ctx_len, *new_len;
-  int32_t *cu, *tok_seq;
-  int64_t *pos, *swa_slot;
-  int32_t *entry_cu;
-  int64_t *entry_pos, *slot;
-  int32_t *n_vis, *swa_len;
+  csa2_slot_maps out;
   int64_t cap, ring, n_tokens, n_entries;
   int32_t batch, m;
 };
@@ -106,10 +102,10 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
     t += n;
     e += (c + n) / a.m - c / a.m;
     if (first) {
-      a.cu[b] = tok[b];
-      a.entry_cu[b] = ent[b];
-      a.n_vis[b] = (int32_t)min(min((c + n) / a.m, a.cap), (int64_t)INT32_MAX);
-      a.swa_len[b] = (int32_t)min(min(c + n, a.ring), (int64_t)INT32_MAX);
+      a.out.cu[b] = tok[b];
+      a.out.entry_cu[b] = ent[b];
+      a.out.n_vis[b] = (int32_t)min(min((c + n) / a.m, a.cap), (int64_t)INT32_MAX);
+      a.out.swa_len[b] = (int32_t)min(min(c + n, a.ring), (int64_t)INT32_MAX);
       bad |= c0 < 0 || n0 < 0 || (c + n) / a.m > a.cap;
     }
   }
@@ -117,8 +113,8 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
     tok[a.batch] = (int32_t)min(tokens, (int64_t)INT32_MAX);
     ent[a.batch] = (int32_t)min(entries, (int64_t)INT32_MAX);
     if (first) {
-      a.cu[a.batch] = tok[a.batch];
-      a.entry_cu[a.batch] = ent[a.batch];
+      a.out.cu[a.batch] = tok[a.batch];
+      a.out.entry_cu[a.batch] = ent[a.batch];
       bad |= tokens > a.n_tokens || entries > a.n_entries;
     }
   }
@@ -137,9 +133,9 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
       if (tok[seq + 1] - tok[seq] - r <= a.ring)
         slot = (int64_t)seq * a.ring + (((uint64_t)pos | (uint64_t)a.ring) >> 32 ? pos % a.ring : (uint32_t)pos % (uint32_t)a.ring);
     }
-    a.tok_seq[i] = seq;
-    a.pos[i] = pos;
-    a.swa_slot[i] = slot;
+    a.out.tok_seq[i] = seq;
+    a.out.pos[i] = pos;
+    a.out.swa_slot[i] = slot;
   }
   for (int64_t i = i0; i < a.n_entries; i += stride) {
     int64_t pos = -1, slot = -1;
@@ -149,29 +145,20 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
       pos = e1 * a.m + a.m - 1;
       if (e1 < a.cap) slot = seq * a.cap + e1;
     }
-    a.entry_pos[i] = pos;
-    a.slot[i] = slot;
+    a.out.entry_pos[i] = pos;
+    a.out.slot[i] = slot;
   }
 }
 
 }  // namespace
 
 cudaError_t launch_slot_map(const int32_t *ctx_len, const int32_t *new_len, int32_t batch, int32_t m, int64_t cap,
-                            int64_t ring, int64_t n_tokens, int64_t n_entries, int32_t *cu, int32_t *tok_seq,
-                            int64_t *pos, int64_t *swa_slot, int32_t *entry_cu, int64_t *entry_pos, int64_t *slot,
-                            int32_t *n_vis, int32_t *swa_len, int num_sms, cudaStream_t stream) {
+                            int64_t ring, int64_t n_tokens, int64_t n_entries, const csa2_slot_maps &out, int num_sms,
+                            cudaStream_t stream) {
   SlotArgs a;
   a.ctx_len = ctx_len;
   a.new_len = new_len;
-  a.cu = cu;
-  a.tok_seq = tok_seq;
-  a.pos = pos;
-  a.swa_slot = swa_slot;
-  a.entry_cu = entry_cu;
-  a.entry_pos = entry_pos;
-  a.slot = slot;
-  a.n_vis = n_vis;
-  a.swa_len = swa_len;
+  a.out = out;
   a.cap = cap;
   a.ring = ring;
   a.n_tokens = n_tokens;

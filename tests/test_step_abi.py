@@ -30,8 +30,14 @@ OK, INVALID, UNSUPPORTED = 0, 1, 2
 def test_slot_map_refusals(c2, change, want):
     a = dict(batch=2, ctx=FAKE, new=FAKE, m=1, cap=100, ring=128, n=10, e=10, cu=FAKE, tok=FAKE, pos=FAKE, swa=FAKE,
              ecu=FAKE, epos=FAKE, slot=FAKE, vis=FAKE, len=FAKE) | change
-    assert c2.lib().csa2_slot_map(*a.values(), None) == want
+    v = list(a.values())
+    out = (ctypes.c_void_p * 9)(*v[8:])
+    assert c2.lib().csa2_slot_map(*v[:8], ctypes.addressof(out), None) == want
     assert c2.last_launch_count() == 0
+
+
+def test_slot_map_without_outputs(c2):
+    assert c2.lib().csa2_slot_map(2, FAKE, FAKE, 1, 100, 128, 10, 10, None, None) == INVALID
 
 
 @pytest.mark.parametrize("change,want", [
