@@ -23,6 +23,12 @@
 //   O = P V        P from tensor memory, V^T from the same slots (MN-major), in
 //                  pieces of 128, 64, 128, 64, 128 channels through two buffers;
 //   rows out       bf16 through shared memory and tensor copies.
+// What bounds it: HBM in a long run (2 x 8,192 tokens, window 128: 359 us, 6.0
+// TB/s, 0.90 of a plain copy's rate; a tile takes 12,000 clocks, of which HBM needs
+// 11,650), the latency of the fill and of a tile's chain in a short one (9 prompts
+// of 3,139 tokens, 22 a CTA: 89 us, 4.6 TB/s; 64 trees of five tokens 23 us): rows 10,000
+// clocks, S 3,000 to 5,000 (Q's arrival), softmax 3,500, the second product and the
+// rows out 7,500.
 // P is kept as two bf16 numbers, its rounding and the rest (16 bits together:
 // bf16 alone would cost 2^-9 of a weight, fp16 would need the rows and the
 // queries in fp16 too).  The reference maximum is over logit + log2(s_k), so that
