@@ -489,7 +489,8 @@ csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *
  *   out       bf16 [n_tokens][64][512] (out), 16-byte aligned; lse fp32
  *             [n_tokens][64] or NULL (out).  A token that sees nothing gives out =
  *             0 and lse = -inf; rows from cu[batch] on are left as they were.
- * Rows no token sees are not read, whatever they hold.  A negative ctx_len (taken
+ * Rows no token sees count for nothing, whatever they hold.  The result is
+ * undefined if cu or ctx_len changes while the call runs.  A negative ctx_len (taken
  * as 0) or a ring too short for the step sets CSA2_DEV_ERR_INDEX.  params.attn_kernel
  * as csa2_params says.  batch == 0 or n_tokens == 0 is a no-op.
  */
@@ -520,7 +521,8 @@ csa2_status csa2_window_attn(const csa2_params *params, int32_t batch, int64_t n
  *   out       bf16 [batch][n_tree][64][512] (out), 16-byte aligned; lse fp32
  *             [batch][n_tree][64] or NULL (out).  A token that sees nothing gives
  *             out = 0 and lse = -inf.
- * A negative ctx_len (taken as 0) or an index outside the cache sets
+ * The result is undefined if ctx_len or tree_mask changes while the call runs.  A
+ * negative ctx_len (taken as 0) or an index outside the cache sets
  * CSA2_DEV_ERR_INDEX.  batch == 0 or n_tree == 0 is a no-op.
  */
 csa2_status csa2_tree_attn(const csa2_params *params, int32_t batch, int32_t n_tree, const void *q, const uint8_t *kv,

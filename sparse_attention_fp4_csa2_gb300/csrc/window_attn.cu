@@ -75,7 +75,6 @@ static_assert(kSmemW <= 232448, "window attention exceeds the shared-memory limi
 
 struct WindowArgs {
   StepRows s;
-  const __nv_bfloat16 *q;
   const uint8_t *swa;
   const float *swa_scale;
   float *lse;
@@ -750,7 +749,6 @@ cudaError_t launch_window_attn(const void *q, const uint8_t *swa, const float *s
                                float *lse, int num_sms, cudaStream_t stream, int *launches) {
   WindowArgs a;
   a.s = s;
-  a.q = static_cast<const __nv_bfloat16 *>(q);
   a.swa = swa;
   a.swa_scale = swa_scale;
   a.lse = lse;

@@ -10,7 +10,6 @@ One key alone is off by 2^-11 of itself, below the same bound.  The output's own
 rounding to bf16 adds 2^-8 of each value.  The log-sum-exp is fp32 over fp32
 logits: 2e-5 of it (or of 1).
 """
-import ctypes
 import math
 
 import pytest
