@@ -243,15 +243,16 @@ __device__ __forceinline__ void load_key(const AttnArgs &a, const Keys &k, int e
   d.kind = 2;
 }
 
-// Q in place from bf16 to fp16.
+// Q in place from bf16 to fp16, by kThreads threads.
+template <int kThreads>
 __device__ __forceinline__ void convert_q(uint8_t *qs, int t) {
   uint4 *q = reinterpret_cast<uint4 *>(qs) + t;
   constexpr int kAtOnce = 8;   // loads before the first store
 #pragma unroll 1
-  for (int i = 0; i < H * D * 2 / 16; i += kAtOnce * kRowG * 32) {
+  for (int i = 0; i < H * D * 2 / 16; i += kAtOnce * kThreads) {
     uint4 v[kAtOnce];
 #pragma unroll
-    for (int u = 0; u < kAtOnce; ++u) v[u] = q[i + u * kRowG * 32];
+    for (int u = 0; u < kAtOnce; ++u) v[u] = q[i + u * kThreads];
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       const uint32_t x[4] = {v[u].x, v[u].y, v[u].z, v[u].w};
@@ -261,7 +262,7 @@ __device__ __forceinline__ void convert_q(uint8_t *qs, int t) {
         const __half2 f = __floats2half2_rn(__uint_as_float(x[j] << 16), __uint_as_float(x[j] & 0xFFFF0000u));
         h[j] = *reinterpret_cast<const uint32_t *>(&f);
       }
-      q[i + u * kRowG * 32] = make_uint4(h[0], h[1], h[2], h[3]);
+      q[i + u * kThreads] = make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
   fence_proxy_async_smem();
@@ -330,20 +331,25 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
     __syncwarp();
     if (lane == 0) mbar_arrive(&S.rows_full[b]);
     load();
-    if (first) {   // the token's Q, which lands about now
-      wait_g(S, &S.q_raw, n & 1);
+    if (first) {   // the token's Q, which lands about now (the first token's is the softmax warps')
+      if (n) {
+        wait_g(S, &S.q_raw, n & 1);
+        convert_q<kRowG * 32>(qs, w * 32 + lane);
+        if (lane == 0) mbar_arrive(&S.q_ready);
+      }
       ++n;
-      convert_q(qs, w * 32 + lane);
-      if (lane == 0) mbar_arrive(&S.q_ready);
     }
   }
 }
 
 // ---------------------------------------------------------------- softmax
-__device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *ps, uint32_t tmem, int w, int lane) {
+__device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t *ps, uint32_t tmem, int w, int lane) {
   const uint32_t lanes = tmem + ((uint32_t)(32 * w) << 16);
   const int th = lane >> 4, h = 16 * w + (lane & 15);
   uint32_t g = 0;
+  wait_g(S, &S.q_raw, 0);
+  convert_q<kSoftG * 32>(qs, w * 32 + lane);
+  if (lane < kRowG / kSoftG) mbar_arrive(&S.q_ready);
   Tokens tokens;
   tokens.start(a);
   int64_t token;
@@ -502,18 +508,20 @@ __device__ __forceinline__ void load_q_g(CtlG &S, const CUtensorMap &tm_q, uint8
 // (both by whole warps, an elected thread issuing)
 __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q, uint8_t *slots, uint8_t *qs, uint32_t tmem) {
   const uint64_t qd = smem_desc(smem_u32(qs), 16, 1024), kd = smem_desc(smem_u32(slots), 16, 1024);
-  uint32_t g = 0, n = 0, copies = 0;
+  uint32_t g = 0, n = 0, copies = 1;
   Tokens tokens;
   tokens.start(a);
   int64_t token;
   for (int steps; tokens.take(a, token, steps);) {
-    // Q's last reader was the token before's last S
-    if (n) wait_g(S, &S.q_free, (n - 1) & 1);
-    if (!S.abort) {
-      if (elect_one()) load_q_g(S, tm_q, qs, token);
-      ++copies;
+    // (the first token's Q is on its way; a later one's last reader was the token before's last S)
+    if (n) {
+      wait_g(S, &S.q_free, (n - 1) & 1);
+      if (!__any_sync(0xffffffffu, S.abort != 0)) {
+        if (elect_one()) load_q_g(S, tm_q, qs, token);
+        ++copies;
+      }
+      __syncwarp();
     }
-    __syncwarp();
     wait_g(S, &S.q_ready, n & 1);
     ++n;
 #pragma unroll 1
@@ -541,8 +549,9 @@ __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q
     }
   }
   if (n) wait_g(S, &S.q_free, (n - 1) & 1);
-  // a copy still in flight lands before the CTA's memory goes, also after a wait ran out
-  if (copies) mbar_wait(&S.q_raw, (copies - 1) & 1);
+  // a copy still in flight lands before the CTA's memory goes, also after a wait ran
+  // out or when the CTA's first token is behind the last sequence
+  mbar_wait(&S.q_raw, (copies - 1) & 1);
 }
 
 __device__ void value_warp_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t *ps, uint32_t tmem) {
@@ -587,7 +596,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   uint8_t *slots = base, *qs = slots + 2 * kSlotG, *ps = qs + H * D * 2;
   CtlG &S = *reinterpret_cast<CtlG *>(ps + 2 * kBlockG);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
+  if (warp == kScoreWarpG && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&S.rows_full[i], kRowG);
       mbar_init(&S.slot_free[i], 1);
@@ -603,7 +612,10 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     fence_barrier_init();
     prefetch_tmap(&tm_q);
   }
+  __syncwarp();
   pdl_enter();
+  if (warp == kScoreWarpG && lane == 0) load_q_g(S, tm_q, qs, blockIdx.x);   // before its keys are known
+  __syncwarp();
   if (warp == kValueWarpG) {
     tmem_alloc(&S.tmem_base, 512);
     tmem_relinquish();
@@ -613,7 +625,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
   tc_fence_after();
   const uint32_t tmem = S.tmem_base;
   if (warp < kSoftG)
-    softmax_warps_g(a, S, ps, tmem, warp, lane);
+    softmax_warps_g(a, S, qs, ps, tmem, warp, lane);
   else if (warp < kScoreWarpG)
     row_warps_g(a, S, slots, qs, warp - kSoftG, lane);
   else if (warp == kScoreWarpG)

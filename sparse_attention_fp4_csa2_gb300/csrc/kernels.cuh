@@ -246,17 +246,17 @@ struct AttnArgs {
 __device__ __forceinline__ bool find_sequence(const int32_t *cu, int32_t batch, int64_t i, int &b) {
   const int lane = threadIdx.x & 31;
   int lo = 0, n = batch;   // the answer is one of lo .. lo + n - 1
-  if (i >= cu[batch]) return false;
-  while (n > 1) {
+  const int32_t end = cu[batch];   // (loaded beside the first probes)
+  do {
     const int step = (n + 31) >> 5;
-    const int at = lo + lane * step;
-    const uint32_t le = __ballot_sync(0xffffffffu, lane * step < n && cu[at] <= i);
+    const bool in = lane * step < n;
+    const uint32_t le = __ballot_sync(0xffffffffu, (in ? cu[lo + lane * step] : INT32_MAX) <= i && in);
     const int k = le ? 31 - __clz(le) : 0;
     lo += k * step;
     n = min(step, n - k * step);
-  }
+  } while (n > 1);
   b = lo;
-  return true;
+  return i < end;
 }
 
 // Workspace of one readout launch (the chunk partials when tokens are split).
