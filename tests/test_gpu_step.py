@@ -282,6 +282,24 @@ def test_window_rows_of_any_size(c2, std, new):
         w.check()
 
 
+@pytest.mark.parametrize("sharp", [30.0, 120.0])
+def test_logits_that_tower(c2, sharp):
+    """Logits of a spread of up to 170 powers of two, whose running reference is
+    raised again and again: windows, trees with and without entries.  (A logit x is
+    off by some 2^-20 of it, so a weight by 1e-4 at most, far below 2^-9.)"""
+    for kernel in (0, 1, 2):
+        w = Window([300, 20, 0], [90, 150, 64], 128, 4, seed=12, sharp=sharp)
+        w.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        w.check()
+        for K in (0, 300):
+            t = Tree(c2, 40, 8, K, 128, [9 * i for i in range(40)], cap=310, seed=13)
+            t.q = queries((40, 8), 14, sharp)
+            t.call(c2, kernel)
+            assert c2.get_device_status() == 0
+            t.check()
+
+
 def test_window_without_lse_and_scales_of_zero(c2):
     w = Window([300], [64], 128, 4, seed=6)
     w.call(c2, lse=False)
