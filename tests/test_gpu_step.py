@@ -300,6 +300,30 @@ def test_logits_that_tower(c2, sharp):
             t.check()
 
 
+def test_logits_past_two_to_the_29(c2):
+    """Queries near fp16's end and rows of 2,000: each head's logit for one key, or
+    for two equal ones, is about 2.7e9, the others' far below, and the output is that
+    key."""
+    sign = torch.where(torch.rand(D, generator=gen(90), device="cuda") < 0.5, -1.0, 1.0)
+    tall = (sign * 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for kernel in (0, 1, 2):
+        w = Window([400, 10], [100, 80], 128, 4, seed=91, std=20.0)
+        w.q = (sign * 60000).bfloat16().expand(180, H, D).contiguous()
+        for b, rows in ((0, (350, 420, 421)), (1, (0, 40))):
+            r = torch.tensor(rows, device="cuda") % w.swa.shape[1]
+            w.swa[b, r], w.scale[b, r] = tall, 2000.0 / 448
+        w.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        w.check()
+        t = Tree(c2, 30, 6, 64, 128, [500 + i for i in range(30)], cap=80, seed=92, std=20.0, empty=False)
+        t.q = (sign * 60000).bfloat16().expand(30, 6, H, D).contiguous()
+        t.swa[:, 7], t.scale[:, 7] = tall, 2000.0 / 448
+        t.tree[:, 2], t.tree_scale[:, 2] = tall, 2000.0 / 448
+        t.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        t.check()
+
+
 def test_window_without_lse_and_scales_of_zero(c2):
     w = Window([300], [64], 128, 4, seed=6)
     w.call(c2, lse=False)
