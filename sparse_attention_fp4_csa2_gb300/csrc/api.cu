@@ -828,20 +828,21 @@ csa2_status run_step(const csa2_params *p, int64_t tokens, const void *q, const 
   a.step = s;
   int launches = 0;
   // A token's keys over a cluster while four CTAs or more a token fit and it has more
-  // keys than four steps of a CTA (5 tokens, 512 + 128 keys: 15.3 us against 23.9 in
-  // one CTA each, 20 tokens 21.8 against 24.2, 40 in pairs 28.5 against 25.5; 5 tokens
-  // with 256 + 128 14.4 against 16.8, with 37 + 128 14.4 against 11.7).
+  // keys than four steps of a CTA (5 tokens, 512 + 128 keys: 15.4 us against 23.4 in
+  // one CTA each, 20 tokens 21.8 against 24.1, 40 in pairs 28.5 against 25.2; 5 tokens
+  // with 256 + 128 14.5 against 16.7, with 37 + 128 14.4 against 11.3).
   // Tiles of two tokens that share their rows, where these are all a token has, fit,
   // and there are tokens enough to share them (packed tokens, windows of 128: 152 of
-  // one sequence 20.3 us against 14.6 in a CTA each, 300 22.4 against 23.1, 1,200 44
-  // against 72; one each of 608 sequences 69 against 45, two each of 304 40 against
-  // 43.  Trees: 64 x 5 27.7 against 27.2, 128 x 5 35 against 42, 300 x 2 40 against 36).
+  // one sequence 18.2 us against 14.4 in a CTA each, 200 18.6 against 22.1, 1,200 38
+  // against 72; one each of 608 sequences 61 against 43, two each of 152 21.4 against
+  // 24.1.  Trees: 30 x 5 18.0 against 13.0, 36 x 5 18.2 against 18.8, 128 x 5 30 against
+  // 40; 200 x 3 42 against 34, 300 x 2 35 and 35).
   // Else a CTA for each token.
   const int sms = num_sms();
   const int64_t keys = (int64_t)a.K + (s.cu ? s.win + s.extras : s.win > s.extras ? s.win : s.extras);
   const bool split = p->attn_kernel == 1 || (p->attn_kernel == 0 && 4 * tokens <= sms && keys > 256);
   const bool shared = p->attn_kernel == 0 && !topk_idx && window_rows_fit(s) &&
-                      (s.cu ? tokens > sms && tokens >= 2 * (int64_t)s.batch : tokens > 2 * sms && s.extras >= 3);
+                      tokens > sms && (s.cu ? tokens >= 2 * (int64_t)s.batch : s.extras >= 4);
   const cudaError_t e = split    ? launch_sparse_attn(a, nullptr, stream, &launches)
                         : shared ? launch_window_attn(q, swa, swa_scale, s, tokens, lse, sms, stream, &launches)
                                  : launch_gather_attn(a, sms, stream, &launches);

@@ -115,7 +115,6 @@ struct StepScale {
 };
 constexpr int kMaxBkStep = 144;
 constexpr uint32_t kStepScaleOff = kRedOffMulti + 2 * H * 4;
-constexpr float kTinyScale = 5.421010862427522e-20f;   // 2^-64
 static_assert(kStepScaleOff >= kMaxBkStep * D * 2 && kStepScaleOff + sizeof(StepScale) <= kTileRegion &&
               kStepScaleOff % 16 == 0, "the step form's scales overlap the tile");
 

@@ -25,10 +25,10 @@
 //            from the same slot; its end frees the slot;
 //   rows out O^T through shared memory, as bf16, while the next
 //            token's first steps are converted and multiplied.
-// Measured: 2,048 tokens of 512 + 128 keys 303 us, 41,500 wavefronts and some 42,000
+// Measured: 2,048 tokens of 512 + 128 keys 302 us, 41,500 wavefronts and some 42,000
 // clocks a token, ten steps of 3,300 and 8,000 between tokens (Q's reload and
-// conversion, beside them the rows out); 256 tokens 51 us, two rounds; 93 tokens of
-// up to 168 keys 11.3.  Both products issued by one thread, a tile of 128 keys and
+// conversion, beside them the rows out); 256 tokens 49.6 us, two rounds; 93 tokens of
+// up to 168 keys 11.1.  Both products issued by one thread, a tile of 128 keys and
 // softmax on the rows' warps, as in the sparse readout: 637 us for the 2,048.
 // Keys that the token does not see take no place: the list (whose -1 are masked),
 // the window's visible rows, then the named extra rows.  (The list first: entries
@@ -53,7 +53,6 @@ constexpr uint32_t kColOG = 256;             // tensor memory: S at 128 slot + 6
 constexpr float kLogitG = 0.06375871295460785f;   // log2(e) / sqrt(512)
 constexpr float kLn2G = 0.69314718055994531f;
 constexpr float kLazyG = 8.0f;               // log2 margin before the reference is raised
-constexpr float kTinyScaleG = 5.421010862427522e-20f;   // 2^-64: rows of a smaller scale count as zeros
 constexpr uint32_t kIdescSG = idesc_f16(0, 0, 0, kStep, H);
 constexpr uint32_t kIdescOG = idesc_f16(0, /*A MN-major*/ 1, 0, H, 128);
 
@@ -310,7 +309,7 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
     const bool first = s == 0;
     if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
     if (block == 0) {
-      const float f = d.scale < kTinyScaleG ? kTinyScaleG : d.scale;
+      const float f = d.scale < kTinyScale ? kTinyScale : d.scale;
       S.rs[b][key] = kLogitG * f;
       S.lg[b][key] = d.kind ? log2f(f) : -INFINITY;
       S.inv[b][key] = d.kind ? 1.0f / f : 1.0f;
@@ -321,7 +320,7 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
       if (d.kind == 1) {
         put_entry(at, d.v[h], d.sc[h]);
       } else if (d.kind == 2) {
-        put_codes(at, d.v[h], d.scale < kTinyScaleG ? 0u : 0x3C003C00u);
+        put_codes(at, d.v[h], d.scale < kTinyScale ? 0u : 0x3C003C00u);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) st_chunk(at, i, 0, 0, 0, 0);

@@ -14,7 +14,7 @@
 // memory and takes every gridDim-th stretch of the tokens and entries, finding a
 // token's sequence by binary search there.  Measured in graphs: 32 sequences of one
 // token 2.9 us, 999 of five 4.7, 196,000 tokens and 98,000 entries of 64 sequences
-// 4.7 (1.2 TB/s); a call from Python takes 6.5.
+// 4.7 (1.2 TB/s); a call from Python takes 5.6.
 #include "kernels.cuh"
 
 namespace csa2 {

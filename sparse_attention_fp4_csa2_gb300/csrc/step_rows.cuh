@@ -4,6 +4,9 @@
 
 namespace csa2 {
 
+// 8-bit rows of a smaller scale count as zeros (2^-64).
+constexpr float kTinyScale = 5.421010862427522e-20f;
+
 // Of token gp: its sequence, the positions that its window may hold, end - left ..
 // end - 1 (those below 0 hold no key), and its extra rows, a bit each.  False for
 // a packed token behind the last sequence.  Called by whole warps.  Nothing read

@@ -38,7 +38,7 @@
 // Warps: 0-7 softmax, 8-15 output, 16 rows, 17 copies of Q, 18 first product, 19
 // second product.  Every wait is bounded; after one runs out every role falls
 // through its waits and the output is undefined (CSA2_DEV_ERR_TIMEOUT).
-#include "kernels.cuh"
+#include "step_rows.cuh"
 
 namespace csa2 {
 
@@ -58,7 +58,6 @@ constexpr uint32_t kColL = 480;                  // 1 / row sum, a column per S 
 constexpr uint32_t kColX = 482;                  // what a row's two softmax threads tell each other: [half] maximum, reference, sum
 constexpr float kLogitW = 0.06375871295460785f;  // log2(e) / sqrt(512)
 constexpr float kLn2W = 0.69314718055994531f;
-constexpr float kTinyScaleW = 5.421010862427522e-20f;   // 2^-64: rows of a smaller scale count as zeros
 
 struct __align__(16) CtlW {
   uint64_t q_full[kQRing], q_free[kQRing];
@@ -213,7 +212,7 @@ __device__ __forceinline__ bool put_row(uint8_t *at, uint32_t half, int slot, co
 
 // What the softmax has to know of a slot (one thread).
 __device__ __forceinline__ void slot_scale(CtlW &S, int slot, float scale, bool bad) {
-  const float f = scale < kTinyScaleW ? kTinyScaleW : scale;
+  const float f = scale < kTinyScale ? kTinyScale : scale;
   S.rs[slot] = kLogitW * f;
   S.lg[slot] = bad ? __int_as_float(0x7FFFFFFF) : log2f(f);
   S.inv[slot] = f <= 3.0e38f ? 1.0f / f : 1.0f;   // finite: it multiplies the weights of masked slots (0) too
@@ -295,7 +294,7 @@ __device__ void fill_slots(const WindowArgs &a, CtlW &S, uint8_t *tile, const Ti
   }
   uint4 v[kBatch];
   get_rows(v, row, lane);
-  const uint32_t tiny = __ballot_sync(0xffffffffu, scale < kTinyScaleW);
+  const uint32_t tiny = __ballot_sync(0xffffffffu, scale < kTinyScale);
   if (i > 0) wait_w(S, &S.pv_done[(i - 1) & 1], ((i - 1) >> 1) & 1);
   uint32_t bad = 0;
   const uint32_t half = 4 * a.slots * 128;
@@ -333,7 +332,7 @@ __device__ void row_warp(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<kTree
         if (filling) wait_w(S, &S.fresh_full, (fresh - 1) & 1);
         filling = false;
         if (s.win > 0) {
-          const uint32_t tiny = __ballot_sync(0xffffffffu, scale < kTinyScaleW);
+          const uint32_t tiny = __ballot_sync(0xffffffffu, scale < kTinyScale);
           const int slot = (int)(t.pos % a.ring), second = slot + 1 == a.ring ? 0 : slot + 1;
           uint8_t *at = tile + (lane >> 3) * a.slots * 128;
           bool bad = put_row(at, 4 * a.slots * 128, slot, ahead[0], tiny & 1, lane);
