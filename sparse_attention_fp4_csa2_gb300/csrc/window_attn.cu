@@ -370,7 +370,7 @@ struct Seen {
     const StepRows &s = a.s;
     if constexpr (kTree) {
       const int64_t ctx = max(s.ctx_len[t.seq], 0);
-      extra = s.mask[t.tok + j] & (s.extras >= 64 ? ~0ull : (1ull << s.extras) - 1);
+      extra = s.mask[t.tok + j] & low_bits(s.extras);
       len = (int)min((int64_t)max(s.win - __popcll(extra), 0), ctx);
       held = s.win;
       at = held - len;
@@ -379,7 +379,7 @@ struct Seen {
       len = (int)(p - first) + 1;
       held = a.ring;
       at = (int)(first % a.ring);
-      extra = (1ull << (before < s.extras ? (before > 0 ? before : 0) : s.extras)) - 1;   // (fewer than 64 fit behind the window)
+      extra = low_bits((int)(before < s.extras ? (before > 0 ? before : 0) : s.extras));
     }
   }
   // slots 16 c .. + 15, a bit each, by whole warps

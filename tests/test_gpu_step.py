@@ -266,6 +266,16 @@ def test_window(c2, case, kernel):
     w.check()
 
 
+@pytest.mark.parametrize("W,S", [(0, 64), (1, 63), (1, 64), (77, 64), (78, 64)])
+def test_window_as_many_sinks_as_there_can_be(c2, W, S):
+    """The most sinks behind windows that leave them room in a tile, and one row more."""
+    w = Window([0, 70], [150, 60], W, S, seed=21)
+    for kernel in (0, 1, 2):
+        w.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        w.check()
+
+
 @pytest.mark.parametrize("std", [1e-15, 1e-12, 1e-5, 1e3, 1e12])
 @pytest.mark.parametrize("new", [1, 150])
 def test_window_rows_of_any_size(c2, std, new):
