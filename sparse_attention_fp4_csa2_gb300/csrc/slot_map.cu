@@ -173,7 +173,9 @@ cudaError_t launch_slot_map(const int32_t *ctx_len, const int32_t *new_len, int3
   ctas = ctas < 1 ? 1 : ctas < num_sms ? ctas : num_sms;
   const size_t smem = ((size_t)3 * batch + 2) * sizeof(int32_t);
   if (smem > 48 * 1024) {   // (less needs no attribute)
-    const cudaError_t e = cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the largest batch's, so that a call of another thread's never lowers it
+    const cudaError_t e = cudaFuncSetAttribute(slot_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)((3 * kMaxMapBatch + 2) * sizeof(int32_t)));
     if (e != cudaSuccess) return e;
   }
   return launch_pdl(slot_map_kernel, dim3((unsigned)ctas), dim3(kMapThreads), smem, stream, 0u, a);

@@ -11,6 +11,7 @@ rounding to bf16 adds 2^-8 of each value.  The log-sum-exp is fp32 over fp32
 logits: 2e-5 of it (or of 1).
 """
 import math
+import threading
 
 import pytest
 import torch
@@ -186,6 +187,32 @@ def test_slot_map_graph_and_stream(c2):
     c2.slot_map(ctx, new, 100, 128, other, stream=s)
     s.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(maps, other))
+
+
+def test_slot_map_from_two_threads(c2):
+    """Calls of two sizes that both need more shared memory than a kernel has by default."""
+    sizes, failed = (8192, 4200), []
+
+    def calls(batch, maps, ctx, new, stream):
+        try:
+            for _ in range(500):
+                c2.slot_map(ctx, new, 100, 128, maps, stream=stream)
+        except c2.Csa2Error as e:
+            failed.append(e)
+
+    given = [(b, c2.slot_maps(b, b), ints(range(b)), ints([1] * b), torch.cuda.Stream()) for b in sizes]
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=calls, args=a) for a in given]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    c2.get_device_status()   # (most of the entries lie past the cap of 100)
+    for b, maps, *_ in given:
+        for got, ref in zip(maps, map64(list(range(b)), [1] * b, 100, 128, b, b, 1)):
+            assert got.tolist() == ref
 
 
 # ------------------------------------------------------------------ window
