@@ -457,7 +457,8 @@ typedef struct {
  *             entries past the outputs' lengths are dropped.
  *   maps      the outputs (out; the struct itself is read by the call)
  * A negative length (taken as 0), dropped tokens or entries, and a sequence past
- * its cap set CSA2_DEV_ERR_NVIS.  batch above 8192 is CSA2_ERR_UNSUPPORTED.
+ * its cap set CSA2_DEV_ERR_NVIS.  batch above 8192 and lengths of the outputs past
+ * 2^31 - 1 are CSA2_ERR_UNSUPPORTED.
  * batch == 0 is a no-op.
  */
 csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *new_len, int32_t m, int64_t cap,
@@ -485,7 +486,8 @@ csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *
  *             + cu[b + 1] - cu[b] <= swa_rows (checked on device); swa_rows >= W
  *   sink      uint8 E4M3 [batch][n_sink][512], 16-byte aligned; sink_scale fp32
  *             [batch][n_sink]; row s holds position s; NULL when n_sink is 0
- *   n_sink    0..64
+ *   n_sink    0..64 (above that, and batch or n_tokens above 2^24,
+ *             CSA2_ERR_UNSUPPORTED)
  *   out       bf16 [n_tokens][64][512] (out), 16-byte aligned; lse fp32
  *             [n_tokens][64] or NULL (out).  A token that sees nothing gives out =
  *             0 and lse = -inf; rows from cu[batch] on are left as they were.
@@ -517,7 +519,8 @@ csa2_status csa2_window_attn(const csa2_params *params, int32_t batch, int64_t n
  *             [batch][n_tree]: the drafted tokens' rows (csa2_swa_quant_write)
  *   tree_mask int64 [batch][n_tree]: bit u of a token's mask names drafted token
  *             u; bits from n_tree on are ignored
- *   n_tree    up to 64 (above that CSA2_ERR_UNSUPPORTED)
+ *   n_tree    up to 64 (above that, and batch * n_tree above 2^24,
+ *             CSA2_ERR_UNSUPPORTED)
  *   out       bf16 [batch][n_tree][64][512] (out), 16-byte aligned; lse fp32
  *             [batch][n_tree][64] or NULL (out).  A token that sees nothing gives
  *             out = 0 and lse = -inf.

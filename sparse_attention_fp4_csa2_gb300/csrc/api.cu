@@ -851,7 +851,7 @@ csa2_status run_step(const csa2_params *p, int64_t tokens, const void *q, const 
   return CSA2_OK;
 }
 
-constexpr int64_t kMaxStepTokens = (int64_t)1 << 24;   // query tokens of a step
+constexpr int64_t kMaxStepTokens = (int64_t)1 << 24;   // query tokens, and sequences, of a step
 constexpr int32_t kMaxExtraRows = 64;                  // sinks of a sequence, drafted tokens of a tree
 
 }  // namespace
@@ -872,7 +872,8 @@ extern "C" csa2_status csa2_window_attn(const csa2_params *params, int32_t batch
   if (!aligned16(q) || !aligned16(out) || !aligned16(swa) || !aligned16(sink) || !aligned4(cu) || !aligned4(ctx_len) ||
       !aligned4(swa_scale) || !aligned4(sink_scale) || !aligned4(lse))
     return CSA2_ERR_INVALID_ARG;
-  if (n_tokens > kMaxStepTokens || n_sink > kMaxExtraRows || swa_rows > kMaxCacheRows / batch) return CSA2_ERR_UNSUPPORTED;
+  if (n_tokens > kMaxStepTokens || batch > kMaxStepTokens || n_sink > kMaxExtraRows || swa_rows > kMaxCacheRows / batch)
+    return CSA2_ERR_UNSUPPORTED;
   StepRows s = {};
   s.cu = cu;
   s.ctx_len = ctx_len;

@@ -46,7 +46,8 @@ def test_slot_map_without_outputs(c2):
     (dict(ctx=None), INVALID), (dict(swa=None), INVALID), (dict(swa=ODD), INVALID), (dict(scale=None), INVALID),
     (dict(sink=None), INVALID), (dict(sink=ODD), INVALID), (dict(sink_scale=None), INVALID), (dict(out=None), INVALID),
     (dict(out=ODD), INVALID), (dict(cu=0x1002), INVALID), (dict(scale=0x1002), INVALID), (dict(lse=0x1002), INVALID),
-    (dict(n=1 << 25), UNSUPPORTED), (dict(ns=65), UNSUPPORTED), (dict(rows=1 << 40), UNSUPPORTED),
+    (dict(n=1 << 25), UNSUPPORTED), (dict(batch=(1 << 24) + 1), UNSUPPORTED),
+    (dict(batch=2 ** 31 - 1, params=dict(sliding_window=0), swa=None, scale=None, rows=0), UNSUPPORTED), (dict(ns=65), UNSUPPORTED), (dict(rows=1 << 40), UNSUPPORTED),
     (dict(params=dict(sliding_window=2000)), UNSUPPORTED), (dict(params=dict(attn_kernel=3)), UNSUPPORTED),
     (dict(batch=0, q=None, out=None), OK), (dict(n=0, q=None, out=None), OK)])
 def test_window_refusals(c2, change, want):
