@@ -510,8 +510,9 @@ csa2_status csa2_window_attn(const csa2_params *params, int32_t batch, int64_t n
  * ends with the token itself).
  *   q         bf16 [batch][n_tree][64][512], as csa2_window_attn
  *   kv        uint8 [batch][cap][288], 16-byte aligned; topk_idx int32
- *             [batch][n_tree][index_topk], entries in [-1, cap); topk_idx NULL: no
- *             entries (a window-only layer; kv may be NULL)
+ *             [batch][n_tree][index_topk], entries in [-1, cap), each a key as
+ *             often as it is named; topk_idx NULL: no entries (a window-only
+ *             layer; kv may be NULL)
  *   swa       the sequences' rings, as csa2_window_attn, rows of the committed
  *             positions; swa_rows >= W
  *   ctx_len   int32 [batch]: committed tokens

@@ -570,6 +570,42 @@ def test_rows_aligned_to_16_bytes_only(c2):
         w.check()
 
 
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+def test_tree_an_index_twice(c2, kernel):
+    """An entry that a list names twice is two keys."""
+    t = Tree(c2, 3, 5, 300, 64, [300, 20, 0], cap=301, seed=51)
+    t.idx[:, :, 150:170] = t.idx[:, :, 7:8]
+    t.idx[1, 4] = 3
+    t.call(c2, kernel)
+    assert c2.get_device_status() == 0
+    t.check()
+
+
+def test_two_streams_at_once(c2):
+    """Each kernel beside another one on a stream of its own gives what it gives alone."""
+    cases = [Window([300, 20], [700, 500], 128, 4, seed=52), Tree(c2, 40, 8, 200, 128, [9 * i for i in range(40)], cap=210, seed=53),
+             Tree(c2, 1, 5, 512, 128, [900], cap=600, seed=54), Tree(c2, 64, 5, 0, 128, [9 * i for i in range(64)], seed=55)]
+    ctx = [None] + [ints(t.ctx) for t in cases[1:]]
+    calls = [lambda **kw: cases[0].call(c2, **kw)] + [
+        (lambda t, c: lambda **kw: t.call(c2, ctx_t=c, **kw))(t, c) for t, c in zip(cases[1:], ctx[1:])]
+    for call in calls:
+        call()
+    torch.cuda.synchronize()
+    alone = [(t.out.clone(), t.lse.clone()) for t in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    for t in cases:
+        t.out.zero_()
+        t.lse.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, s in zip(calls, streams):
+            call(stream=s)
+    torch.cuda.synchronize()
+    assert c2.get_device_status() == 0
+    for t, (out, lse) in zip(cases, alone):
+        assert torch.equal(t.out, out) and torch.equal(t.lse, lse)
+
+
 def test_tree_bad_indices(c2):
     """An index past the cache, a length below zero: reported, no access; the tokens without them are right."""
     t = Tree(c2, 2, 4, 16, 128, [300, 20], cap=64, seed=36, empty=False)
