@@ -937,15 +937,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       // P = 2^(logit - m_ref) (x the SWA row scale) into P^T; the row sum
       // gathers the unscaled exponents.  `over` flags a logit above
-      // m_ref + kLazy (the one-pass attempt below).
-      auto store_p = [&](int mi, const float (&x)[16], float mref_s) {
+      // `top` (the one-pass attempt below).
+      auto store_p = [&](int mi, const float (&x)[16], float mref_s, float top) {
         bool over = false;
         const int k0 = 16 * (2 * (2 * mi + wh) + th);
         uint32_t pk[8];
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
           // masked keys hold -inf: 2^-inf = 0 (no branch); m_ref = -inf only when all are masked
-          over |= (x[i] > mref_s + kLazy) | (x[i + 1] > mref_s + kLazy);
+          over |= (x[i] > top) | (x[i + 1] > top);
           const float p0 = ex2_approx(x[i] - mref_s), p1 = ex2_approx(x[i + 1] - mref_s);
           if constexpr (kStep) {
             const float2 r2 = *reinterpret_cast<const float2 *>(scales.inv + (k0 < a.Bk ? k0 + i : 0));
@@ -967,21 +967,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         return over;
       };
-      auto write_p = [&](float mref_s) {
+      auto write_p = [&](float mref_s, float top) {
         bool over = false;
 #pragma unroll 1
         for (int mi = 0; mi < kPairs; ++mi) {
           float x[16];
           logits(mi, x);
-          over |= store_p(mi, x, mref_s);
+          over |= store_p(mi, x, mref_s, top);
         }
         return over;
       };
       // After an item's first block the reference max is rarely raised: one
       // pass writes P with the current reference, and only if some logit is
       // above it by more than 2^kLazy (any thread) is the block redone by the
-      // two passes below (max, then exponents).  Whether a reference exists
-      // is the same for every head (it depends on which keys were valid).
+      // two passes below (max, then exponents).  Every thread takes the same
+      // way, whatever its logits are: the barriers count on all of them (a
+      // head of nothing but NaNs has no reference where the others have one;
+      // without one any key is above it).
       bool done_p = false;
       if constexpr (kSingle) {
         // one block (nothing accumulated yet): every logit of this thread
@@ -1008,12 +1010,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         m_ref = fmaxf(red[0][h], red[1][h]);
         const float ms = m_ref == -INFINITY ? 0.0f : m_ref;
 #pragma unroll
-        for (int mi = 0; mi < kPairs; ++mi) (void)store_p(mi, x[mi], ms);
+        for (int mi = 0; mi < kPairs; ++mi) (void)store_p(mi, x[mi], ms, INFINITY);
         done_p = true;
       } else {
-        if (m_ref != -INFINITY) {
+        if (j > 0) {
           const float l_save = l_part, l2_save = l2_part;
-          const bool over = write_p(m_ref);
+          const bool over = write_p(m_ref == -INFINITY ? 0.0f : m_ref, m_ref + kLazy);
           done_p = !bar_named_or(2, kWorkers, over);
           if (!done_p) {
             l_part = l_save;
@@ -1065,7 +1067,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         l_part *= f;
         l2_part *= f;
-        (void)write_p(m_ref == -INFINITY ? 0.0f : m_ref);
+        (void)write_p(m_ref == -INFINITY ? 0.0f : m_ref, INFINITY);
       }
       fence_proxy_async_smem();
       tc_fence_before();

@@ -1,0 +1,67 @@
+"""Calls of the step operators, and of the readout they share, at the ends of what
+the header allows: queries that are no numbers, entries and rows far smaller than
+what they share a softmax with, padded steps, outputs changed in place."""
+import copy
+import math
+
+import pytest
+import torch
+
+from test_gpu_step import D, ENTRY, H, Tree, Window, attend64, c2, check_out, entries, gen, ints, kv64, queries, rows64, rows8  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+BAD_HEADS = {3: math.nan, 16: math.inf, 17: 1e38, 40: -math.inf}   # (1e38 and infinities are beyond the range of q)
+
+
+def bad_heads(q):
+    """q with some heads that are no numbers, the heads that stay, the others."""
+    bad = q.clone()
+    for h, v in BAD_HEADS.items():
+        bad[..., h, :] = v
+    bad[..., 40, 1::2] = 1.0
+    rest = [h for h in range(H) if h not in BAD_HEADS]
+    return bad, rest
+
+
+@pytest.mark.parametrize("B,kernel", [(3, 0), (60, 0), (60, 1), (60, 2), (170, 0), (3, 2)])
+def test_sparse_attn_heads_of_nan(c2, B, kernel):  # noqa: F811
+    """Heads whose logits are no numbers leave the other heads alone, in one block of keys and in several."""
+    K, W, cap = 512, 128, 600
+    kv = entries(c2, B * cap, 1).view(B, cap, ENTRY)
+    idx = torch.stack([torch.randperm(cap, generator=gen(b), device="cuda")[:K].sort().values for b in range(B)]).int()
+    swa, scale = rows8((B, W), 2)
+    q = queries((B,), 3)
+    bad, rest = bad_heads(q)
+    p = c2.Params.make(attn_kernel=kernel)
+    ws = c2.workspace(c2.OP_ATTN, B, cap, p)
+    out, lse = [], []
+    for x in (q, bad):
+        out.append(torch.empty(B, H, D, device="cuda"))
+        lse.append(torch.empty(B, H, device="cuda"))
+        c2.sparse_attn(p, x, kv, idx, swa, scale, ints([W] * B), out[-1], ws, lse=lse[-1])
+        assert c2.get_device_status() == 0
+    assert torch.isfinite(out[0]).all()
+    assert torch.equal(out[0][:, rest], out[1][:, rest]) and torch.equal(lse[0][:, rest], lse[1][:, rest])
+    assert torch.isnan(out[1][:, 3]).all()
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+def test_step_heads_of_nan(c2, kernel):  # noqa: F811
+    """The same of trees and windows."""
+    steps = [Tree(c2, 1, 5, 512, 128, [900], cap=600, seed=4), Tree(c2, 12, 9, 300, 128, [70 * i for i in range(12)], cap=310, seed=5),
+             Tree(c2, 1, 2, 2048, 1024, [5000], cap=2100, seed=6), Tree(c2, 40, 8, 0, 128, [9 * i for i in range(40)], seed=7),
+             Window([700, 0, 40], [120, 60, 3], 128, 4, seed=8), Window([3000], [2], 1024, 64, seed=9)]
+    for s in steps:
+        s.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        out, lse = s.out.clone(), s.lse.clone()
+        good, (s.q, rest) = s.q, bad_heads(s.q)
+        s.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        assert torch.equal(s.out[..., rest, :], out[..., rest, :]) and torch.equal(s.lse[..., rest], lse[..., rest])
+        seen = ~torch.isneginf(lse[..., 3])
+        assert torch.isnan(s.out[..., 3, :][seen].float()).all()
+        s.q = good
+        s.call(c2, kernel)
+        s.check()
