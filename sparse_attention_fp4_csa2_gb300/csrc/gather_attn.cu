@@ -37,6 +37,7 @@
 // Warps: 0-3 softmax, 4-11 rows, 12 S, 13 second product.  Every wait is bounded;
 // after one runs out every role falls through its waits and the output is
 // undefined (CSA2_DEV_ERR_TIMEOUT).
+#include "gather_q.h"
 #include "step_rows.cuh"
 
 namespace csa2 {
@@ -332,7 +333,11 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
     load();
     if (first) {   // the token's Q, which lands about now (the first token's is the softmax warps')
       if (n) {
-        wait_g(S, &S.q_raw, n & 1);
+#pragma unroll
+        for (int i = 0; i < kQWaits; ++i) {
+          const QWait q = q_wait(n, i);
+          wait_g(S, q.ready ? &S.q_ready : &S.q_raw, q.phase & 1);
+        }
         convert_q<kRowG * 32>(qs, w * 32 + lane);
         if (lane == 0) mbar_arrive(&S.q_ready);
       }

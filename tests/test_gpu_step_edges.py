@@ -65,3 +65,18 @@ def test_step_heads_of_nan(c2, kernel):  # noqa: F811
         s.q = good
         s.call(c2, kernel)
         s.check()
+
+
+@pytest.mark.parametrize("kernel", [0, 2])
+def test_many_tokens_of_a_single_step(c2, kernel):  # noqa: F811
+    """Tokens of at most 64 keys, several for each CTA, beside some of more."""
+    t = Tree(c2, 330, 3, 8, 16, [7 * i for i in range(330)], cap=11, seed=15)
+    for _ in range(5):
+        t.out.fill_(7.0)
+        t.call(c2, kernel)
+        assert c2.get_device_status() == 0
+    t.check()
+    w = Window([0, 900, 20], [300, 1, 400], 16, 4, spare=3, seed=16)
+    w.call(c2, kernel)
+    assert c2.get_device_status() == 0
+    w.check()
