@@ -839,10 +839,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = cur_j;
       // ------------------------------------------------------ Q of a new item
       // --------------------------------------------------------- dequant
-      if (cp == 0 && r0 < a.Bk) put_row_info<kStep>(S, tile, r0, b0);
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
         if (g > 0) wait_ft(S, &S.cols_free[p], (g - 1) & 1u);
+        // (behind the first wait: the block before's products follow every warp's
+        // softmax, which has read the rows' scales for the last time)
+        if (p == 0 && cp == 0 && r0 < a.Bk) put_row_info<kStep>(S, tile, r0, b0);
         if (r0 < a.Bk) dequant_front<kStep>(tile, col_stride, r0, cp + 2 * p, b0);
         fence_proxy_async_smem();
         mbar_arrive(&S.cols_full[p]);
