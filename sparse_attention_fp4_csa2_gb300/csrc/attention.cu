@@ -907,6 +907,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           rsv[4 * q + 3] = f4.w;
         }
       };
+      // (step form: of no key -inf, also for a query of infinities or NaNs, whose
+      // product with the zeros in its place is a NaN)
+      auto logit_of = [](bool in, uint32_t u, float rs, float lg) {
+        return in && lg != -INFINITY ? fmaf(__uint_as_float(u), rs, lg) : -INFINITY;
+      };
       auto apply = [&](int mi, const uint32_t (&u)[16], const float (&rsv)[16], const uint32_t (&vb)[4],
                        float (&x)[16]) {
         const int k0 = 16 * (2 * (2 * mi + wh) + th);
@@ -916,10 +921,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const float4 g = l4[q];
-            x[4 * q] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q]), rsv[4 * q], g.x) : -INFINITY;
-            x[4 * q + 1] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q + 1]), rsv[4 * q + 1], g.y) : -INFINITY;
-            x[4 * q + 2] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q + 2]), rsv[4 * q + 2], g.z) : -INFINITY;
-            x[4 * q + 3] = k0 < a.Bk ? fmaf(__uint_as_float(u[4 * q + 3]), rsv[4 * q + 3], g.w) : -INFINITY;
+            x[4 * q] = logit_of(k0 < a.Bk, u[4 * q], rsv[4 * q], g.x);
+            x[4 * q + 1] = logit_of(k0 < a.Bk, u[4 * q + 1], rsv[4 * q + 1], g.y);
+            x[4 * q + 2] = logit_of(k0 < a.Bk, u[4 * q + 2], rsv[4 * q + 2], g.z);
+            x[4 * q + 3] = logit_of(k0 < a.Bk, u[4 * q + 3], rsv[4 * q + 3], g.w);
           }
         } else {
 #pragma unroll

@@ -359,10 +359,12 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t
   int64_t token;
   for (int steps; tokens.take(a, token, steps);) {
     float m = -INFINITY, l = 0.0f;
+    bool any = false;   // the token has a key
 #pragma unroll 1
     for (int s = 0; s < steps; ++s, ++g) {
       const uint32_t b = g & 1, ph = (g >> 1) & 1;
       wait_g(S, &S.rows_full[b], ph);   // the keys' scales
+      any |= __any_sync(0xffffffffu, S.lg[b][lane] != -INFINITY || S.lg[b][lane + 32] != -INFINITY);
       wait_g(S, &S.s_full[b], ph);
       tc_fence_after();
       float x[2][16];
@@ -443,7 +445,9 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t
       mbar_arrive(&S.p_full[b]);
     }
     // ---------------------------------------------------------- token's end
-    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    // (a query of infinities or NaNs makes NaNs of the zeros in place of masked keys,
+    // which shows where no key is left: nothing of them counts then)
+    l = any ? l + __shfl_xor_sync(0xffffffffu, l, 16) : 0.0f;
     if (th == 0) {
       S.inv_l[h] = l > 0.0f && !S.abort ? 1.0f / l : l;   // (0 stays 0, a NaN a NaN)
       if (a.lse) a.lse[token * H + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2G;
@@ -477,6 +481,10 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t
         if (h0 && t == 3) {   // O^T is read: the next token's products may start
           tc_fence_before();
           mbar_arrive(&S.o_free);
+        }
+        if (!any) {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) v[q] = 0;
         }
         const uint32_t stage = smem_u32(ps + w * 4096 + (t & 1) * 2048);   // (two in turn: one barrier a time)
         uint32_t o[16];

@@ -80,3 +80,25 @@ def test_many_tokens_of_a_single_step(c2, kernel):  # noqa: F811
     w.call(c2, kernel)
     assert c2.get_device_status() == 0
     w.check()
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+@pytest.mark.parametrize("B,T,K", [(1, 6, 40), (2, 9, 0), (60, 4, 200), (50, 7, 0)])
+def test_padding_tokens_of_nan(c2, kernel, B, T, K):  # noqa: F811
+    """Tokens that see nothing give 0 and -inf whatever their queries hold; the others
+    are right."""
+    t = Tree(c2, B, T, K, 0, [9 * i for i in range(B)], cap=210 if K else 0, seed=17)
+    for b in range(B):
+        for i in range(1, T, 2):
+            t.mask[b][i] = 0
+            if K:
+                t.idx[b, i] = -1
+    t.put_mask()
+    good = t.q.clone()
+    for i, v in zip(range(1, T, 2), (math.nan, math.inf, -math.inf)):
+        t.q[:, i, 5:] = v
+    t.call(c2, kernel)
+    assert c2.get_device_status() == 0
+    assert (t.out[:, 1::2] == 0).all() and torch.isneginf(t.lse[:, 1::2]).all()
+    t.q = good
+    t.check()
