@@ -63,6 +63,7 @@ struct __align__(16) CtlG {
   volatile uint32_t abort;
   float fac[H];
   __align__(16) float inv_l[H];
+  __align__(16) uint32_t none[kSoftG];   // a softmax warp has found that the token sees nothing
   // per key of a slot: log2(e) / sqrt(512) x scale, log2(scale) (-inf: no key), 1 / scale
   __align__(16) float rs[2][kStep];
   __align__(16) float lg[2][kStep];
@@ -104,6 +105,17 @@ __device__ __forceinline__ Keys keys_of(const AttnArgs &a, int64_t gp) {
   const int n = k.rows + k.named + a.K;
   k.steps = n > kStep ? (n + kStep - 1) / kStep : 1;
   return k;
+}
+
+// Whether a token sees any key (by whole warps).
+__device__ __noinline__ bool has_keys(const AttnArgs &a, int64_t gp, int lane) {
+  const Keys k = keys_of(a, gp);
+  bool any = k.rows + k.named > 0;
+  for (int e = lane; e < a.K; e += 32) {
+    const int32_t id = __ldg(a.idx + gp * a.K + e);
+    any |= id >= 0 && id < a.cap;
+  }
+  return __any_sync(0xffffffffu, any);
 }
 
 // The CTA's tokens that have steps, by whole warps; the next one is looked up while
@@ -359,12 +371,10 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t
   int64_t token;
   for (int steps; tokens.take(a, token, steps);) {
     float m = -INFINITY, l = 0.0f;
-    bool any = false;   // the token has a key
 #pragma unroll 1
     for (int s = 0; s < steps; ++s, ++g) {
       const uint32_t b = g & 1, ph = (g >> 1) & 1;
       wait_g(S, &S.rows_full[b], ph);   // the keys' scales
-      any |= __any_sync(0xffffffffu, S.lg[b][lane] != -INFINITY || S.lg[b][lane + 32] != -INFINITY);
       wait_g(S, &S.s_full[b], ph);
       tc_fence_after();
       float x[2][16];
@@ -445,9 +455,15 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t
       mbar_arrive(&S.p_full[b]);
     }
     // ---------------------------------------------------------- token's end
-    // (a query of infinities or NaNs makes NaNs of the zeros in place of masked keys,
-    // which shows where no key is left: nothing of them counts then)
-    l = any ? l + __shfl_xor_sync(0xffffffffu, l, 16) : 0.0f;
+    l += __shfl_xor_sync(0xffffffffu, l, 16);
+    // a query of infinities or NaNs makes NaNs of the zeros in place of masked keys:
+    // without a key nothing of them counts
+    bool none = false;
+    if (__any_sync(0xffffffffu, l != l)) {
+      none = !has_keys(a, token, lane);
+      if (none) l = 0.0f;
+    }
+    if (lane == 0) S.none[w] = none;
     if (th == 0) {
       S.inv_l[h] = l > 0.0f && !S.abort ? 1.0f / l : l;   // (0 stays 0, a NaN a NaN)
       if (a.lse) a.lse[token * H + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2G;
@@ -455,6 +471,8 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t
     bar_named(1, kSoftG * 32);
     wait_g(S, &S.slot_free[(g - 1) & 1], ((g - 1) >> 1) & 1);
     tc_fence_after();
+    const uint4 nw = *reinterpret_cast<const uint4 *>(S.none);
+    none = nw.x | nw.y | nw.z | nw.w;   // (one head's warp has found it out for all)
     // 32 heads x 32 channels at a time: a lane's channel, heads in pairs, through the
     // P buffers (which the last products have read) as rows [channel][32 heads], and
     // back transposed, 8 channels of a head a lane, for 64 contiguous bytes a head.
@@ -482,7 +500,7 @@ __device__ void softmax_warps_g(const AttnArgs &a, CtlG &S, uint8_t *qs, uint8_t
           tc_fence_before();
           mbar_arrive(&S.o_free);
         }
-        if (!any) {
+        if (none) {
 #pragma unroll
           for (int q = 0; q < 32; ++q) v[q] = 0;
         }
