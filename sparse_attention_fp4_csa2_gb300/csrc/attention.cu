@@ -97,17 +97,15 @@ struct __align__(16) Ctl {
   float lfin[H];           // per head at an item's end: row sum
 };
 
-// Step form: per row log2 of its scale (-inf: no key) and 1 / scale, behind
-// what both block forms keep in the tile region (its single blocks are of up to
-// 144 rows).  The reference max is taken over logit + log2(scale), so that what
-// goes to the tensor core, 2^(logit - m) x scale, is at most 1 (2^kLazy) whatever
-// the rows' scales are; the row sum takes it times 1 / scale.  A row whose scale
-// is below 2^-64 counts as zeros (NaN codes stay NaN): codes x 0, with a scale of
-// 2^-64, so that it never sets the reference and, up to scales of 2^50 beside it,
-// 2^(logit - m) x 2^-64 is still an fp32 number that gives back its weight.
+// Step form: per key log2 of its scale f (step_rows.cuh; -inf: no key) and 1 / f,
+// behind what both block forms keep in the tile region (its single blocks are of up
+// to 144 rows).  The reference max is taken over logit + log2(f), so that what goes to
+// the tensor core, 2^(logit - m) f, is at most 1 (2^kLazy) whatever the keys' sizes
+// are; the row sum takes it times 1 / f.  A row whose scale is below 2^-64 counts as
+// zeros (NaN codes stay NaN).
 // A chunk's partial is O over the sum of its scaled weights, a convex combination
-// of what the tile holds (at most 2688 and, of 8-bit rows, codes): within fp16
-// whatever the scales; that sum goes along with the row sum.
+// of what the tile holds (below 3): within fp16 whatever the scales; that sum goes
+// along with the row sum.
 struct StepScale {
   float lg[kMaxBk], inv[kMaxBk];
   float red2[2][H];
@@ -282,7 +280,8 @@ __device__ __forceinline__ void dequant_front(uint8_t *tile, uint32_t col_stride
     for (int i = 0; i < 8; ++i) {
       // 8 codes = 8 dims of scale group i / 2
       const uint32_t sb = (sc >> (8 * (i >> 1))) & 0xFFu;
-      const uint32_t s2 = e4m3x2_to_half2((uint16_t)(sb | (sb << 8)));
+      uint32_t s2 = e4m3x2_to_half2((uint16_t)(sb | (sb << 8)));
+      if constexpr (kStep) s2 = hmul2_u32(s2, __float_as_uint(b.scale));
       uint32_t h[4];
       e2m1x8_to_half2x4(w[i], h);
       const uint4 o = make_uint4(hmul2_u32(h[0], s2), hmul2_u32(h[1], s2), hmul2_u32(h[2], s2), hmul2_u32(h[3], s2));
@@ -295,7 +294,6 @@ __device__ __forceinline__ void dequant_front(uint8_t *tile, uint32_t col_stride
   }
   if constexpr (N == 16) {
     if (b.kind == 2) {
-      const uint32_t keep2 = kStep && b.scale < kTinyScale ? 0u : 0x3C003C00u;   // fp16 1, 1
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint4 raw = b.v[u];
@@ -307,8 +305,9 @@ __device__ __forceinline__ void dequant_front(uint8_t *tile, uint32_t col_stride
             make_uint4(e4m3x2_to_half2((uint16_t)(w[2] & 0xFFFF)), e4m3x2_to_half2((uint16_t)(w[2] >> 16)),
                        e4m3x2_to_half2((uint16_t)(w[3] & 0xFFFF)), e4m3x2_to_half2((uint16_t)(w[3] >> 16)));
         if constexpr (kStep) {
-          o0 = make_uint4(hmul2_u32(o0.x, keep2), hmul2_u32(o0.y, keep2), hmul2_u32(o0.z, keep2), hmul2_u32(o0.w, keep2));
-          o1 = make_uint4(hmul2_u32(o1.x, keep2), hmul2_u32(o1.y, keep2), hmul2_u32(o1.z, keep2), hmul2_u32(o1.w, keep2));
+          const uint32_t norm = __float_as_uint(b.scale);
+          o0 = make_uint4(hmul2_u32(o0.x, norm), hmul2_u32(o0.y, norm), hmul2_u32(o0.z, norm), hmul2_u32(o0.w, norm));
+          o1 = make_uint4(hmul2_u32(o1.x, norm), hmul2_u32(o1.y, norm), hmul2_u32(o1.z, norm), hmul2_u32(o1.w, norm));
         }
         *reinterpret_cast<uint4 *>(rowp + (((2 * u) ^ sw) << 4)) = o0;
         *reinterpret_cast<uint4 *>(rowp + (((2 * u + 1) ^ sw) << 4)) = o1;
@@ -322,18 +321,46 @@ __device__ __forceinline__ void dequant_front(uint8_t *tile, uint32_t col_stride
   for (int i = 0; i < 8; ++i) *reinterpret_cast<uint4 *>(rowp + ((i ^ sw) << 4)) = make_uint4(0, 0, 0, 0);
 }
 
+// The row's scale.  Step form: f (step_rows.cuh), and what the values are multiplied by
+// on their way to the tile, two fp16 numbers, takes the scale's place; by the two
+// neighbouring lanes that hold it (whole warps: blocks are of a multiple of 16 rows).
+template <bool kStep>
+__device__ __forceinline__ float size_row(RowBuf &b) {
+  if constexpr (kStep) {
+    uint32_t size = 0, codes = 0;
+    if (b.kind == 1) {
+      const uint4 &sc = b.v[8];
+      __half2 m(0.0f, 0.0f);
+      m = scales_size(sc.x, scales_size(sc.y, m));
+      size = larger_half(scales_size(sc.z, scales_size(sc.w, m)));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) codes |= (b.v[i].x | b.v[i].y | b.v[i].z | b.v[i].w) & 0x77777777u;
+    } else if (b.kind == 2) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) codes |= (b.v[i].x | b.v[i].y | b.v[i].z | b.v[i].w) & 0x7F7F7F7Fu;
+    }
+    const uint32_t mine = codes ? size : size | 0x10000u, other = __shfl_xor_sync(0xffffffffu, mine, 1);
+    size = max(mine & 0xFFFFu, other & 0xFFFFu);
+    uint32_t norm;
+    const float f = key_scale(b.kind == 1, size, b.scale, (mine & other) >> 16, norm);
+    b.scale = __uint_as_float(norm);
+    return f;
+  } else {
+    return b.scale;
+  }
+}
+
 // What the softmax has to know of row r: its scale and whether it holds a key.
 template <bool kStep>
-__device__ __forceinline__ void put_row_info(Ctl &S, uint8_t *tile, int r, const RowBuf &b) {
+__device__ __forceinline__ void put_row_info(Ctl &S, uint8_t *tile, int r, float scale, int kind) {
   if constexpr (kStep) {
     StepScale &sc = *reinterpret_cast<StepScale *>(tile + kStepScaleOff);
-    const float f = b.scale < kTinyScale ? kTinyScale : b.scale;
-    S.rs[r] = kLogit * f;   // (of a row of zeros the products are 0, or NaN)
-    sc.lg[r] = b.kind != 0 ? log2f(f) : -INFINITY;
-    sc.inv[r] = 1.0f / f;
+    S.rs[r] = kLogit * scale;   // (of a row of zeros the products are 0, or NaN)
+    sc.lg[r] = kind != 0 ? log2f(scale) : -INFINITY;
+    sc.inv[r] = 1.0f / scale;
   } else {
-    S.rs[r] = b.scale;
-    S.vld[r] = b.kind != 0 ? 1 : 0;
+    S.rs[r] = scale;
+    S.vld[r] = kind != 0 ? 1 : 0;
   }
 }
 
@@ -708,7 +735,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive(&S.q_ready[p]);
         }
         if (ht < 64) {
-          if (rows && hcp == 0) put_row_info<kStep>(S, tile, r, b0);
+          if (rows) {
+            const float f = size_row<kStep>(b0);
+            if (hcp == 0) put_row_info<kStep>(S, tile, r, f, b0.kind);
+          }
 #pragma unroll 1
           for (int p = 0; p < 4; ++p) {
             if (rows) dequant_front<kStep>(tile, col_stride, r, hcp + 2 * p, b0);
@@ -839,12 +869,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int j = cur_j;
       // ------------------------------------------------------ Q of a new item
       // --------------------------------------------------------- dequant
+      const float f0 = r0 < a.Bk ? size_row<kStep>(b0) : 0.0f;
 #pragma unroll 1
       for (int p = 0; p < 4; ++p) {
         if (g > 0) wait_ft(S, &S.cols_free[p], (g - 1) & 1u);
         // (behind the first wait: the block before's products follow every warp's
         // softmax, which has read the rows' scales for the last time)
-        if (p == 0 && cp == 0 && r0 < a.Bk) put_row_info<kStep>(S, tile, r0, b0);
+        if (p == 0 && cp == 0 && r0 < a.Bk) put_row_info<kStep>(S, tile, r0, f0, b0.kind);
         if (r0 < a.Bk) dequant_front<kStep>(tile, col_stride, r0, cp + 2 * p, b0);
         fence_proxy_async_smem();
         mbar_arrive(&S.cols_full[p]);

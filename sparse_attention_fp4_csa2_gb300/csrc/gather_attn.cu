@@ -1,9 +1,10 @@
 // The step form of the readout, one CTA per token: a token's listed main-KV
 // entries, its window rows and its extra rows (csa2_tree_attn; csa2_window_attn
 // when its rows do not fit in the tiles of window_attn.cu), in one softmax:
-//   o_h = sum_k softmax_k(q_h . v_k s_k / sqrt(512)) v_k s_k,
-// v_k an entry's 512 values (E2M1 x E4M3, s_k = 1) or a row's E4M3 codes, s_k its
-// scale, all exact in fp16.
+//   o_h = sum_k softmax_k(q_h . v_k f_k / sqrt(512)) v_k f_k,
+// v_k f_k an entry's 512 values (E2M1 x E4M3) or a row's E4M3 codes times its scale,
+// f_k a power of two, or a row's scale times one, of their size (step_rows.cuh), so
+// that the v_k are exact in fp16.
 //
 // No two tokens list the same entries, so a token's 64 heads are all that share a
 // key: 4 x 64 x 512 flop for 288 bytes, which the tensor cores take as products of
@@ -19,7 +20,7 @@
 //   S        M = 64 heads, N = 64 keys, K = 512, in two accumulators in turn
 //            (products into one wait for each other), two S buffers;
 //   softmax  4 warps, a head's 64 logits on two lanes; the reference maximum (over
-//            logit + log2(s_k)) is raised only past 2^8, O^T then rescaled; P to
+//            logit + log2(f_k)) is raised only past 2^8, O^T then rescaled; P to
 //            shared memory as fp16;
 //   O^T += V^T P^T  M = 128 channels (four blocks), N = 64 heads, K = 64 keys, V^T
 //            from the same slot; its end frees the slot;
@@ -31,8 +32,7 @@
 // up to 168 keys 11.1.  Both products issued by one thread, a tile of 128 keys and
 // softmax on the rows' warps, as in the sparse readout: 637 us for the 2,048.
 // Keys that the token does not see take no place: the list (whose -1 are masked),
-// the window's visible rows, then the named extra rows.  (The list first: entries
-// have scale 1, so the first step sets a reference that rows rarely raise.)
+// the window's visible rows, then the named extra rows.
 //
 // Warps: 0-3 softmax, 4-11 rows, 12 S, 13 second product.  Every wait is bounded;
 // after one runs out every role falls through its waits and the output is
@@ -64,7 +64,7 @@ struct __align__(16) CtlG {
   float fac[H];
   __align__(16) float inv_l[H];
   __align__(16) uint32_t none[kSoftG];   // a softmax warp has found that the token sees nothing
-  // per key of a slot: log2(e) / sqrt(512) x scale, log2(scale) (-inf: no key), 1 / scale
+  // per key of a slot: log2(e) / sqrt(512) x f, log2(f) (-inf: no key), 1 / f
   __align__(16) float rs[2][kStep];
   __align__(16) float lg[2][kStep];
   __align__(16) float inv[2][kStep];
@@ -166,7 +166,7 @@ __device__ __forceinline__ int nth_bit(uint64_t m, int n) {
 struct KeyData {
   uint4 v[2][4];      // [block]: an entry's codes in the first two, or a row's 64
   uint32_t sc[2];     // [block]: an entry's four scales
-  float scale;
+  float scale;        // of a row
   int kind;           // 0 none, 1 entry, 2 row of codes
 };
 
@@ -175,10 +175,33 @@ __device__ __forceinline__ void st_chunk(uint32_t at, int chunk, uint32_t x, uin
                : "memory");
 }
 
+__device__ __forceinline__ uint32_t or_words(const uint4 (&v)[4], int n) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int u = 0; u < n; ++u) any |= v[u].x | v[u].y | v[u].z | v[u].w;
+  return any;
+}
+
+// The key's scale f, and what its values are multiplied by, by the four lanes that
+// hold it.
+__device__ __forceinline__ float scale_of(const KeyData &d, int lane, uint32_t &norm) {
+  uint32_t size = 0, codes = 0;
+  if (d.kind == 1) {
+    size = larger_half(scales_size(d.sc[0], scales_size(d.sc[1], __half2(0.0f, 0.0f))));
+    codes = (or_words(d.v[0], 2) | or_words(d.v[1], 2)) & 0x77777777u;
+  } else if (d.kind == 2) {
+    codes = (or_words(d.v[0], 4) | or_words(d.v[1], 4)) & 0x7F7F7F7Fu;
+  }
+  size = max(size, __shfl_xor_sync(0xffffffffu, size, 8));
+  size = max(size, __shfl_xor_sync(0xffffffffu, size, 16));
+  const uint32_t any = __ballot_sync(0xffffffffu, codes) & (0x01010101u << (lane & 7));
+  return key_scale(d.kind == 1, size, d.scale, any == 0, norm);
+}
+
 // 64 channels into the 128-byte row whose chunk 0 is at `at` (chunk i at ^ 16 i).
-__device__ __forceinline__ void put_entry(uint32_t at, const uint4 (&v)[4], uint32_t sc) {
+__device__ __forceinline__ void put_entry(uint32_t at, const uint4 (&v)[4], uint32_t sc, uint32_t norm) {
   const uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
-  const uint32_t e[2] = {e4m3x2_to_half2((uint16_t)sc), e4m3x2_to_half2((uint16_t)(sc >> 16))};
+  const uint32_t e[2] = {hmul2_u32(e4m3x2_to_half2((uint16_t)sc), norm), hmul2_u32(e4m3x2_to_half2((uint16_t)(sc >> 16)), norm)};
 #pragma unroll
   for (int i = 0; i < 8; ++i) {   // 8 channels, of scale i / 2
     uint32_t h[4];
@@ -188,16 +211,16 @@ __device__ __forceinline__ void put_entry(uint32_t at, const uint4 (&v)[4], uint
   }
 }
 
-__device__ __forceinline__ void put_codes(uint32_t at, const uint4 (&v)[4], uint32_t keep) {
+__device__ __forceinline__ void put_codes(uint32_t at, const uint4 (&v)[4], uint32_t norm) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      st_chunk(at, 2 * i + j, hmul2_u32(e4m3x2_to_half2((uint16_t)w[2 * j]), keep),
-               hmul2_u32(e4m3x2_to_half2((uint16_t)(w[2 * j] >> 16)), keep),
-               hmul2_u32(e4m3x2_to_half2((uint16_t)w[2 * j + 1]), keep),
-               hmul2_u32(e4m3x2_to_half2((uint16_t)(w[2 * j + 1] >> 16)), keep));
+      st_chunk(at, 2 * i + j, hmul2_u32(e4m3x2_to_half2((uint16_t)w[2 * j]), norm),
+               hmul2_u32(e4m3x2_to_half2((uint16_t)(w[2 * j] >> 16)), norm),
+               hmul2_u32(e4m3x2_to_half2((uint16_t)w[2 * j + 1]), norm),
+               hmul2_u32(e4m3x2_to_half2((uint16_t)(w[2 * j + 1] >> 16)), norm));
   }
 }
 
@@ -320,9 +343,10 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
   for (uint32_t g = 0; k.steps; ++g) {
     const uint32_t b = g & 1;
     const bool first = s == 0;
+    uint32_t norm;
+    const float f = scale_of(d, lane, norm);
     if (g > 1) wait_g(S, &S.slot_free[b], ((g >> 1) - 1) & 1);
     if (block == 0) {
-      const float f = d.scale < kTinyScale ? kTinyScale : d.scale;
       S.rs[b][key] = kLogitG * f;
       S.lg[b][key] = d.kind ? log2f(f) : -INFINITY;
       S.inv[b][key] = d.kind ? 1.0f / f : 1.0f;
@@ -331,9 +355,9 @@ __device__ void row_warps_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t 
     for (int h = 0; h < 2; ++h) {
       const uint32_t at = smem_u32(slots) + b * kSlotG + (4 * h + block) * kBlockG + key * 128 + ((key & 7) << 4);
       if (d.kind == 1) {
-        put_entry(at, d.v[h], d.sc[h]);
+        put_entry(at, d.v[h], d.sc[h], norm);
       } else if (d.kind == 2) {
-        put_codes(at, d.v[h], d.scale < kTinyScale ? 0u : 0x3C003C00u);
+        put_codes(at, d.v[h], norm);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) st_chunk(at, i, 0, 0, 0, 0);

@@ -102,3 +102,52 @@ def test_padding_tokens_of_nan(c2, kernel, B, T, K):  # noqa: F811
     assert (t.out[:, 1::2] == 0).all() and torch.isneginf(t.lse[:, 1::2]).all()
     t.q = good
     t.check()
+
+
+def scaled_entries(c2, rows, seed, std):  # noqa: F811
+    kv = torch.zeros(rows, ENTRY, dtype=torch.uint8, device="cuda")
+    at = torch.arange(rows, device="cuda")
+    lat = (torch.randn(rows, D, generator=gen(seed), device="cuda") * std).bfloat16()
+    c2.kv_quant_write(lat, None, 1, at, at.clone(), kv)
+    return kv
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+@pytest.mark.parametrize("row_std", [1.0, 1e-3, 1e-4, 1e-6, 1e-12])
+@pytest.mark.parametrize("entry_std", [0.0, 5e-3, 1.0])
+def test_entries_smaller_than_fp16_weights(c2, kernel, row_std, entry_std):  # noqa: F811
+    """Entries of zeros or of small values beside rows that are smaller still: a key
+    counts by its logit, and what it adds is held to its own size."""
+    for B, T, K in ((2, 9, 40), (1, 3, 300), (40, 6, 8), (20, 9, 100)):
+        t = Tree(c2, B, T, K, 128, [300 + i for i in range(B)], cap=310, seed=18, std=row_std)
+        t.kv = scaled_entries(c2, B * 310, 19, entry_std).view(B, 310, ENTRY)
+        t.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        t.check()
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+@pytest.mark.parametrize("row_std", [1e3, 1e-2, 1e-6])
+def test_entries_and_rows_of_every_scale(c2, kernel, row_std):  # noqa: F811
+    """Entries whose scales cover E4M3's range, blocks of zeros under large scales and
+    all-zero entries among them; rows of zero codes whose scale is 1."""
+    for B, T, K in ((2, 9, 40), (1, 3, 300), (40, 6, 8), (20, 9, 100)):
+        t = Tree(c2, B, T, K, 128, [300 + i for i in range(B)], cap=310, seed=20, std=row_std)
+        n = B * 310
+        kv = torch.randint(0, 256, (n, ENTRY), generator=gen(21), device="cuda", dtype=torch.uint8)
+        top = torch.randint(1, 127, (n, 1), generator=gen(22), device="cuda")
+        kv[:, 256:] = (torch.rand(n, 32, generator=gen(23), device="cuda") * (top + 1)).long().clamp(max=126).to(torch.uint8)
+        kv[::5, :128] = 0                     # the first half's codes, whatever its scales are
+        kv[::5, 256:272] = 126
+        kv[::5, 272:] = (kv[::5, 272:] & 7)   # and the other half subnormal
+        kv[3::7, :256] &= 0x88                # zeros and negative zeros
+        kv[4::11, 256:] = 0
+        t.kv = kv.view(B, 310, ENTRY)
+        t.swa[:, ::9] = 0
+        t.scale[:, ::9] = 1.0
+        t.tree[:, 1::3] = 0x80
+        t.tree_scale[:, 1::3] = 1.0
+        t.q = (t.q.float() * 2e-4).bfloat16()   # logits of ordinary size under the largest entries
+        t.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        t.check()
