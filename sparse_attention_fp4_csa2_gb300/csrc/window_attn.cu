@@ -31,9 +31,11 @@
 // rows out 7,500.
 // P is kept as two bf16 numbers, its rounding and the rest (16 bits together:
 // bf16 alone would cost 2^-9 of a weight, fp16 would need the rows and the
-// queries in fp16 too).  The reference maximum is over logit + log2(s_k), so that
-// P = 2^(logit - m) s_k is at most 1 whatever the rows' scales are; the row sum
-// takes it times 1 / s_k.
+// queries in fp16 too).  The reference is over logit + log2(s_k), so that P =
+// 2^(logit - m) s_k is at most 1 when m is set (2^40 before it is raised) whatever the
+// rows' scales are; the row sum takes it times 1 / s_k.  References are whole numbers:
+// what a raise multiplies the weights written so far by is then a power of two, and
+// both parts keep their bits.
 //
 // Warps: 0-7 softmax, 8-15 output, 16 rows, 17 copies of Q, 18 first product, 19
 // second product.  Every wait is bounded; after one runs out every role falls
@@ -391,8 +393,11 @@ struct Seen {
   }
 };
 
-// Weights already written (chunks c0 .. c1 - 1 of 16 slots) times f: the words of a
-// chunk are 8 of upper halves and 8 of the rest.
+// 2^d of a whole number d <= 0 (0 below fp32's range).
+__device__ __forceinline__ float pow2_whole(float d) { return d < -126.0f ? 0.0f : __int_as_float((127 + (int)d) << 23); }
+
+// Weights already written (chunks c0 .. c1 - 1 of 16 slots) times f, a power of two or
+// 0: the words of a chunk are 8 of upper halves and 8 of the rest.
 __device__ __noinline__ void scale_weights(uint32_t st, int c0, int c1, float f) {
   tmem_st_wait();
 #pragma unroll 1
@@ -411,7 +416,7 @@ __device__ __noinline__ void scale_weights(uint32_t st, int c0, int c1, float f)
 }
 
 // Two threads a row, each on half of its chunks of 16 slots, in one pass: the
-// reference is the maximum over both threads' first chunks, raised only when a
+// reference is the maximum over both threads' first chunks (rounded up), raised only when a
 // logit exceeds it by 2^kLazyW (bf16 has fp32's exponents, so weights above 1 cost
 // nothing), which hardly ever happens; the weights written until then are then
 // scaled in place, and the other thread's at the end.
@@ -481,11 +486,12 @@ __device__ void softmax_warps(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<
       for (int q = 0; q < 16; ++q) mx[q & 3] = fmaxf(mx[q & 3], x[q]);
       float cm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       if (c == c0) {
-        m = fmaxf(cm, swap_row(lanes, 0, half, quarter, cm));
+        m = ceilf(fmaxf(cm, swap_row(lanes, 0, half, quarter, cm)));
       } else {
         const bool up = cm > m + kLazyW;
         if (__any_sync(0xffffffffu, up)) {
-          const float f = !up ? 1.0f : m == -INFINITY ? 0.0f : ex2_approx(m - cm);
+          cm = ceilf(cm);
+          const float f = !up ? 1.0f : m == -INFINITY ? 0.0f : pow2_whole(m - cm);
           if (__any_sync(0xffffffffu, up && m != -INFINITY)) scale_weights(st, c0, c, f);
           l *= f;
           if (up) m = cm;
@@ -513,17 +519,17 @@ __device__ void softmax_warps(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<
       l += l2;
       tmem_st16(st + 16 * c, o);
     }
-    if (c0 == c1) m = swap_row(lanes, 0, half, quarter, m);   // (16 slots in all: none of them this thread's)
+    if (c0 == c1) m = ceilf(swap_row(lanes, 0, half, quarter, m));   // (16 slots in all: none of them this thread's)
     // one reference and one sum for the row
     tmem_st1(lanes + kColX + 4 + half, __float_as_uint(l));
     const float mo = swap_row(lanes, 1, half, quarter, m), mm = fmaxf(m, mo);
     const float lo = __uint_as_float(tmem_ld1(lanes + kColX + 4 + (half ^ 1)));
     if (__any_sync(0xffffffffu, m < mm)) {
-      const float f = m < mm ? (m == -INFINITY ? 0.0f : ex2_approx(m - mm)) : 1.0f;
+      const float f = m < mm ? (m == -INFINITY ? 0.0f : pow2_whole(m - mm)) : 1.0f;
       scale_weights(st, c0, c1, f);
       l *= f;
     }
-    l += mo < mm ? (mo == -INFINITY ? 0.0f : lo * ex2_approx(mo - mm)) : lo;
+    l += mo < mm ? (mo == -INFINITY ? 0.0f : lo * pow2_whole(mo - mm)) : lo;
     if (half == 0) tmem_st1(lanes + kColL + b, __float_as_uint(l > 0.0f && !S.abort ? 1.0f / l : l));   // (0 stays 0, a NaN a NaN)
     tmem_st_wait();
     tc_fence_before();

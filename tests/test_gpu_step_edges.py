@@ -151,3 +151,60 @@ def test_entries_and_rows_of_every_scale(c2, kernel, row_std):  # noqa: F811
         t.call(c2, kernel)
         assert c2.get_device_status() == 0
         t.check()
+
+
+def check_close(out, q, keys_of):
+    """Outputs [n, 64, 512] within half a step of bf16 of the formula's, and 2^-13 of the sum
+    of the weighted magnitudes: weights of 16 bits (2^-15), logits within 2^-16 at the
+    sizes here, exponentials and sums in fp32."""
+    for i in range(out.shape[0]):
+        keys = keys_of(i)
+        r, lse = attend64(q[i].double(), keys)
+        w = torch.exp(q[i].double() @ keys.T / math.sqrt(D) - lse[:, None])
+        err = 2.0 ** -13 * (w @ keys.abs())
+        half = torch.exp2(torch.floor(torch.log2(r.abs() + err)) - 8)
+        over = (out[i].double() - r).abs() - half - err
+        assert (over <= 0).all(), f"token {i}: off by {(over / err).max().item()} allowances too much"
+
+
+def test_tile_weights_keep_16_bits_without_a_first_reference(c2):  # noqa: F811
+    """Trees without a window whose masks leave out the first 16 rows of both halves:
+    each half of a row's softmax finds a reference of its own."""
+    B, T = 3, 64
+    t = Tree(c2, B, T, 0, 0, [5, 60, 700], seed=24, empty=False)
+    g = torch.Generator().manual_seed(25)
+    for b in range(B):
+        for i in range(T):
+            bits = torch.randperm(16, generator=g)[:5].tolist()
+            t.mask[b][i] = sum(1 << (16 + k) | 1 << (48 + (5 * k + i) % 16) for k in bits)
+    t.put_mask()
+    t.call(c2)
+    assert c2.get_device_status() == 0
+    t.check()
+    for b in range(B):
+        rows = rows64(t.tree[b], t.tree_scale[b])
+        check_close(t.out[b], t.q[b], lambda i: rows[[u for u in range(T) if t.mask[b][i] >> u & 1]])
+
+
+def test_tile_weights_keep_16_bits_when_a_reference_is_raised(c2):  # noqa: F811
+    """A window with a row 2^39 and a later one 2^41 above the first ones of a softmax thread."""
+    B, T, W = 3, 64, 64
+    t = Tree(c2, B, T, 0, W, [64, 64, 64], seed=26, empty=False)
+    sign = torch.where(torch.rand(D, generator=gen(27), device="cuda") < 0.5, -1.0, 1.0)
+    level = torch.zeros(W, device="cuda")
+    level[20], level[40] = 38.4 / 41, 40.6 / 41
+    x = level[:, None] * sign + torch.randn(B, W, D, generator=gen(28), device="cuda") * 0.2
+    t.scale = x.abs().amax(-1) / 448
+    t.swa = (x / t.scale[..., None]).to(torch.float8_e4m3fn).view(torch.uint8)
+    t.q = (sign * (41 * math.log(2) / math.sqrt(D))).bfloat16().expand(B, T, H, D).contiguous()
+    t.mask = [[0] * T for _ in range(B)]
+    t.put_mask()
+    t.call(c2)
+    assert c2.get_device_status() == 0
+    t.check()
+    for b in range(B):
+        rows = rows64(t.swa[b], t.scale[b])   # (position p in row p: rings of W rows, W tokens)
+        logit = t.q[b, 0, 0].double() @ rows.T / math.sqrt(D) / math.log(2) + torch.log2(t.scale[b].double())
+        first, mid, top = logit[:16].max(), logit[16:32].max(), logit[32:48].max()
+        assert mid < first + 40 < top and mid > top - 3.5
+        check_close(t.out[b], t.q[b], lambda i: rows)
