@@ -58,7 +58,7 @@ constexpr uint32_t kIdescSG = idesc_f16(0, 0, 0, kStep, H);
 constexpr uint32_t kIdescOG = idesc_f16(0, /*A MN-major*/ 1, 0, H, 128);
 
 struct __align__(16) CtlG {
-  uint64_t rows_full[2], slot_free[2], s_full[2], p_full[2], q_raw, q_ready, q_free, o_free, done;
+  uint64_t rows_full[2], slot_free[2], s_full[2], p_full[2], q_raw, q_ready, q_free, o_free, done[2];
   uint32_t tmem_base;
   volatile uint32_t abort;
   float fac[H];
@@ -559,6 +559,15 @@ __device__ __forceinline__ void load_q_g(CtlG &S, const CUtensorMap &tm_q, uint8
   for (int c = 0; c < 8; ++c) tma_load_2d(qs + c * kBlockG, &tm_q, 64 * c, (int32_t)(token * H), &S.q_raw);
 }
 
+// Every product that a warp's elected thread has issued has completed before the
+// teardown, also after a wait ran out (a commit tells of its own thread's products
+// only).
+__device__ __forceinline__ void drain(uint64_t *done) {
+  if (elect_one()) mma_commit(done);
+  __syncwarp();
+  mbar_wait(done, 0);
+}
+
 // (both by whole warps, an elected thread issuing)
 __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q, uint8_t *slots, uint8_t *qs, uint32_t tmem) {
   const uint64_t qd = smem_desc(smem_u32(qs), 16, 1024), kd = smem_desc(smem_u32(slots), 16, 1024);
@@ -602,7 +611,7 @@ __device__ void score_warp_g(const AttnArgs &a, CtlG &S, const CUtensorMap &tm_q
       __syncwarp();
     }
   }
-  if (n) wait_g(S, &S.q_free, (n - 1) & 1);
+  drain(&S.done[0]);
   // a copy still in flight lands before the CTA's memory goes, also after a wait ran
   // out or when the CTA's first token is behind the last sequence
   mbar_wait(&S.q_raw, (copies - 1) & 1);
@@ -637,10 +646,7 @@ __device__ void value_warp_g(const AttnArgs &a, CtlG &S, uint8_t *slots, uint8_t
       __syncwarp();
     }
   }
-  // every product has completed before the teardown, also after a wait ran out
-  if (elect_one()) mma_commit(&S.done);
-  __syncwarp();
-  mbar_wait(&S.done, 0);
+  drain(&S.done[1]);
 }
 
 __global__ void __launch_bounds__(kThreadsG, 1)
@@ -661,7 +667,7 @@ __global__ void __launch_bounds__(kThreadsG, 1)
     mbar_init(&S.q_ready, kRowG);
     mbar_init(&S.q_free, 1);
     mbar_init(&S.o_free, kSoftG * 32);
-    mbar_init(&S.done, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&S.done[i], 1);
     S.abort = 0;
     fence_barrier_init();
     prefetch_tmap(&tm_q);

@@ -63,7 +63,7 @@ constexpr float kLn2W = 0.69314718055994531f;
 
 struct __align__(16) CtlW {
   uint64_t q_full[kQRing], q_free[kQRing];
-  uint64_t fresh_full, rows_full[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2], done;
+  uint64_t fresh_full, rows_full[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_free[2], done[2];
   uint32_t tmem_base;
   volatile uint32_t abort;
   __align__(16) float rs[kMaxSlots];         // per slot: log2(e) / sqrt(512) x scale
@@ -618,6 +618,13 @@ __device__ void copy_warp(const WindowArgs &a, CtlW &S, const CUtensorMap &tm_q,
   for (uint32_t k = n > kQRing ? n - kQRing : 0; k < n; ++k) mbar_wait(&S.q_full[k % kQRing], (k / kQRing) & 1);
 }
 
+// Every product that this thread has issued has completed before the teardown, also
+// after a wait ran out (a commit tells of its own thread's products only).
+__device__ __forceinline__ void drain(uint64_t *done) {
+  mma_commit(done);
+  mbar_wait(done, 0);
+}
+
 template <bool kTree>
 __device__ void score_warp(const WindowArgs &a, CtlW &S, uint8_t *tile, uint8_t *ring, Walk<kTree> walk, uint32_t tmem) {
   const uint32_t idesc = idesc_f16(/*bf16*/ 1, 0, 0, (uint32_t)a.slots, 128);
@@ -642,6 +649,7 @@ __device__ void score_warp(const WindowArgs &a, CtlW &S, uint8_t *tile, uint8_t 
     }
     mma_commit(&S.s_full[b]);
   }
+  drain(&S.done[0]);
 }
 
 template <bool kTree>
@@ -674,9 +682,7 @@ __device__ void value_warp(const WindowArgs &a, CtlW &S, uint8_t *tile, Walk<kTr
     }
     mma_commit(&S.pv_done[b]);
   }
-  // every product has completed before the teardown, also after a wait ran out
-  mma_commit(&S.done);
-  mbar_wait(&S.done, 0);
+  drain(&S.done[1]);
 }
 
 template <bool kTree>
@@ -702,7 +708,7 @@ __global__ void __launch_bounds__(kThreadsW, 1)
       mbar_init(&S.o_free[i], kOutWarps);
     }
     mbar_init(&S.fresh_full, kFillWarps);
-    mbar_init(&S.done, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&S.done[i], 1);
     S.abort = 0;
     fence_barrier_init();
   }
