@@ -130,8 +130,9 @@ int32_t csa2_indexer_entry_bytes(int32_t fp4);
  *   z         bf16 [n_entries][m][512] for m = 2, NULL for m = 1
  *   m         1 or 2
  *   entry_pos int64 [n_entries] RoPE positions
- *   slot      int64 [n_entries] destination row in kv, 0 <= slot < kv_rows
- *             (an out-of-range slot is skipped and sets CSA2_DEV_ERR_INDEX)
+ *   slot      int64 [n_entries] destination row in kv, 0 <= slot < kv_rows, or -1
+ *             (a place without an entry, skipped); any other slot, or a position
+ *             out of range, is skipped and sets CSA2_DEV_ERR_INDEX
  *   kv        uint8 [kv_rows][288], 16-byte aligned
  * n_entries == 0 is a no-op.
  */
@@ -167,8 +168,8 @@ csa2_status csa2_kv_quant_write_ik(const void *latent, const void *z, int32_t m,
  * [rows][4] (byte E + 127 for dims 32i..32i+31) at k_fp4 + rows * 64: 68 B per
  * entry ([A] 3.1).
  *   k      bf16 [n][128], 16-byte aligned
- *   slot   int64 [n] destination rows, 0 <= slot < rows (others are skipped
- *          and set CSA2_DEV_ERR_INDEX)
+ *   slot   int64 [n] destination rows, 0 <= slot < rows, or -1 (skipped; others
+ *          are skipped and set CSA2_DEV_ERR_INDEX)
  *   k_fp4  uint8 [rows * 68], 16-byte aligned; rows a multiple of 4
  * n == 0 is a no-op.
  */
@@ -348,9 +349,10 @@ csa2_status csa2_hier_pool_select_static(const float *block_scores, const int32_
  *   scale (NaNs do not count for the maximum).
  *   latent    bf16 [n][512], 16-byte aligned
  *   pos       int64 [n], 0 <= pos < 2^22, or NULL (no RoPE)
- *   slot      int64 [n] destination rows, distinct, 0 <= slot < rows (a slot
- *             or position out of range is skipped and sets CSA2_DEV_ERR_INDEX;
- *             rows named twice hold a mixture of their writers)
+ *   slot      int64 [n] destination rows, distinct, 0 <= slot < rows, or -1 (a
+ *             place without a row, skipped); any other slot, or a position out of
+ *             range, is skipped and sets CSA2_DEV_ERR_INDEX; rows named twice hold
+ *             a mixture of their writers
  *   swa       uint8 E4M3 [rows][512], 16-byte aligned; swa_scale fp32 [rows]
  * Rows not named are left as they were.  n == 0 is a no-op.
  */
@@ -453,8 +455,8 @@ typedef struct {
  *   ctx_len, new_len int32 [batch]
  *   m         1 or 2; cap entries and swa_rows >= 1 ring rows per sequence
  *   n_tokens, n_entries: lengths of the outputs.  Places past the last token or
- *             entry get -1 (which the writers skip, and report); tokens and
- *             entries past the outputs' lengths are dropped.
+ *             entry get -1 (which the writers skip); tokens and entries past the
+ *             outputs' lengths are dropped.
  *   maps      the outputs (out; the struct itself is read by the call)
  * A negative length (taken as 0), dropped tokens or entries, and a sequence past
  * its cap set CSA2_DEV_ERR_NVIS.  batch above 8192 and lengths of the outputs past

@@ -170,7 +170,8 @@ def get_device_status(stream=None) -> int:
 
 
 def kv_quant_write(latent, z, m, entry_pos, slot, kv, rope_theta=10000.0, stream=None):
-    """latent/z bf16 [n, m, 512] (z None at m=1); entry_pos, slot int64 [n]; kv uint8 [rows, 288]."""
+    """latent/z bf16 [n, m, 512] (z None at m=1); entry_pos, slot int64 [n]
+    (-1: skipped); kv uint8 [rows, 288]."""
     n = entry_pos.numel()
     _check(lib().csa2_kv_quant_write(_ptr(latent, torch.bfloat16, "latent"), _ptr(z, torch.bfloat16, "z"), m, n,
                                      _ptr(entry_pos, torch.int64, "entry_pos"), _ptr(slot, torch.int64, "slot"),
@@ -213,7 +214,7 @@ def indexer_k_fp4_planes(k_fp4: torch.Tensor):
 
 
 def indexer_k_quant(k, slot, k_fp4, stream=None):
-    """k bf16 [n, 128]; slot int64 [n]; k_fp4 uint8 cache of ``indexer_k_fp4_cache``."""
+    """k bf16 [n, 128]; slot int64 [n] (-1: skipped); k_fp4 uint8 cache of ``indexer_k_fp4_cache``."""
     n = slot.numel()
     _check(lib().csa2_indexer_k_quant(_ptr(k, torch.bfloat16, "k"), n, _ptr(slot, torch.int64, "slot"),
                                       _ptr(k_fp4, torch.uint8, "k_fp4"), k_fp4.numel() // FP4_ENTRY_BYTES,
@@ -362,7 +363,7 @@ def _stream_on(dev, stream):
 
 def swa_quant_write(latent, slot, swa, swa_scale, pos=None, rope_theta=10000.0, stream=None):
     """Write sliding-window rows as FP8: latent bf16 [n, 512]; slot int64 [n]
-    (distinct); pos int64 [n] or None (no RoPE); swa uint8 [rows, 512] and
+    (distinct; -1: skipped); pos int64 [n] or None (no RoPE); swa uint8 [rows, 512] and
     swa_scale fp32 [rows] (or with leading dimensions, rows flattened)."""
     n, rows, dev = slot.numel(), swa_scale.numel(), _cur(latent)
     if swa.numel() != rows * D:

@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(256) swa_quant_write_kernel(const __nv_bfloat1
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     if (e0 + r >= n) return;
+    if (row[r] == -1) continue;   // a place without a token
     if (row[r] < 0 || row[r] >= rows || p[r] < 0 || p[r] >= kMaxRopePos) {
       if (lane == 0) set_error(CSA2_DEV_ERR_INDEX);
       continue;

@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(256) indexer_k_quant_kernel(const __nv_bfloat1
   const int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (i >= n) return;   // warp-uniform
   const int64_t row = __ldg(slot + i);
+  if (row == -1) return;   // a place without a key
   if (row < 0 || row >= rows) {
     if (lane == 0) set_error(CSA2_DEV_ERR_INDEX);
     return;

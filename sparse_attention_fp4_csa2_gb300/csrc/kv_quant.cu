@@ -153,6 +153,7 @@ __global__ void __launch_bounds__(256) kv_quant_write_kernel(const __nv_bfloat16
   if (e >= n_entries) return;   // uniform over the warp (the block, when projecting)
   const int64_t row = slot[e];
   const int64_t p = pos[e];
+  if (row == -1) return;   // a place without an entry
   if (row < 0 || row >= kv_rows || p < 0 || p >= kMaxRopePos || (kProject && row >= ik.k_rows)) {
     if (lane == 0 && (!kProject || threadIdx.x == 0)) set_error(CSA2_DEV_ERR_INDEX);
     return;

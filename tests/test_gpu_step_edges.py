@@ -208,3 +208,83 @@ def test_tile_weights_keep_16_bits_when_a_reference_is_raised(c2):  # noqa: F811
         first, mid, top = logit[:16].max(), logit[16:32].max(), logit[32:48].max()
         assert mid < first + 40 < top and mid > top - 3.5
         check_close(t.out[b], t.q[b], lambda i: rows)
+
+
+def test_writers_skip_places_without_a_row(c2):  # noqa: F811
+    """Slot -1 is no row and no error, whatever position and values stand beside it;
+    slots below it and past the cache are reported."""
+    lat = torch.randn(40, D, generator=gen(30), device="cuda").bfloat16()
+    pos = torch.arange(40, device="cuda")
+    slot = torch.randperm(64, generator=gen(31), device="cuda")[:40]
+    use = torch.arange(40, device="cuda") % 3 != 0
+    gaps, gap_pos, gap_lat = torch.where(use, slot, -1), torch.where(use, pos, -1), torch.where(use[:, None], lat, math.nan)
+    w_ik = torch.randn(128, D, generator=gen(32), device="cuda").bfloat16()
+    key = torch.randn(40, 128, generator=gen(33), device="cuda").bfloat16()
+
+    def write(lat, pos, slot, key):
+        swa, scale = torch.full((64, D), 9, dtype=torch.uint8, device="cuda"), torch.full((64,), 9.0, device="cuda")
+        kv, kv2 = (torch.full((64, ENTRY), 9, dtype=torch.uint8, device="cuda") for _ in range(2))
+        k_bf, k_f4 = torch.full((64, 128), 9.0, dtype=torch.bfloat16, device="cuda"), c2.indexer_k_fp4_cache(64)
+        bits = []
+        for call in (lambda: c2.swa_quant_write(lat, slot, swa, scale, pos=pos), lambda: c2.kv_quant_write(lat, None, 1, pos, slot, kv),
+                     lambda: c2.kv_quant_write_ik(lat, None, 1, pos, slot, kv2, w_ik, k_bf), lambda: c2.indexer_k_quant(key, slot, k_f4)):
+            call()
+            bits.append(c2.get_device_status())
+        return (swa, scale, kv, kv2, k_bf, k_f4), bits
+
+    want, bits = write(lat[use], pos[use], slot[use], key[use])
+    assert bits == [0] * 4
+    got, bits = write(gap_lat, gap_pos, gaps, key)
+    assert bits == [0] * 4
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    for bad in (-2, 64, -(1 << 62)):
+        got, bits = write(gap_lat, gap_pos, torch.where(pos == 1, bad, gaps), key)
+        assert bits == [2] * 4
+        rest = torch.ones(64, dtype=torch.bool, device="cuda")
+        rest[slot[1]] = False
+        assert all(torch.equal(x[rest], y[rest]) for x, y in zip(got[:5], want[:5]))
+
+
+@pytest.mark.parametrize("m", [1, 2])
+def test_padded_steps_leave_the_status_clear(c2, m):  # noqa: F811
+    """Maps of more places than tokens, and steps longer than the rings: the writers take
+    them as they are, nothing is reported, and the rings hold the last positions."""
+    B, W, S, cap, ring, n = 3, 128, 2, 1200, 140, 900
+    swa, scale = torch.full((B, ring, D), 0x7F, dtype=torch.uint8, device="cuda"), torch.full((B, ring), math.nan, device="cuda")
+    kv = torch.zeros(B, cap, ENTRY, dtype=torch.uint8, device="cuda")
+    texts = [torch.randn(1000, D, generator=gen(34 + b), device="cuda").bfloat16() for b in range(B)]
+    maps, ctx = c2.slot_maps(B, n, m), [0] * B
+    c2.get_device_status()
+    for step, new in enumerate(([500, 7, 300], [1, 0, 12], [11, 1, 1])):
+        c2.slot_map(ints(ctx), ints(new), cap, ring, maps, m=m)
+        lat = torch.full((n, D), math.nan, dtype=torch.bfloat16, device="cuda")
+        lat[:sum(new)] = torch.cat([texts[b][c:c + k] for b, (c, k) in enumerate(zip(ctx, new))])
+        c2.swa_quant_write(lat, maps.swa_slot, swa, scale, pos=maps.pos)
+        e = maps.slot.numel()
+        pair = torch.full((e, m, D), math.nan, dtype=torch.bfloat16, device="cuda")
+        done = [(b, p) for b, (c, k) in enumerate(zip(ctx, new)) for p in range(c, c + k) if p % m == m - 1]
+        pair[:len(done)] = torch.stack([texts[b][p - m + 1:p + 1] for b, p in done])
+        c2.kv_quant_write(pair if m == 2 else pair[:, 0].contiguous(), torch.zeros_like(pair) if m == 2 else None, m,
+                          maps.entry_pos, maps.slot, kv)
+        assert c2.get_device_status() == 0
+        before, ctx = ctx, [c + k for c, k in zip(ctx, new)]
+        for b in range(B):
+            p = torch.arange(max(0, ctx[b] - ring), ctx[b], device="cuda")
+            one, one_scale = torch.zeros(len(p), D, dtype=torch.uint8, device="cuda"), torch.zeros(len(p), device="cuda")
+            c2.swa_quant_write(texts[b][p], torch.arange(len(p), device="cuda"), one, one_scale, pos=p)
+            assert torch.equal(swa[b, p % ring], one) and torch.equal(scale[b, p % ring], one_scale)
+            pe = torch.arange(ctx[b] // m, device="cuda")
+            src = texts[b][:len(pe) * m].view(-1, m, D)
+            whole = torch.zeros(len(pe), ENTRY, dtype=torch.uint8, device="cuda")
+            c2.kv_quant_write(src if m == 2 else src[:, 0].contiguous(), torch.zeros_like(src) if m == 2 else None, m, m * pe + m - 1, pe, whole)
+            assert torch.equal(kv[b, :len(pe)], whole)
+        if step:   # (a ring shorter than its step has lost rows that the first one's tokens see)
+            w = Window.__new__(Window)
+            w.ctx, w.new, w.W, w.S, w.cu, w.ctx_t = before, new, W, 0, maps.cu, ints(before)
+            w.swa, w.scale, w.sink, w.sink_scale = swa, scale, swa[:, :0], scale[:, :0]
+            w.q = queries((n,), 40 + step)
+            w.out = torch.full((n, H, D), 7.0, dtype=torch.bfloat16, device="cuda")
+            w.lse = torch.full((n, H), 7.0, device="cuda")
+            w.call(c2)
+            assert c2.get_device_status() == 0
+            w.check()
