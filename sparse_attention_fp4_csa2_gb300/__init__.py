@@ -442,6 +442,9 @@ def prefix_attn(params, q, prefix_kv, kv, topk_idx, swa, swa_scale, swa_len, out
         _dev(ws, torch.uint8, None, "ws", dev), ws.numel(), _stream(stream)), "csa2_prefix_attn")
 
 
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel   # (mapped over nine tensors: half a microsecond each)
+
+
 class _SlotMaps(NamedTuple):
     cu: torch.Tensor
     tok_seq: torch.Tensor
@@ -460,20 +463,18 @@ class SlotMaps(_SlotMaps):
     [entries], n_vis and swa_len int32 [B]."""
 
     def pointers(self, batch, dev):
-        """The lengths and the address of the C struct of the nine device pointers
-        (checked: the checks' result is kept with the pointers it holds for, those of
-        the two buffers behind ``slot_maps``' outputs or of all nine, and redone when
-        one of them has changed)."""
+        """The lengths and the C struct of the nine device pointers.  What is kept
+        between calls is the struct and the nine addresses and sizes that it was made
+        and checked for: an output that is replaced, resized or set to other memory in
+        place is checked again."""
         d = self.__dict__
-        key = [t.data_ptr() for t in d.get("_buffers", self)], batch, dev
+        key = [*map(_data_ptr, self), *map(_numel, self), batch, dev]
         if d.get("_checked") != key:
-            p = [t.data_ptr() for t in self]
             n, e, i32, i64 = self.pos.numel(), self.slot.numel(), torch.int32, torch.int64
             for t, dtype, size, name in zip(self, (i32, i32, i64, i64, i32, i64, i64, i32, i32),
                                             (batch + 1, n, n, n, batch + 1, e, e, batch, batch), self._fields):
                 _dev(t, dtype, (size,), name, dev)
-            d["_struct"] = (ctypes.c_void_p * 9)(*p)
-            d["_args"] = n, e, ctypes.addressof(d["_struct"])
+            d["_args"] = n, e, (ctypes.c_void_p * 9)(*key[:9])
             d["_checked"] = key
         return d["_args"]
 
@@ -488,9 +489,7 @@ def slot_maps(batch: int, n_tokens: int, m: int = 1, device=None) -> SlotMaps:
     i32 = torch.full((n_tokens + 4 * batch + 2,), -1, dtype=torch.int32, device=device or "cuda")
     pos, swa_slot, entry_pos, slot = i64.split([n_tokens, n_tokens, entries, entries])
     cu, entry_cu, n_vis, swa_len, tok_seq = i32.split([batch + 1, batch + 1, batch, batch, n_tokens])
-    maps = SlotMaps(cu, tok_seq, pos, swa_slot, entry_cu, entry_pos, slot, n_vis, swa_len)
-    maps._buffers = i64, i32
-    return maps
+    return SlotMaps(cu, tok_seq, pos, swa_slot, entry_cu, entry_pos, slot, n_vis, swa_len)
 
 
 def slot_map(ctx_len, new_len, cap, swa_rows, maps, m=1, stream=None):

@@ -288,3 +288,34 @@ def test_padded_steps_leave_the_status_clear(c2, m):  # noqa: F811
             w.call(c2)
             assert c2.get_device_status() == 0
             w.check()
+
+
+def test_slot_map_outputs_changed_in_place(c2):  # noqa: F811
+    """An output that is resized, or set to other memory, between two calls is the one that the
+    next call checks and writes."""
+    ctx, new = ints([5, 0, 9]), ints([3, 4, 1])
+    maps = c2.slot_maps(3, 12)
+    c2.slot_map(ctx, new, 100, 128, maps)
+    assert maps.pos.tolist() == [5, 6, 7, 0, 1, 2, 3, 9] + [-1] * 4
+    other = torch.full((40,), 77, dtype=torch.int64, device="cuda")
+    maps.pos.set_(other[8:20])
+    c2.slot_map(ctx, new + 1, 100, 128, maps)
+    want = [5, 6, 7, 8, 0, 1, 2, 3, 4, 9, 10, -1]
+    assert maps.pos.tolist() == want and other[8:20].tolist() == want
+    assert (other[:8] == 77).all() and (other[20:] == 77).all()
+    maps.slot.set_(torch.full((12,), 55, dtype=torch.int64, device="cuda"))
+    c2.slot_map(ctx, new, 100, 128, maps)
+    assert maps.slot.tolist() == [5, 6, 7, 100, 101, 102, 103, 209] + [-1] * 4
+    for name, change in (("swa_slot", lambda t: t.resize_(11)), ("pos", lambda t: t.resize_(400)),
+                         ("cu", lambda t: t.set_(torch.zeros(5, dtype=torch.int32, device="cuda"))),
+                         ("n_vis", lambda t: setattr(t, "data", torch.zeros(3, dtype=torch.int64, device="cuda"))),
+                         ("slot", lambda t: t.set_(torch.zeros(24, dtype=torch.int64, device="cuda")[::2])),
+                         ("tok_seq", lambda t: setattr(t, "data", torch.zeros(12, dtype=torch.int32)))):
+        maps = c2.slot_maps(3, 12)
+        c2.slot_map(ctx, new, 100, 128, maps)
+        change(getattr(maps, name))
+        with pytest.raises(c2.Csa2Error):
+            c2.slot_map(ctx, new, 100, 128, maps)
+    with pytest.raises(c2.Csa2Error):   # maps of another batch
+        c2.slot_map(ints([1, 2]), ints([1, 1]), 100, 128, c2.slot_maps(3, 12))
+    assert c2.get_device_status() == 0
