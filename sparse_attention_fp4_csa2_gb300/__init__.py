@@ -462,6 +462,10 @@ class SlotMaps(_SlotMaps):
     swa_slot int64 [n], entry_cu int32 [B + 1], entry_pos and slot int64
     [entries], n_vis and swa_len int32 [B]."""
 
+    def __getstate__(self):
+        """Copies and pickles carry the tensors, not the pointers kept for a call."""
+        return None
+
     def pointers(self, batch, dev):
         """The lengths and the C struct of the nine device pointers.  What is kept
         between calls is the struct and the nine addresses and sizes that it was made

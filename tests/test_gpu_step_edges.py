@@ -3,6 +3,7 @@ the header allows: queries that are no numbers, entries and rows far smaller tha
 what they share a softmax with, padded steps, outputs changed in place."""
 import copy
 import math
+import pickle
 
 import pytest
 import torch
@@ -319,3 +320,17 @@ def test_slot_map_outputs_changed_in_place(c2):  # noqa: F811
     with pytest.raises(c2.Csa2Error):   # maps of another batch
         c2.slot_map(ints([1, 2]), ints([1, 1]), 100, 128, c2.slot_maps(3, 12))
     assert c2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, lambda m: pickle.loads(pickle.dumps(m))], ids=["copy", "deepcopy", "pickle"])
+def test_slot_maps_are_copied_after_a_call(c2, how):  # noqa: F811
+    ctx, new = ints([5, 0, 9]), ints([3, 4, 1])
+    maps = c2.slot_maps(3, 12)
+    c2.slot_map(ctx, new, 100, 128, maps)
+    twin = how(maps)
+    assert type(twin) is type(maps) and not twin.__dict__ and all(torch.equal(x, y) for x, y in zip(maps, twin))
+    kept = [t.clone() for t in maps]
+    c2.slot_map(ctx + 1, new, 100, 128, twin)
+    assert twin.pos.tolist() == [6, 7, 8, 1, 2, 3, 4, 10] + [-1] * 4
+    if how is not copy.copy:   # (a copy of the tuple names the same tensors)
+        assert all(torch.equal(x, y) for x, y in zip(maps, kept))
