@@ -334,3 +334,19 @@ def test_slot_maps_are_copied_after_a_call(c2, how):  # noqa: F811
     assert twin.pos.tolist() == [6, 7, 8, 1, 2, 3, 4, 10] + [-1] * 4
     if how is not copy.copy:   # (a copy of the tuple names the same tensors)
         assert all(torch.equal(x, y) for x, y in zip(maps, kept))
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+@pytest.mark.parametrize("new", [[30, 4], [100, 90], [170, 60]])
+def test_a_short_ring_leaves_the_other_sequences_right(c2, kernel, new):  # noqa: F811
+    """A sequence whose ring has lost rows, or whose length is negative, is reported by every
+    kernel, and the one beside it comes out as it should."""
+    w = Window([500, 40], new, 128, 4, seed=43)
+    w.swa, w.scale = w.swa[:, :130].contiguous(), w.scale[:, :130].contiguous()
+    ref, ref_lse, n = w.reference()
+    for first in (500, -3):
+        w.ctx_t = ints([first, 40])
+        w.out.fill_(7.0)
+        w.call(c2, kernel)
+        assert c2.get_device_status() == 2
+        check_out(w.out[new[0]:], w.lse[new[0]:], ref[new[0]:], ref_lse[new[0]:])
