@@ -457,7 +457,8 @@ typedef struct {
  *   n_tokens, n_entries: lengths of the outputs.  Places past the last token or
  *             entry get -1 (which the writers skip); tokens and entries past the
  *             outputs' lengths are dropped.
- *   maps      the outputs (out; the struct itself is read by the call)
+ *   maps      the outputs (out; the struct itself is read by the call), none of
+ *             which may share memory with ctx_len or new_len
  * A negative length (taken as 0), dropped tokens or entries, and a sequence past
  * its cap set CSA2_DEV_ERR_NVIS.  batch above 8192 and lengths of the outputs past
  * 2^31 - 1 are CSA2_ERR_UNSUPPORTED.

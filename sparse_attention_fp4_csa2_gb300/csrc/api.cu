@@ -37,6 +37,10 @@ namespace {
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool aligned8(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 7u) == 0; }
+bool overlap(const void *a, int64_t a_bytes, const void *b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
 
 int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
@@ -797,6 +801,14 @@ extern "C" csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, cons
   if (batch > kMaxMapBatch || n_tokens > INT32_MAX || n_entries > INT32_MAX || cap > kMaxCacheRows / batch ||
       swa_rows > kMaxCacheRows / batch)
     return CSA2_ERR_UNSUPPORTED;
+  // (the lengths are read while outputs are written)
+  const struct { const void *p; int64_t bytes; } outs[] = {
+      {o.cu, 4 * (int64_t)(batch + 1)}, {o.entry_cu, 4 * (int64_t)(batch + 1)}, {o.n_vis, 4 * (int64_t)batch},
+      {o.swa_len, 4 * (int64_t)batch},  {o.tok_seq, 4 * n_tokens},              {o.pos, 8 * n_tokens},
+      {o.swa_slot, 8 * n_tokens},       {o.entry_pos, 8 * n_entries},           {o.slot, 8 * n_entries}};
+  for (const auto &x : outs)
+    if (overlap(x.p, x.bytes, ctx_len, 4 * (int64_t)batch) || overlap(x.p, x.bytes, new_len, 4 * (int64_t)batch))
+      return CSA2_ERR_INVALID_ARG;
   if (launch_slot_map(ctx_len, new_len, batch, m, cap, swa_rows, n_tokens, n_entries, o, num_sms(),
                       reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
     return CSA2_ERR_CUDA;

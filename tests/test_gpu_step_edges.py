@@ -350,3 +350,17 @@ def test_a_short_ring_leaves_the_other_sequences_right(c2, kernel, new):  # noqa
         w.call(c2, kernel)
         assert c2.get_device_status() == 2
         check_out(w.out[new[0]:], w.lse[new[0]:], ref[new[0]:], ref_lse[new[0]:])
+
+
+def test_slot_map_lengths_in_place_are_refused(c2):  # noqa: F811
+    """The counts that a step gives do not take the place of its lengths; next to them they may lie."""
+    maps = c2.slot_maps(3, 12)
+    with pytest.raises(c2.Csa2Error):
+        c2.slot_map(maps.n_vis, ints([1, 2, 3]), 100, 128, maps)
+    both = torch.zeros(9, dtype=torch.int32, device="cuda")
+    ctx, new = both[:3], both[6:]
+    ctx += 5
+    new += 2
+    maps = maps._replace(n_vis=both[3:6])
+    c2.slot_map(ctx, new, 100, 128, maps)
+    assert both.tolist() == [5] * 3 + [7] * 3 + [2] * 3 and c2.get_device_status() == 0
