@@ -364,3 +364,43 @@ def test_slot_map_lengths_in_place_are_refused(c2):  # noqa: F811
     maps = maps._replace(n_vis=both[3:6])
     c2.slot_map(ctx, new, 100, 128, maps)
     assert both.tolist() == [5] * 3 + [7] * 3 + [2] * 3 and c2.get_device_status() == 0
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+def test_rows_nobody_names_hold_anything(c2, kernel):  # noqa: F811
+    """Rows of a tree, a ring and sinks that no mask or window reaches: NaN codes, scales of
+    NaN, infinity and below zero."""
+    odd = torch.tensor([math.nan, math.inf, -math.inf, -1.0], device="cuda")
+    for B, T, K in ((2, 9, 0), (40, 8, 0), (40, 8, 30), (1, 5, 300)):
+        t = Tree(c2, B, T, K, 16, [3 * i for i in range(B)], cap=310 if K else 0, seed=45, slack=4)
+        for b in range(B):
+            for i in range(T):
+                t.mask[b][i] &= ~(1 << (T - 1) | 1 << 2)
+        t.put_mask()
+        t.tree[:, [2, T - 1]] = 0x7F
+        t.tree_scale[:, 2], t.tree_scale[:, T - 1] = odd[torch.arange(B, device="cuda") % 4], odd[torch.arange(B, device="cuda") % 3]
+        for b, c in enumerate(t.ctx):
+            far = [p % 20 for p in range(c, max(c, 20))] if c < 20 else [p % 20 for p in range(c - 20, c - 16)]
+            t.swa[b, far], t.scale[b, far] = 0xFF, odd[b % 4]
+        t.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        t.check()
+
+
+@pytest.mark.parametrize("kernel", [0, 1, 2])
+def test_scales_at_the_ends_of_their_range(c2, kernel):  # noqa: F811
+    """Rows whose scales are 2^50, 2^-64, less, and 0, in one softmax (queries of zeros:
+    equal weights; then ones under which one row takes all)."""
+    for new in (1, 160):
+        w = Window([200, 100], [new, new], 128, 4, seed=46)
+        for i, s in enumerate((2.0 ** 50, 2.0 ** 49, 1.0, 2.0 ** -64, 2.0 ** -70, 0.0)):
+            w.scale[:, i::6] = torch.where(torch.isnan(w.scale[:, i::6]), math.nan, s)
+        w.q.zero_()
+        w.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        w.check()
+        w.scale[w.scale <= 1.0] = 0.0
+        w.q = torch.full_like(w.q, 2.0 ** -24)   # (logits far apart: one key takes all)
+        w.call(c2, kernel)
+        assert c2.get_device_status() == 0
+        w.check()
