@@ -241,6 +241,21 @@ struct AttnArgs {
   StepRows step;              // step.out: this form instead (W = win + extras)
 };
 
+// The last of places lo .. lo + n - 1 of ascending sums whose sum is at most x (lo's is).
+template <typename T>
+__device__ __forceinline__ int last_not_above(const int32_t *sums, int lo, int n, T x) {
+  while (n > 1) {
+    const int half = n >> 1;
+    if (sums[lo + half] <= x) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return lo;
+}
+
 // The sequence of packed token i: the last b with cu[b] <= i < cu[batch] (false
 // when there is none).  Called by whole warps: 32 probes at a time.
 __device__ __forceinline__ bool find_sequence(const int32_t *cu, int32_t batch, int64_t i, int &b) {

@@ -62,21 +62,6 @@ __device__ __forceinline__ void scan_pair(int64_t &a, int64_t &b, int64_t (*part
   b += bb - b0;
 }
 
-// The last b with cu[b] <= i (cu[0] = 0, i >= 0).
-__device__ __forceinline__ int sequence_of(const int32_t *cu, int batch, int32_t i) {
-  int lo = 0, n = batch;
-  while (n > 1) {
-    const int half = n >> 1;
-    if (cu[lo + half] <= i) {
-      lo += half;
-      n -= half;
-    } else {
-      n = half;
-    }
-  }
-  return lo;
-}
-
 __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a) {
   extern __shared__ int32_t sums[];   // [batch + 1] tokens, [batch + 1] entries, [batch] tokens before the step
   __shared__ int64_t part[kMapThreads / 32][2];
@@ -132,7 +117,7 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const SlotArgs a)
     int32_t seq = -1;
     int64_t pos = -1, slot = -1;
     if (at < cu[a.batch]) {
-      seq = sequence_of(cu, a.batch, (int32_t)at);
+      seq = last_not_above(cu, 0, a.batch, (int32_t)at);
       const int32_t r = (int32_t)at - cu[seq];
       if (entry) {
         const int64_t e1 = (int64_t)(ctx[seq] >> (a.m - 1)) + r;

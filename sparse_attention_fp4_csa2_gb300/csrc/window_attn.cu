@@ -153,18 +153,7 @@ struct Walk {
       if (tok == seq_end) {
         // the next one with tokens: the neighbour, or by binary search (a run of empty ones)
         ++seq;
-        if (seq + 1 < a.s.batch && a.s.cu[seq + 1] <= tok) {
-          int n = a.s.batch - seq;   // the answer is one of seq .. seq + n - 1
-          while (n > 1) {
-            const int half = n >> 1;
-            if (a.s.cu[seq + half] <= tok) {
-              seq += half;
-              n -= half;
-            } else {
-              n = half;
-            }
-          }
-        }
+        if (seq + 1 < a.s.batch && a.s.cu[seq + 1] <= tok) seq = last_not_above(a.s.cu, seq, a.s.batch - seq, tok);
         enter(a);
       }
       t.n = seq_end - tok > 1 ? 2 : 1;
@@ -771,7 +760,7 @@ cudaError_t launch_window_attn(const void *q, const uint8_t *swa, const float *s
   int64_t grid;
   if (s.cu) {
     a.parts = 0;
-    grid = tokens < num_sms ? tokens : num_sms;
+    grid = num_sms;   // (there are more tokens: csrc/api.cu)
   } else {
     // as many CTAs for each sequence as fit, at least a pair of tokens each
     const int pairs = (s.extras + 1) / 2, fit = num_sms / s.batch;
