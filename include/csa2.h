@@ -245,7 +245,8 @@ csa2_status csa2_hier_pool_select(const float *block_scores, const int32_t *n_vi
  *   kv        uint8 [batch][cap][288], 16-byte aligned
  *   topk_idx  int32 [batch][index_topk], entries in [-1, cap)
  *   swa       uint8 E4M3 [batch][sliding_window][512], 16-byte aligned
- *   swa_scale fp32 [batch][sliding_window]
+ *   swa_scale fp32 [batch][sliding_window] (a weight goes to the products times its
+ *             row's scale, as fp16: below scales of about 2^-14 bits are lost)
  *   swa_len   int32 [batch], 0..sliding_window
  *   out       fp32 [batch][64][512] (out); lse fp32 [batch][64] or NULL (out)
  */

@@ -848,7 +848,11 @@ csa2_status run_step(const csa2_params *p, int64_t tokens, const void *q, const 
   // one sequence 18.2 us against 14.4 in a CTA each, 200 18.6 against 22.1, 1,200 38
   // against 72; one each of 608 sequences 61 against 43, two each of 152 21.4 against
   // 24.1.  Trees: 30 x 5 18.0 against 13.0, 36 x 5 18.2 against 18.8, 128 x 5 30 against
-  // 40; 200 x 3 42 against 34, 300 x 2 35 and 35).
+  // 40; 200 x 3 42 against 34, 300 x 2 35 and 35.  Narrow windows gain later: of 16 rows
+  // 156 tokens 13.3 against 12.5, 400 19.4 against 20.1, 1,200 33 against 45, 16,384 337
+  // against 537; trees of 16 rows 36 x 5 12.9 against 12.6, 3 x 64 14.7 against 12.8, 20
+  // x 40 26 against 33.  Wider windows have no tiles: 8,192 tokens of 142 rows 459, of
+  // 256 647, of 512 1,066).
   // Else a CTA for each token.
   const int sms = num_sms();
   const int64_t keys = (int64_t)a.K + (s.cu ? s.win + s.extras : s.win > s.extras ? s.win : s.extras);

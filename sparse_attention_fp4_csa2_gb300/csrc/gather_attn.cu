@@ -26,10 +26,10 @@
 //            from the same slot; its end frees the slot;
 //   rows out O^T through shared memory, as bf16, while the next
 //            token's first steps are converted and multiplied.
-// Measured: 2,048 tokens of 512 + 128 keys 302 us, 41,500 wavefronts and some 42,000
-// clocks a token, ten steps of 3,300 and 8,000 between tokens (Q's reload and
-// conversion, beside them the rows out); 256 tokens 49.6 us, two rounds; 93 tokens of
-// up to 168 keys 11.1.  Both products issued by one thread, a tile of 128 keys and
+// Measured: 2,048 tokens of 512 + 128 keys 310 us, 41,600 wavefronts and some 43,000
+// clocks a token, ten steps of 3,400 and 8,000 between tokens (Q's reload and
+// conversion, beside them the rows out); 256 tokens 52 us, two rounds; 93 tokens of
+// up to 168 keys 11.0 in a graph, 11.8 to 13.2 called one by one.  Both products issued by one thread, a tile of 128 keys and
 // softmax on the rows' warps, as in the sparse readout: 637 us for the 2,048.
 // Keys that the token does not see take no place: the list (whose -1 are masked),
 // the window's visible rows, then the named extra rows.

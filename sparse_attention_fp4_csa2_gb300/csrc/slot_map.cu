@@ -13,8 +13,8 @@
 // stay in L2), keeps both prefix sums and the lengths before the step in shared
 // memory and takes every gridDim-th stretch of the tokens and entries, finding a
 // token's sequence by binary search there.  Measured in graphs: 32 sequences of one
-// token 2.9 us, 999 of five 4.7, 196,000 tokens and 98,000 entries of 64 sequences
-// 4.7 (1.2 TB/s); a call from Python takes 5.6.
+// token 2.8 us, 999 of five 4.9, 196,000 tokens and 98,000 entries of 64 sequences
+// 4.8 (1.1 TB/s); a call from Python takes 6.6.
 #include "kernels.cuh"
 
 namespace csa2 {

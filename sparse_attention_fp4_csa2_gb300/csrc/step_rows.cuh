@@ -18,7 +18,7 @@ constexpr float kTinyScale = 5.421010862427522e-20f;
 //   an 8-bit row's f is its scale x 2^8 (its codes reach 448 = 1.75 x 2^8);
 // so that keys of one size have nearly the same f.  (An entry's size is that of its
 // scales: a block of zero codes under a large one counts too.  The writers leave none.)
-// What it costs: 32 x 64 drafted tokens 312 us, with f = 1 for entries and a row's scale
+// What it costs: 32 x 64 drafted tokens 310 us, with f = 1 for entries and a row's scale
 // 303; but entries of zeros beside rows of 1e-6 then came out as nothing.
 //   a key of nothing but zero codes has f = 2^-56: it never sets m beside others, and up to
 //   row scales of 2^50 beside it 2^(logit - m) f is an fp32 number that gives back
