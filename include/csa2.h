@@ -496,7 +496,7 @@ csa2_status csa2_slot_map(int32_t batch, const int32_t *ctx_len, const int32_t *
  *             [n_tokens][64] or NULL (out).  A token that sees nothing gives out =
  *             0 and lse = -inf; rows from cu[batch] on are left as they were.
  * Logits, row sums and log-sum-exps are fp32.  A weight goes to the second product as
- * fp16, off by at most 2^-11 of itself or by 2^-25 of the largest weight x size of a
+ * fp16, off by at most 2^-11 of itself or by 2^-24 of the largest weight x size of a
  * key, its size being its scale x 448 (an entry's: its largest block scale x 6); with
  * a token's keys split over a cluster the parts' sums are fp16 once more.  Where tokens
  * share their rows in tiles the weight has 16 bits.
