@@ -24,7 +24,7 @@
 //                  pieces of 128, 64, 128, 64, 128 channels through two buffers;
 //   rows out       bf16 through shared memory and tensor copies.
 // What bounds it: HBM in a long run (2 x 8,192 tokens, window 128: 356 us in a graph,
-// 6.1 TB/s, 0.91 of a plain copy's rate, and 380 to 389 called one by one; a tile takes 12,000 clocks, of which HBM needs
+// 6.1 TB/s, 0.91 of a plain copy's rate, and 377 to 389 called one by one; a tile takes 12,000 clocks, of which HBM needs
 // 11,650), the latency of the fill and of a tile's chain in a short one (9 prompts
 // of 3,139 tokens, 22 a CTA: 89 us, 4.6 TB/s; 64 trees of five tokens 23 us): rows 10,000
 // clocks, S 3,000 to 5,000 (Q's arrival), softmax 3,500, the second product and the
